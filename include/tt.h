@@ -113,6 +113,38 @@ TT_API int tt_tree_schedules(const void* ws, int64_t N, int32_t* send, int32_t* 
                              int32_t* fwd_cnt, int32_t* fwd_order, int32_t* bwd_cnt, int32_t* bwd_order,
                              tt_stream_t stream);
 
+/* ------------------------------------------------------- rotary positions
+ * The attention calls take Q and K after the rotary embedding; this call
+ * applies it (exact per-branch results need each token's depth along its
+ * path as position: tok_pos of tt_tree_build). One position axis for text,
+ * several (time, height, width) for tokens of images and video:
+ *   θ_i = pos[axis_host[i]][t]·freq_host[i],   i < rot/2,
+ *   (x1, x2) -> (x1·cos θ_i − x2·sin θ_i, x2·cos θ_i + x1·sin θ_i)
+ * over the pairs (i, i + rot/2) of every head, or (2i, 2i + 1) with adjacent
+ * != 0; dimensions from rot on pass through. inverse != 0 turns by −θ: the
+ * inverse, and the backward pass (dQ, dK of the rotated tensors in, those of
+ * the unrotated ones out).
+ *   q: [N][Hq][d] with tokens q_ld elements apart (>= Hq·d; heads and
+ *      dimensions contiguous), q_out likewise with q_out_ld; k, k_out with
+ *      Hkv. All of type dtype (TT_DT_*). A tensor with 0 heads may be NULL.
+ *      q_out may be q (with q_out_ld = q_ld), k_out may be k; other overlaps
+ *      are not supported. Elements between the rows are neither read nor
+ *      written.
+ *   pos: device int32 [axes][N] with axes pos_ld entries apart (>= N, or 0:
+ *      every axis reads the same positions); any value, negative ones too.
+ *   axis_host: host uint8 [rot/2], each < axes; freq_host: host double
+ *      [rot/2], finite. Both are read before the call returns. Angles are
+ *      exact to 2^-23 of a turn at every int32 position.
+ * Limits (TT_ERR_UNSUPPORTED): d and rot even, d <= 1024, rot <= 256, at most
+ * 4 axes and 1024 heads each. N = 0 does nothing. 16-byte accesses when all
+ * bases and strides are 16-byte multiples and rot and d multiples of 32 bytes;
+ * element accesses otherwise. */
+enum { TT_DT_BF16 = 0, TT_DT_F16 = 1, TT_DT_F32 = 2 };
+TT_API int tt_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, const void* k, void* k_out, int64_t k_ld,
+                   int64_t k_out_ld, int dtype, int64_t N, int Hq, int Hkv, int d, int rot, const int32_t* pos,
+                   int64_t pos_ld, int axes, const uint8_t* axis_host, const double* freq_host, int adjacent,
+                   int inverse, tt_stream_t stream);
+
 /* ---------------------------------------------------------- tree attention
  * Forward ("Tree Training", Abstract: attention adapted so each token's
  * result equals independent per-branch causal attention):
@@ -394,6 +426,42 @@ TT_API int tt_weighted_logprob(const tt_bf16* logits, int64_t N, int64_t V, int6
                                const float* weights, float g, float* logp, double* loss, tt_bf16* dlogits,
                                int32_t* err, tt_stream_t stream);
 
+/* ------------------------- log-prob, entropy and top alternatives per token
+ * The per-token quantities of a policy objective, from logits z [N][ld]
+ * (ld >= V) of type dtype (TT_DT_*), any element alignment of the rows:
+ *   lse_t = log Σ_v exp(z_tv);   logp_t = z_{t,y_t} − lse_t;
+ *   entropy_t = −Σ_v p_tv·log p_tv;
+ *   top_ids[t][j], top_logp[t][j]: the k largest logits of the row in
+ *   descending order, ties to the lower index, and their log-probs.
+ * targets int32 [N], or NULL (logp is then not written and may be NULL);
+ * logp, entropy, lse fp32 [N]; top_ids int32, top_logp fp32 [N][k], 0 <= k <=
+ * min(V, 32) (larger k <= V: TT_ERR_UNSUPPORTED; k = 0: both may be NULL).
+ * A target outside [0, V) sets `err` = TT_ERR_INVALID_ARG and that row's logp
+ * to NaN. A logit of −inf is a masked token: probability 0, no part in the
+ * entropy. A row with nothing but −inf has no distribution: lse, logp,
+ * top_logp = −inf, entropy = 0, top_ids = 0 .. k−1. A row with a NaN or +inf
+ * gives NaN in all floating outputs; with a NaN its top_ids are some ids in
+ * [0, V). N = 0 does nothing. No workspace; repeated calls agree bitwise. */
+TT_API int tt_token_logprob(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* targets,
+                            int k, float* logp, float* entropy, float* lse, int32_t* top_ids, float* top_logp,
+                            int32_t* err, tt_stream_t stream);
+/* Backward: the gradient with respect to the logits, given the gradients of
+ * an objective with respect to the outputs (each fp32, NULL = zero): dlogp[N]
+ * (with targets), dentropy[N] (with the forward's entropy), dlse[N], and
+ * dtop[N][k] of the log-probs of the tokens top_ids[N][k] (any ids: the
+ * forward's alternatives, or another model's; a repeated id adds up):
+ *   dz_tv = p_tv·(dlse − dlogp − Σ_j dtop_j − dentropy·(log p_tv + entropy))
+ *           + dlogp·[v == y_t] + Σ_j dtop_j·[v == top_ids_j].
+ * lse: the forward's. dlogits: type and ld of logits; it may be logits itself
+ * (overwritten), other overlaps are not supported; columns from V on are left
+ * as they are. 0 <= k <= 32. An id outside [0, V) sets `err` =
+ * TT_ERR_INVALID_ARG and its one-hot term is omitted. A masked logit gets 0
+ * (plus its one-hot terms), a row with nothing but −inf (lse = −inf) zeros. */
+TT_API int tt_token_logprob_bwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const float* lse,
+                                const float* entropy, const int32_t* targets, const float* dlogp,
+                                const float* dentropy, const float* dlse, const int32_t* top_ids, const float* dtop,
+                                int k, void* dlogits, int32_t* err, tt_stream_t stream);
+
 /* ---------------------------------------------------------------- trie build (host)
  * The step before tt_tree_build: the prefix tree of a task's rollouts from
  * their token sequences ("Tree Training", Abstract: a task's tokens form a
@@ -454,6 +522,33 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
                                  const int32_t* targets, const float* weights, float g, const float* lse,
                                  tt_bf16* d_hidden, float* d_w_vocab, void* ws, size_t ws_bytes, int32_t* err,
                                  tt_stream_t stream);
+
+/* The LM head fused with the per-token log-prob and entropy (the quantities of
+ * tt_token_logprob without the top alternatives; logits never stored):
+ *   z = hidden·w_vocabᵀ;  lse, logp, entropy as there, fp32 [N] each, all written.
+ * Arguments, limits and errors as tt_lmhead_logprob (targets required; hidden
+ * and w_vocab finite). ws: tt_lmhead_token_logprob_workspace_bytes(N, V) bytes
+ * (12·N·ceil(V/256) + 4·N and padding), 16-byte aligned. */
+TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V);
+TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
+                                   const int32_t* targets, float* logp, float* entropy, float* lse, void* ws,
+                                   size_t ws_bytes, int32_t* err, tt_stream_t stream);
+/* Its backward, given the gradients dlogp, dentropy, dlse (fp32 [N], NULL =
+ * zero) of an objective with respect to the outputs:
+ *   dz_tv = p_tv·(dlse − dlogp − dentropy·(log p_tv + entropy)) + dlogp·[v == y_t],
+ *   d_hidden = dz·W ([N][Hd] bf16), d_w_vocab = dzᵀ·H ([V][Hd] of type
+ *   dw_dtype: TT_DT_F32 or TT_DT_BF16), both written.
+ * lse, entropy: the forward's (entropy may be NULL without dentropy). dz is
+ * rounded to bf16 and kept in ws (tt_lmhead_token_logprob_bwd_workspace_bytes
+ * bytes, 16-byte aligned), as in tt_lmhead_logprob_bwd. A target outside
+ * [0, V) sets `err` = TT_ERR_INVALID_ARG and its row's dz omits the one-hot
+ * term. */
+TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V);
+TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
+                                       const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* dlogp, const float* dentropy, const float* dlse,
+                                       tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws, size_t ws_bytes,
+                                       int32_t* err, tt_stream_t stream);
 
 /* ---------------------------------------------------------------- launch timing
  * A measurement aid, off by default, and the one state the library keeps

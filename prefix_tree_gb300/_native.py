@@ -7,7 +7,9 @@ missing libtt.so raises immediately.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -74,10 +76,18 @@ _SIGS = {
     "tt_dta_plan_launch": (_int, [_vp, _vp]),
     "tt_dta_plan_destroy": (_int, [_vp]),
     "tt_weighted_logprob": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "tt_rope": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _int, _i64, _int, _int, _int, _int, _vp, _i64, _int,
+                       _vp, _vp, _int, _int, _vp]),
+    "tt_token_logprob": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "tt_token_logprob_bwd": (_int, [_vp, _int, _i64, _i64, _i64] + [_vp] * 8 + [_int, _vp, _vp, _vp]),
     "tt_lmhead_logprob_workspace_bytes": (_sz, [_i64, _i64]),
     "tt_lmhead_logprob": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tt_lmhead_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "tt_lmhead_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "tt_lmhead_token_logprob_workspace_bytes": (_sz, [_i64, _i64]),
+    "tt_lmhead_token_logprob": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "tt_lmhead_token_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "tt_lmhead_token_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int] + [_vp] * 8 + [_int, _vp, _sz, _vp, _vp]),
     "tt_status_string": (ctypes.c_char_p, [_int]),
     "tt_version": (_int, []),
     "tt_trie_build": (_int, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),
@@ -207,6 +217,101 @@ def tree_schedules(tree: Tree) -> dict:
     _check(lib().tt_tree_schedules(_p(tree.ws), tree.N, *(_p(out[n]) for n in names), _stream(dev)),
            "tt_tree_schedules")
     return out
+
+
+# --------------------------------------------------------------------------- rotary positions
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # TT_DT_*
+
+
+def _on(t, *others):
+    """Context that makes t's device current; the other tensors must be on it."""
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+    return torch.cuda.device(t.device) if t.device.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_tables(rot, sections, interleaved, base, inv_freq):
+    """Host tables of tt_rope: the axis and the frequency of each pair."""
+    half = rot // 2
+    if any(n < 0 for n in sections) or sum(sections) != half:
+        raise ValueError(f"sections must be non-negative and add up to rot_dim / 2 = {half}")
+    if interleaved:
+        axis = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    freq = [base ** (-i / half) for i in range(half)] if inv_freq is None else list(inv_freq)
+    if len(freq) != half:
+        raise ValueError(f"inv_freq must hold rot_dim / 2 = {half} frequencies")
+    return (ctypes.c_uint8 * half)(*axis), (ctypes.c_double * half)(*freq)
+
+
+def _rope_rows(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 3:
+        raise TypeError(f"{name} must be a 3-D bf16, fp16 or fp32 CUDA tensor [N, heads, d]")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjacent=False, base=10000.0, inv_freq=None,
+         out=None, inverse=False):
+    """Rotary positions of q [N,Hq,d] and k [N,Hkv,d] (tt_rope; k may be None): returns (q_out, k_out).
+
+    `positions`: int32 [N] (one axis, e.g. Tree.tok_pos) or [axes, N]. The first `rot_dim` (default d) dimensions turn,
+    in the pairs (i, i + rot_dim/2) or, `adjacent`, (2i, 2i + 1), by positions times the frequencies base^(-2i/rot_dim)
+    or `inv_freq` (rot_dim/2 numbers). `sections`: how many frequencies each axis takes, one after the other or,
+    `interleaved`, the axes in turn while their section lasts. q and k may be views of one buffer (tokens any stride
+    apart); `out` = (q_out, k_out) may be (q, k). `inverse` turns back."""
+    q_ld = _rope_rows(q, "q")
+    N, hq, d = q.shape
+    hkv, k_ld = 0, 0
+    if k is not None:
+        k_ld = _rope_rows(k, "k")
+        hkv = k.shape[1]
+        if k.dtype != q.dtype or k.shape[0] != N or k.shape[2] != d:
+            raise ValueError("q and k must share type, tokens and head dimension")
+    if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32:
+        raise TypeError("positions must be an int32 CUDA tensor")
+    pos = positions[None] if positions.dim() == 1 else positions
+    if pos.dim() != 2 or pos.shape[1] != N or (N > 1 and pos.stride(1) != 1):
+        raise ValueError("positions must be [N] or [axes, N] with contiguous tokens")
+    axes = pos.shape[0]
+    rot = d if rot_dim is None else int(rot_dim)
+    if rot < 2 or rot > d or rot % 2:
+        raise ValueError("rot_dim must be even and in 2 .. d")
+    if sections is None:
+        if axes != 1:
+            raise ValueError("several axes need sections")
+        sections = (rot // 2,)
+    elif len(sections) != axes:
+        raise ValueError("positions and sections must agree on the number of axes")
+    axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base),
+                              None if inv_freq is None else tuple(float(f) for f in inv_freq))
+    if out is None:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        qo_ld, ko_ld = hq * d, hkv * d
+    else:
+        qo, ko = out
+        if qo.shape != q.shape or qo.dtype != q.dtype or (ko is None) != (k is None) or \
+                (k is not None and (ko.shape != k.shape or ko.dtype != k.dtype)):
+            raise ValueError("out must have the shapes and type of q and k")
+        qo_ld = _rope_rows(qo, "q_out")
+        ko_ld = 0 if ko is None else _rope_rows(ko, "k_out")
+    with _on(q, k, pos, qo, ko):
+        rc = lib().tt_rope(_p(q), _p(qo), q_ld, qo_ld, _p(k), _p(ko), k_ld, ko_ld, _DTYPES[q.dtype], N, hq, hkv, d, rot,
+                           _p(pos), pos.stride(0), axes, axis, freq, int(bool(adjacent)), int(bool(inverse)),
+                           _stream(q.device))
+    _check(rc, "tt_rope")
+    return qo, ko
+
+
+def rope_bwd(dq, dk, positions, **how):
+    """Gradients of the unrotated q and k from those of rope's outputs (the inverse rotation; arguments as rope's)."""
+    return rope(dq, dk, positions, inverse=True, **how)
 
 
 # --------------------------------------------------------------------------- attention
@@ -469,6 +574,78 @@ def weighted_logprob(logits, targets, weights=None, g=1.0, want_dlogits=True, ou
     return logp, loss, dl
 
 
+# --------------------------------------------------------------------------- log-prob, entropy, top alternatives
+def _logit_rows(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D bf16, fp16 or fp32 CUDA tensor")
+    N, V = t.shape
+    ld = t.stride(0) if N > 1 else V
+    if (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{name} rows must be contiguous (stride(1) == 1, stride(0) >= V)")
+    return N, V, ld
+
+
+def _per_row(t, dtype, name, shape):
+    if t is not None:
+        _need(t, dtype, name, len(shape))
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}")
+
+
+def token_logprob(logits, targets=None, top_k=0, out=None, err=None):
+    """Per row of logits [N,V] (bf16, fp16 or fp32; rows may be padded): (logp, entropy, lse, top_ids, top_logp) of
+    tt_token_logprob: fp32 [N] each, and int32 / fp32 [N, top_k] of the top alternatives. logp is None without
+    targets, top_ids and top_logp are None with top_k = 0."""
+    N, V, ld = _logit_rows(logits, "logits")
+    _per_row(targets, torch.int32, "targets", (N,))
+    dev, k = logits.device, int(top_k)
+    if out is None:
+        f = torch.empty(3, N, dtype=torch.float32, device=dev)
+        logp, entropy, lse = (f[0] if targets is not None else None), f[1], f[2]
+        ids = torch.empty(N, k, dtype=torch.int32, device=dev) if k > 0 else None
+        top = torch.empty(N, k, dtype=torch.float32, device=dev) if k > 0 else None
+    else:
+        logp, entropy, lse, ids, top = out
+        for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
+            _per_row(t, torch.float32, n, (N,))
+        _per_row(ids, torch.int32, "top_ids", (N, k))
+        _per_row(top, torch.float32, "top_logp", (N, k))
+    err = new_err(dev) if err is None else err
+    with _on(logits, targets, logp, entropy, lse, ids, top, err):
+        rc = lib().tt_token_logprob(_p(logits), _DTYPES[logits.dtype], N, V, ld, _p(targets), k, _p(logp), _p(entropy),
+                                    _p(lse), _p(ids), _p(top), _p(err), _stream(dev))
+    _check(rc, "tt_token_logprob")
+    return logp, entropy, lse, ids, top
+
+
+def token_logprob_bwd(logits, lse, entropy=None, targets=None, dlogp=None, dentropy=None, dlse=None, top_ids=None,
+                      dtop=None, out=None, err=None):
+    """dlogits (type and row stride of logits) of an objective whose gradients with respect to token_logprob's outputs
+    are dlogp, dentropy, dlse [N] and dtop [N, k] (log-probs of top_ids), each optional (tt_token_logprob_bwd). `out`
+    may be logits itself, which is then overwritten."""
+    N, V, ld = _logit_rows(logits, "logits")
+    _per_row(targets, torch.int32, "targets", (N,))
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
+        _per_row(t, torch.float32, n, (N,))
+    if (top_ids is None) != (dtop is None):
+        raise ValueError("top_ids and dtop go together")
+    k = 0 if dtop is None else dtop.shape[-1]
+    _per_row(top_ids, torch.int32, "top_ids", (N, k))
+    _per_row(dtop, torch.float32, "dtop", (N, k))
+    dev = logits.device
+    if out is None:
+        out = torch.empty(N, ld, dtype=logits.dtype, device=dev)[:, :V]
+    elif out.dtype != logits.dtype or out.shape != logits.shape or (N > 1 and out.stride() != logits.stride()):
+        raise ValueError("out must have the type, shape and strides of logits")
+    err = new_err(dev) if err is None else err
+    with _on(logits, lse, entropy, targets, dlogp, dentropy, dlse, top_ids, dtop, out, err):
+        rc = lib().tt_token_logprob_bwd(_p(logits), _DTYPES[logits.dtype], N, V, ld, _p(lse), _p(entropy), _p(targets),
+                                        _p(dlogp), _p(dentropy), _p(dlse), _p(top_ids), _p(dtop), k, _p(out), _p(err),
+                                        _stream(dev))
+    _check(rc, "tt_token_logprob_bwd")
+    return out
+
+
 def lmhead_logprob(hidden, w_vocab, targets, weights=None, out=None, ws=None, err=None):
     """LM head fused with the weighted log-prob (tt_lmhead_logprob): logits z = hidden·w_vocabᵀ are never stored.
     hidden [N,Hd] bf16, w_vocab [V,Hd] bf16 -> (logp fp32 [N], lse fp32 [N], loss fp64 device scalar)."""
@@ -519,6 +696,68 @@ def lmhead_logprob_bwd(hidden, w_vocab, targets, lse, weights=None, g=1.0, out=N
     rc = lib().tt_lmhead_logprob_bwd(_p(hidden), _p(w_vocab), N, V, Hd, _p(targets), _p(weights), g, _p(lse), _p(dh),
                                      _p(dw), _p(ws), ws.numel(), _p(err), _stream(dev))
     _check(rc, "tt_lmhead_logprob_bwd")
+    return dh, dw
+
+
+def _lmhead_args(hidden, w_vocab, targets):
+    _need(hidden, torch.bfloat16, "hidden", 2)
+    _need(w_vocab, torch.bfloat16, "w_vocab", 2)
+    N, Hd = hidden.shape
+    if w_vocab.shape[1] != Hd:
+        raise ValueError("hidden and w_vocab must share Hd")
+    _need(targets, torch.int32, "targets", 1)
+    _per_row(targets, torch.int32, "targets", (N,))
+    return N, w_vocab.shape[0], Hd
+
+
+def lmhead_token_logprob(hidden, w_vocab, targets, out=None, ws=None, err=None):
+    """LM head fused with the per-token log-prob and entropy (tt_lmhead_token_logprob): logits z = hidden·w_vocabᵀ are
+    never stored. hidden [N,Hd] bf16, w_vocab [V,Hd] bf16 -> (logp, entropy, lse), fp32 [N] each."""
+    N, V, Hd = _lmhead_args(hidden, w_vocab, targets)
+    dev = hidden.device
+    if out is None:
+        out = tuple(torch.empty(3, N, dtype=torch.float32, device=dev))
+    logp, entropy, lse = out
+    for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
+        _need(t, torch.float32, n, 1)
+        _per_row(t, torch.float32, n, (N,))
+    if ws is None:
+        ws = torch.empty(lib().tt_lmhead_token_logprob_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
+    err = new_err(dev) if err is None else err
+    with _on(hidden, w_vocab, targets, logp, entropy, lse, ws, err):
+        rc = lib().tt_lmhead_token_logprob(_p(hidden), _p(w_vocab), N, V, Hd, _p(targets), _p(logp), _p(entropy),
+                                           _p(lse), _p(ws), ws.numel() * ws.element_size(), _p(err), _stream(dev))
+    _check(rc, "tt_lmhead_token_logprob")
+    return logp, entropy, lse
+
+
+def lmhead_token_logprob_bwd(hidden, w_vocab, targets, lse, entropy=None, dlogp=None, dentropy=None, dlse=None,
+                             out=None, ws=None, err=None, dw_dtype=torch.float32):
+    """Gradients of an objective whose gradients with respect to lmhead_token_logprob's outputs are dlogp, dentropy and
+    dlse [N] (each optional; tt_lmhead_token_logprob_bwd): d_hidden bf16 [N,Hd], d_w_vocab fp32 or bf16 [V,Hd]
+    (`dw_dtype`, or the type of out[1])."""
+    N, V, Hd = _lmhead_args(hidden, w_vocab, targets)
+    dev = hidden.device
+    _need(lse, torch.float32, "lse", 1)
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
+        _per_row(t, torch.float32, n, (N,))
+    if out is None:
+        if dw_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("dw_dtype must be torch.float32 or torch.bfloat16")
+        out = (torch.empty_like(hidden), torch.empty(V, Hd, dtype=dw_dtype, device=dev))
+    dh, dw = out
+    _per_row(dh, torch.bfloat16, "d_hidden", (N, Hd))
+    if dw.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("d_w_vocab must be fp32 or bf16")
+    _per_row(dw, dw.dtype, "d_w_vocab", (V, Hd))
+    if ws is None:
+        ws = torch.empty(lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
+    err = new_err(dev) if err is None else err
+    with _on(hidden, w_vocab, targets, lse, entropy, dlogp, dentropy, dlse, dh, dw, ws, err):
+        rc = lib().tt_lmhead_token_logprob_bwd(_p(hidden), _p(w_vocab), N, V, Hd, _p(targets), _p(lse), _p(entropy),
+                                               _p(dlogp), _p(dentropy), _p(dlse), _p(dh), _p(dw), _DTYPES[dw.dtype],
+                                               _p(ws), ws.numel() * ws.element_size(), _p(err), _stream(dev))
+    _check(rc, "tt_lmhead_token_logprob_bwd")
     return dh, dw
 
 

@@ -64,8 +64,12 @@ constexpr uint32_t kBox = 64 * 64 * 2;       // one [64 K rows][64 columns] box 
 constexpr uint32_t kTmemCols = 512;          // two [128][256] fp32 accumulators
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Epilogues: per-row log-sum-exp partials (forward), dz (bf16), plain bf16 / fp32 stores.
-enum { EPI_LSE = 0, EPI_DZ = 1, EPI_BF16 = 2, EPI_F32 = 3 };
+// Epilogues: per-row log-sum-exp partials (forward), dz (bf16), plain bf16 / fp32 stores; the partials with an
+// entropy sum beside them, and dz of an objective of log-prob and entropy.
+enum { EPI_LSE = 0, EPI_DZ = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_LSE_H = 4, EPI_DZ_H = 5 };
+// What stands for a column >= V where an entropy is summed: far below any
+// logit, and finite, so that 0·(z − m) is 0.
+constexpr float kNoColumn = -1e30f;
 
 // mbarriers: FULL[s] (TMA bytes landed), EMPTY[s] (MMAs reading stage s done),
 // ACC_FULL[a] (accumulator a holds a finished tile), ACC_EMPTY[a] (the 128
@@ -105,6 +109,9 @@ struct LhArgs {
   float* of;               // EPI_F32: [M][ldo]
   int64_t ldo;
   int32_t* err;
+  float* pu;             // EPI_LSE_H: [nN][M] Σ 2^x·x, x = (z − m)·log2 e
+  const float* entropy;  // EPI_DZ_H, as the next three (each may be NULL): per row
+  const float *dlogp, *dentropy, *dlse;
 };
 
 template <int EPI, bool A_MN, bool B_MN>
@@ -112,6 +119,8 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
     lmhead_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const LhArgs a) {
   using L = LhSmem;
+  constexpr bool kLse = EPI == EPI_LSE || EPI == EPI_LSE_H, kDz = EPI == EPI_DZ || EPI == EPI_DZ_H;
+  constexpr bool kEnt = EPI == EPI_LSE_H || EPI == EPI_DZ_H;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::bars);
@@ -270,16 +279,26 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       const bool row_ok = row < a.M;
       int y = -1;
       float gw = 0.f, lrow = 0.f;
-      if (EPI == EPI_LSE || EPI == EPI_DZ) y = row_ok ? a.targets[row] : -1;
-      if (EPI == EPI_DZ && row_ok) {
-        gw = a.g * (a.weights ? a.weights[row] : 1.f);
+      if (kLse || kDz) y = row_ok ? a.targets[row] : -1;
+      float gh = 0.f, gb = 0.f;  // EPI_DZ_H: dz = −p·(gb + gh·log p) + gw·[column == target]
+      if (kDz && row_ok) {
+        if (kEnt) {
+          gw = a.dlogp ? a.dlogp[row] : 0.f;
+          gb = a.dlse ? gw - a.dlse[row] : gw;
+          if (a.dentropy) {
+            gh = a.dentropy[row];
+            gb = fmaf(gh, a.entropy[row], gb);
+          }
+        } else {
+          gw = a.g * (a.weights ? a.weights[row] : 1.f);
+        }
         lrow = a.lse[row];
         if ((y < 0 || (int64_t)y >= a.Ncols) && n == 0) set_err(a.err, TT_ERR_INVALID_ARG);
       }
       const int64_t yc = (int64_t)y - c0;  // target column within the tile
       if (!mbar_wait(&bar[ACC_FULL + acc], (uint32_t)((it >> 1) & 1), abort_flag, 4)) break;
       tc_fence_after();
-      float m_run = -INFINITY, s_run = 0.f, zt = 0.f;
+      float m_run = -INFINITY, s_run = 0.f, u_run = 0.f, zt = 0.f;
       bool found = false;
 #pragma unroll 1
       for (int c = 0; c < kBN / 32; ++c) {
@@ -289,11 +308,11 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         tmem_pin(u);
         const int64_t col0 = c0 + c * 32;
         const int64_t nvalid = a.Ncols - col0;  // columns j < nvalid exist
-        if (EPI == EPI_LSE) {
+        if (kLse) {
           float cm = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float z = j < nvalid ? __uint_as_float(u[j]) : -INFINITY;
+            const float z = j < nvalid ? __uint_as_float(u[j]) : kEnt ? kNoColumn : -INFINITY;
             u[j] = __float_as_uint(z);
             cm = fmaxf(cm, z);
           }
@@ -312,16 +331,23 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
           }
           const float nm = fmaxf(m_run, cm);
           if (nm != -INFINITY) {
+            if (kEnt) {  // Σ 2^x·x around the new maximum (its offset kept finite while m_run is still -inf)
+              const float dx = fmaxf((m_run - nm) * kLog2e, kNoColumn);
+              u_run = fmaf(dx, s_run, u_run) * fast_exp2(dx);
+            }
             s_run *= fast_exp2((m_run - nm) * kLog2e);  // 0 while m_run is still -inf (s_run is 0 then)
             const float2 l2 = make_float2(kLog2e, kLog2e), nn = make_float2(-nm, -nm);
-            float2 acc2 = make_float2(0.f, 0.f);
+            float2 acc2 = make_float2(0.f, 0.f), ent2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float2 x = __fmul2_rn(
                   __fadd2_rn(make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), nn), l2);
-              acc2 = __fadd2_rn(acc2, make_float2(fast_exp2(x.x), fast_exp2(x.y)));
+              const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              acc2 = __fadd2_rn(acc2, e);
+              if (kEnt) ent2 = __ffma2_rn(e, x, ent2);
             }
             s_run += acc2.x + acc2.y;
+            if (kEnt) u_run += ent2.x + ent2.y;
             m_run = nm;
           }
         } else if (EPI == EPI_F32) {
@@ -335,6 +361,24 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
                                 __uint_as_float(u[4 * q + 3]));
           }
         } else {
+          if (EPI == EPI_DZ_H) {
+            const float2 l2 = make_float2(kLog2e, kLog2e), nl = make_float2(-lrow, -lrow);
+            const float2 nh = make_float2(-gh, -gh), nb = make_float2(-gb, -gb);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 lp = __fadd2_rn(make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), nl);
+              const float2 x = __fmul2_rn(lp, l2);
+              const float2 dz = __fmul2_rn(make_float2(fast_exp2(x.x), fast_exp2(x.y)), __ffma2_rn(nh, lp, nb));
+              u[2 * j] = __float_as_uint(dz.x);
+              u[2 * j + 1] = __float_as_uint(dz.y);
+            }
+            if ((uint64_t)(yc - c * 32) < 32u) {
+              const int jc = (int)(yc - c * 32);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j == jc) u[j] = __float_as_uint(__uint_as_float(u[j]) + gw);
+            }
+          }
           if (EPI == EPI_DZ) {
             // dz = g·w·(e^(z − lse) − [column == target])
             const float2 l2 = make_float2(kLog2e, kLog2e), nl = make_float2(-lrow, -lrow);
@@ -369,9 +413,10 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       }
       tc_fence_before();
       mbar_arrive(&bar[ACC_EMPTY + acc]);
-      if (EPI == EPI_LSE && row_ok) {
+      if (kLse && row_ok) {
         a.pm[(int64_t)n * a.M + row] = m_run;
         a.ps[(int64_t)n * a.M + row] = s_run;
+        if (kEnt) a.pu[(int64_t)n * a.M + row] = u_run;
         if (found) a.pz[row] = zt;
       }
     }
@@ -442,8 +487,56 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   logp[row] = lp;
 }
 
+// The same with the entropy: per row, (m, s, u) of the nV tiles joined around
+// the row's maximum M as S = Σ s_j·f_j, U = Σ (u_j·ln 2 + (m_j − M)·s_j)·f_j,
+// f_j = e^(m_j − M); H = ln S − U/S, lse = M + ln S, logp = (z_{t,y_t} − M) −
+// ln S.
+struct LhStat {
+  float m, s, u;
+};
+__device__ __forceinline__ void stat_merge(LhStat& a, const LhStat& b) {
+  const float M = fmaxf(a.m, b.m);
+  if (M == -INFINITY) return;
+  const float da = fmaxf(a.m - M, kNoColumn), db = fmaxf(b.m - M, kNoColumn);
+  const float fa = expf(da), fb = expf(db);
+  a.u = fmaf(da, a.s, a.u) * fa + fmaf(db, b.s, b.u) * fb;
+  a.s = a.s * fa + b.s * fb;
+  a.m = M;
+}
+__global__ void __launch_bounds__(32 * kCombineWarps)
+    lmhead_combine_entropy_kernel(const float* pm, const float* ps, const float* pu, const float* pz, int64_t N, int nV,
+                                  int64_t V, const int32_t* targets, float* logp, float* entropy, float* lse,
+                                  int32_t* err) {
+  __shared__ LhStat part[kCombineWarps][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  LhStat t = {-INFINITY, 0.f, 0.f};
+  if (row < N)
+    for (int j = w; j < nV; j += kCombineWarps) {
+      const int64_t at = (int64_t)j * N + row;
+      stat_merge(t, LhStat{pm[at], ps[at], pu[at] * 0.6931471805599453f});
+    }
+  part[w][lane] = t;
+  __syncthreads();
+  if (w != 0 || row >= N) return;
+#pragma unroll
+  for (int k = 1; k < kCombineWarps; ++k) stat_merge(t, part[k][lane]);
+  const float log_s = logf(t.s);
+  const float h = log_s - t.u / t.s;
+  entropy[row] = h < 0.f ? 0.f : h;
+  lse[row] = t.m + log_s;
+  const int y = targets[row];
+  if (y < 0 || (int64_t)y >= V) {
+    set_err(err, TT_ERR_INVALID_ARG);
+    logp[row] = __int_as_float(0x7fc00000);
+  } else {
+    logp[row] = (pz[row] - t.m) - log_s;
+  }
+}
+
 struct LhWs {
   size_t pm, ps, pz, total;
+  size_t pu, total_u;  // with the entropy sums behind the rest
 };
 LhWs lh_layout(int64_t N, int64_t V) {
   const int64_t nV = (V + kBN - 1) / kBN;
@@ -454,6 +547,8 @@ LhWs lh_layout(int64_t N, int64_t V) {
   w.ps = take(sizeof(float) * (size_t)nV * (size_t)N);
   w.pz = take(sizeof(float) * (size_t)N);
   w.total = o;
+  w.pu = take(sizeof(float) * (size_t)nV * (size_t)N);
+  w.total_u = o;
   return w;
 }
 
@@ -527,6 +622,60 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
   return dz_bytes(N, V) + 256;
 }
 
+namespace {
+// dH = dz·W (bf16) and dW = dzᵀ·H (fp32, or bf16 with dw_dtype = TT_DT_BF16) from dz [N][ldz]; ctr[1], ctr[2]: their
+// tile counters (0 at launch).
+int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd, const __nv_bfloat16* dz,
+                int* ctr, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, int32_t* err, cudaStream_t st) {
+  const int64_t ldz = dz_ld(V);
+  // 2. dH = dz·W: A = dz [N][V] (K-major, K = V); B = W [V][Hd] read MN-major; token-major tiles
+  CUtensorMap mdz, mw_mn;
+  if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
+      !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
+    return TT_ERR_CUDA;
+  LhArgs b = lh_args(N, Hd, V, 0, err);
+  b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr + 1;
+  // 3. dW = dzᵀ·H: A = dz read MN-major ([K = tokens][M = vocabulary]), B = H [N][Hd] read MN-major
+  CUtensorMap mdz_mn, mh_mn;
+  if (!make_tmap_bf16_ld(&mdz_mn, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, 64) ||
+      !make_tmap_bf16(&mh_mn, hidden, (uint64_t)Hd, (uint64_t)N, 64))
+    return TT_ERR_CUDA;
+  LhArgs c = lh_args(V, Hd, N, 0, err);
+  const bool dw_bf16 = dw_dtype == TT_DT_BF16;
+  if (dw_bf16)
+    c.ob = static_cast<__nv_bfloat16*>(d_w_vocab);
+  else
+    c.of = static_cast<float*>(d_w_vocab);
+  c.ldo = Hd; c.counter = ctr + 2;
+  // dH and dW both only read dz: dW runs on a second stream forked after dz,
+  // so that its CTAs (which claim tiles as they free up) take the SMs that
+  // dH's last round of tiles (792 tiles of K = V at the benchmarked shape,
+  // 5.2 per SM) leaves idle; joined back before returning. Not while the
+  // caller's stream is being captured into a graph (the second stream is
+  // destroyed here, before such a capture would end).
+  cudaStream_t side = nullptr;
+  cudaEvent_t fork = nullptr, join = nullptr;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  const bool two = cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
+                   cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking) == cudaSuccess &&
+                   cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) == cudaSuccess &&
+                   cudaEventCreateWithFlags(&join, cudaEventDisableTiming) == cudaSuccess &&
+                   cudaEventRecord(fork, st) == cudaSuccess && cudaStreamWaitEvent(side, fork, 0) == cudaSuccess;
+  if (!two) (void)cudaGetLastError();
+  const int rc = launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
+  int rc2 = rc;
+  if (!rc)
+    rc2 = dw_bf16 ? launch_gemm<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
+                  : launch_gemm<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st);
+  if (two && (cudaEventRecord(join, side) != cudaSuccess || cudaStreamWaitEvent(st, join, 0) != cudaSuccess))
+    rc2 = rc2 ? rc2 : TT_ERR_CUDA;
+  if (join) cudaEventDestroy(join);
+  if (fork) cudaEventDestroy(fork);
+  if (side) cudaStreamDestroy(side);
+  return rc ? rc : rc2;
+}
+}  // namespace
+
 TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
                                  const int32_t* targets, const float* weights, float g, const float* lse,
                                  tt_bf16* d_hidden, float* d_w_vocab, void* ws, size_t ws_bytes, int32_t* err,
@@ -550,41 +699,68 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
   a.targets = targets; a.weights = weights; a.g = g; a.lse = lse; a.ob = dz; a.ldo = ldz; a.counter = ctr;
   rc = launch_gemm<EPI_DZ, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  // 2. dH = dz·W: A = dz [N][V] (K-major, K = V); B = W [V][Hd] read MN-major; token-major tiles
-  CUtensorMap mdz, mw_mn;
-  if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
-      !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
+  return lh_products(hidden, w_vocab, N, V, Hd, dz, ctr, d_hidden, d_w_vocab, TT_DT_F32, err, st);
+}
+
+TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V) {
+  if (N < 1 || V < 1) return 0;
+  return lh_layout(N, V).total_u;
+}
+
+TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
+                                   const int32_t* targets, float* logp, float* entropy, float* lse, void* ws,
+                                   size_t ws_bytes, int32_t* err, tt_stream_t stream) {
+  int rc = lh_check(hidden, w_vocab, N, V, Hd, targets, err);
+  if (rc) return rc;
+  if (!logp || !entropy || !lse || !ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
+  const LhWs Lw = lh_layout(N, V);
+  if (ws_bytes < Lw.total_u) return TT_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  CUtensorMap mh, mw;
+  if (!make_tmap_bf16(&mh, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ||
+      !make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN))
     return TT_ERR_CUDA;
-  LhArgs b = lh_args(N, Hd, V, 0, err);
-  b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr + 1;
-  // 3. dW = dzᵀ·H: A = dz read MN-major ([K = tokens][M = vocabulary]), B = H [N][Hd] read MN-major
-  CUtensorMap mdz_mn, mh_mn;
-  if (!make_tmap_bf16_ld(&mdz_mn, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, 64) ||
-      !make_tmap_bf16(&mh_mn, hidden, (uint64_t)Hd, (uint64_t)N, 64))
+  LhArgs a = lh_args(N, V, Hd, 1, err);
+  a.targets = targets;
+  a.pm = ws_at<float>(ws, Lw.pm);
+  a.ps = ws_at<float>(ws, Lw.ps);
+  a.pz = ws_at<float>(ws, Lw.pz);
+  a.pu = ws_at<float>(ws, Lw.pu);
+  rc = launch_gemm<EPI_LSE_H, false, false>(mh, mw, a, st);
+  if (rc) return rc;
+  lmhead_combine_entropy_kernel<<<(unsigned)((N + 31) / 32), 32 * kCombineWarps, 0, st>>>(
+      a.pm, a.ps, a.pu, a.pz, N, a.nN, V, targets, logp, entropy, lse, err);
+  TT_LAUNCH_CHECK();
+  return TT_OK;
+}
+
+TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
+  return tt_lmhead_logprob_bwd_workspace_bytes(N, V);
+}
+
+TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
+                                       const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* dlogp, const float* dentropy, const float* dlse,
+                                       tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws, size_t ws_bytes,
+                                       int32_t* err, tt_stream_t stream) {
+  int rc = lh_check(hidden, w_vocab, N, V, Hd, targets, err);
+  if (rc) return rc;
+  if (!lse || (dentropy && !entropy) || !d_hidden || !d_w_vocab || !ws || !aligned16(ws) || !aligned16(d_hidden) ||
+      !aligned16(d_w_vocab) || (dw_dtype != TT_DT_F32 && dw_dtype != TT_DT_BF16))
+    return TT_ERR_INVALID_ARG;
+  if (ws_bytes < tt_lmhead_token_logprob_bwd_workspace_bytes(N, V)) return TT_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
+  int* ctr = ws_at<int>(ws, dz_bytes(N, V));  // [3]: dz, dH, dW
+  if (cudaMemsetAsync(ctr, 0, 3 * sizeof(int), st) != cudaSuccess) return TT_ERR_CUDA;
+  CUtensorMap mh, mw;
+  if (!make_tmap_bf16(&mh, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ||
+      !make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN))
     return TT_ERR_CUDA;
-  LhArgs c = lh_args(V, Hd, N, 0, err);
-  c.of = d_w_vocab; c.ldo = Hd; c.counter = ctr + 2;
-  // dH and dW both only read dz: dW runs on a second stream forked after dz,
-  // so that its CTAs (which claim tiles as they free up) take the SMs that
-  // dH's last round of tiles (792 tiles of K = V at the benchmarked shape,
-  // 5.2 per SM) leaves idle; joined back before returning. Not while the
-  // caller's stream is being captured into a graph (the second stream is
-  // destroyed here, before such a capture would end).
-  cudaStream_t side = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  const bool two = cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
-                   cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking) == cudaSuccess &&
-                   cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) == cudaSuccess &&
-                   cudaEventCreateWithFlags(&join, cudaEventDisableTiming) == cudaSuccess &&
-                   cudaEventRecord(fork, st) == cudaSuccess && cudaStreamWaitEvent(side, fork, 0) == cudaSuccess;
-  if (!two) (void)cudaGetLastError();
-  rc = launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
-  int rc2 = rc ? rc : launch_gemm<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st);
-  if (two && (cudaEventRecord(join, side) != cudaSuccess || cudaStreamWaitEvent(st, join, 0) != cudaSuccess))
-    rc2 = rc2 ? rc2 : TT_ERR_CUDA;
-  if (join) cudaEventDestroy(join);
-  if (fork) cudaEventDestroy(fork);
-  if (side) cudaStreamDestroy(side);
-  return rc ? rc : rc2;
+  LhArgs a = lh_args(N, V, Hd, 1, err);
+  a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
+  a.ob = dz; a.ldo = dz_ld(V); a.counter = ctr;
+  rc = launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
+  if (rc) return rc;
+  return lh_products(hidden, w_vocab, N, V, Hd, dz, ctr, d_hidden, d_w_vocab, dw_dtype, err, st);
 }

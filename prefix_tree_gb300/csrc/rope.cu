@@ -1,0 +1,190 @@
+// Rotary positions of Q and K with one or several position axes, and their
+// inverse (the rotation is orthogonal, so the inverse is also the backward
+// pass).
+//
+//   θ_i = pos[a(i)][t]·f_i,   (x1, x2) -> (x1·cos θ_i − x2·sin θ_i, x2·cos θ_i + x1·sin θ_i),  i < rot/2
+//
+// over the pairs (i, i + rot/2) or (2i, 2i + 1) of every head; dimensions >=
+// rot pass through.
+//
+// Angles. f_i/2π modulo 1 is held as a 64-bit binary fraction of a turn, so
+// pos·f_i modulo one turn is one wrapping 64-bit product: no large argument
+// is ever rounded to fp32 (at position 10^6 an fp32 angle is off by up to
+// 0.03 rad), and no fp64 instruction is needed. The top 32 bits, as a signed
+// fraction of half a turn, go to sincospif.
+#include "common.cuh"
+
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+namespace tt {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kMaxHalf = 128;  // rot <= 256
+constexpr int kMaxAxes = 4;
+constexpr int kTokens = 4;  // tokens per block
+
+struct RopeArgs {
+  const void* x[2];  // q, k
+  void* y[2];
+  int64_t ld[2], ldo[2];
+  int heads[2];
+  int64_t N;
+  int d, half, npv, nrot;  // npv: vector pairs of a head, the first nrot of them rotated
+  const int32_t* pos;
+  int64_t pos_ld;
+  int adjacent, inverse;
+  uint64_t turn[kMaxHalf];  // f_i/2π mod 1, in units of 2^-64
+  uint8_t axis[kMaxHalf];
+};
+
+// VEC consecutive elements of type T as floats.
+template <typename T, int VEC>
+struct Vec {
+  static __device__ __forceinline__ void load(const T* p, float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+      f[0] = static_cast<float>(*p);
+    } else {
+      static_assert(VEC * sizeof(T) == 16, "16-byte vectors");
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[i] = static_cast<float>(e[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+      *p = static_cast<T>(f[0]);
+    } else {
+      uint4 u;
+      T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = static_cast<T>(f[i]);
+      *reinterpret_cast<uint4*>(p) = u;
+    }
+  }
+};
+
+// One pair turned; the order of the roundings is fixed, so that results do not depend on alignment.
+__device__ __forceinline__ void turn_pair(float& x1, float& x2, float c, float s) {
+  const float p = x1, q = x2;
+  x1 = __fmaf_rn(-q, s, __fmul_rn(p, c));
+  x2 = __fmaf_rn(p, s, __fmul_rn(q, c));
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float sc[kTokens][kMaxHalf], ss[kTokens][kMaxHalf];
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int nt = (int)min((int64_t)kTokens, a.N - t0);
+  for (int i = threadIdx.x; i < nt * a.half; i += kRopeThreads) {
+    const int t = i / a.half, f = i - t * a.half;
+    const int64_t pos = a.pos[a.axis[f] * a.pos_ld + t0 + t];
+    const uint64_t turn = (uint64_t)pos * a.turn[f];
+    float s, c;
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+    sc[t][f] = c;
+    ss[t][f] = a.inverse ? -s : s;
+  }
+  __syncthreads();
+  const int H = a.heads[0] + a.heads[1];
+  for (int i = threadIdx.x; i < nt * H * a.npv; i += kRopeThreads) {
+    const int r = i / a.npv, pv = i - r * a.npv;
+    const int t = r / H, hh = r - t * H;
+    const int w = hh >= a.heads[0];
+    const int64_t head = (int64_t)(hh - (w ? a.heads[0] : 0)) * a.d;
+    const T* x = static_cast<const T*>(a.x[w]) + (t0 + t) * a.ld[w] + head;
+    T* y = static_cast<T*>(a.y[w]) + (t0 + t) * a.ldo[w] + head;
+    // the two vectors of this item: half a rotation apart, or next to each other
+    const bool rotated = pv < a.nrot;
+    const int o1 = a.adjacent || !rotated ? (rotated ? 2 * VEC * pv : 2 * a.half + 2 * VEC * (pv - a.nrot)) : VEC * pv;
+    const int o2 = a.adjacent || !rotated ? o1 + VEC : o1 + a.half;
+    if (!rotated && x == y) continue;
+    float u[VEC], v[VEC];
+    Vec<T, VEC>::load(x + o1, u);
+    Vec<T, VEC>::load(x + o2, v);
+    if (rotated) {
+      const float* c = &sc[t][VEC * pv];
+      const float* s = &ss[t][VEC * pv];
+      if (!a.adjacent) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) turn_pair(u[j], v[j], c[j], s[j]);
+      } else if constexpr (VEC == 1) {
+        turn_pair(u[0], v[0], c[0], s[0]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          turn_pair(u[2 * j], u[2 * j + 1], c[j], s[j]);
+          turn_pair(v[2 * j], v[2 * j + 1], c[VEC / 2 + j], s[VEC / 2 + j]);
+        }
+      }
+    }
+    Vec<T, VEC>::store(y + o1, u);
+    Vec<T, VEC>::store(y + o2, v);
+  }
+}
+
+template <typename T>
+int launch_rope(RopeArgs& a, int rot, cudaStream_t st) {
+  constexpr int VEC = 16 / sizeof(T);
+  bool vec = rot % (2 * VEC) == 0 && a.d % (2 * VEC) == 0;
+  for (int w = 0; w < 2; ++w)
+    if (a.heads[w] > 0)
+      vec = vec && aligned16(a.x[w]) && aligned16(a.y[w]) && a.ld[w] % VEC == 0 && a.ldo[w] % VEC == 0;
+  const int step = vec ? VEC : 1;
+  a.npv = a.d / (2 * step);
+  a.nrot = rot / (2 * step);
+  const unsigned grid = (unsigned)((a.N + kTokens - 1) / kTokens);
+  if (vec)
+    rope_kernel<T, VEC><<<grid, kRopeThreads, 0, st>>>(a);
+  else
+    rope_kernel<T, 1><<<grid, kRopeThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace tt
+
+using namespace tt;
+
+TT_API int tt_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, const void* k, void* k_out, int64_t k_ld,
+                   int64_t k_out_ld, int dtype, int64_t N, int Hq, int Hkv, int d, int rot, const int32_t* pos,
+                   int64_t pos_ld, int axes, const uint8_t* axis_host, const double* freq_host, int adjacent,
+                   int inverse, tt_stream_t stream) {
+  if (N < 0 || Hq < 0 || Hkv < 0 || d < 2 || rot < 2 || rot > d || axes < 1) return TT_ERR_INVALID_ARG;
+  if (dtype != TT_DT_BF16 && dtype != TT_DT_F16 && dtype != TT_DT_F32) return TT_ERR_INVALID_ARG;
+  if (!axis_host || !freq_host) return TT_ERR_INVALID_ARG;
+  if (d % 2 || rot % 2 || d > 1024 || rot > 2 * kMaxHalf || axes > kMaxAxes || Hq > 1024 || Hkv > 1024)
+    return TT_ERR_UNSUPPORTED;
+  RopeArgs a = {};
+  for (int i = 0; i < rot / 2; ++i) {
+    if (axis_host[i] >= axes || !std::isfinite(freq_host[i])) return TT_ERR_INVALID_ARG;
+    double t = freq_host[i] / 6.283185307179586476925;
+    t -= std::floor(t);
+    a.turn[i] = t < 1.0 ? (uint64_t)(t * 0x1p64) : 0;
+    a.axis[i] = axis_host[i];
+  }
+  if (N == 0 || Hq + Hkv == 0) return TT_OK;
+  const size_t es = dtype == TT_DT_F32 ? 4 : 2;
+  const void* x[2] = {q, k};
+  void* y[2] = {q_out, k_out};
+  const int64_t ld[2] = {q_ld, k_ld}, ldo[2] = {q_out_ld, k_out_ld};
+  const int heads[2] = {Hq, Hkv};
+  for (int w = 0; w < 2; ++w) {
+    a.x[w] = x[w]; a.y[w] = y[w]; a.ld[w] = ld[w]; a.ldo[w] = ldo[w]; a.heads[w] = heads[w];
+    if (heads[w] == 0) continue;
+    if (!x[w] || !y[w] || ld[w] < (int64_t)heads[w] * d || ldo[w] < (int64_t)heads[w] * d) return TT_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(x[w]) | reinterpret_cast<uintptr_t>(y[w])) % es) return TT_ERR_INVALID_ARG;
+    if (x[w] == y[w] && ld[w] != ldo[w]) return TT_ERR_INVALID_ARG;
+  }
+  if (!pos || (axes > 1 && pos_ld != 0 && pos_ld < N) || N > (int64_t)INT32_MAX) return TT_ERR_INVALID_ARG;
+  a.N = N; a.d = d; a.half = rot / 2; a.pos = pos; a.pos_ld = pos_ld; a.adjacent = adjacent; a.inverse = inverse;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case TT_DT_BF16: return launch_rope<__nv_bfloat16>(a, rot, st);
+    case TT_DT_F16: return launch_rope<__half>(a, rot, st);
+    default: return launch_rope<float>(a, rot, st);
+  }
+}

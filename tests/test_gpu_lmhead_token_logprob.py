@@ -1,0 +1,182 @@
+"""tt_lmhead_token_logprob and its backward (LM head fused with log-prob and entropy) against the fp64 oracle, and a
+policy-optimisation step over a tree through all the calls."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import attention as A
+from oracle import lmhead as LH
+from oracle import rope as R
+from oracle import token_logprob as TL
+from oracle import tree as T
+from tests._util import GRAD_RL2, LOGP_ATOL, dev_to_f64, f64, rel_l2, to_dev_bf16
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(1, 1, 64), (77, 1000, 64), (300, 3001, 128), (129, 256, 192), (513, 4099, 256), (256, 511, 64)]
+
+
+def _inputs(N, V, Hd):
+    d = synth.lmhead_inputs(N + V + Hd, n_rows=N, vocab=V, hidden=Hd)
+    y = torch.tensor(d["targets"], dtype=torch.int32, device="cuda")
+    return d, to_dev_bf16(d["H"]), to_dev_bf16(d["W"]), y
+
+
+@pytest.mark.parametrize("N,V,Hd", SHAPES)
+def test_forward(tt, N, V, Hd):
+    """log-probs and lse within 1e-4 (as the log-prob fused with the head); the entropy adds U/S, off by as much
+    relative to |U/S| = max z + ... = lse − max z − H."""
+    d, H, W, y = _inputs(N, V, Hd)
+    err = tt.new_err("cuda")
+    logp, h, lse = tt.lmhead_token_logprob(H, W, y, err=err)
+    assert int(err.item()) == 0
+    z = LH.logits(f64(d["H"]), f64(d["W"]))
+    r_logp, r_h, r_lse, _, _ = TL.token_logprob(z, d["targets"])
+    assert np.abs(dev_to_f64(logp) - r_logp).max() <= LOGP_ATOL
+    assert np.abs(dev_to_f64(lse) - r_lse).max() <= LOGP_ATOL
+    us = np.abs(r_lse - z.max(1) - r_h)
+    assert (np.abs(dev_to_f64(h) - r_h) <= LOGP_ATOL * (1 + us)).all()
+    # bitwise repeatable; the log-prob call's values up to rounding
+    again = tt.lmhead_token_logprob(H, W, y)
+    assert all(torch.equal(a, b) for a, b in zip((logp, h, lse), again))
+    old, old_lse, _ = tt.lmhead_logprob(H, W, y)
+    assert (old - logp).abs().max().item() <= 2e-5 and (old_lse - lse).abs().max().item() <= 2e-5
+
+
+@pytest.mark.parametrize("N,V,Hd", SHAPES[1:])
+@pytest.mark.parametrize("dw_dtype", [torch.float32, torch.bfloat16])
+def test_backward(tt, N, V, Hd, dw_dtype):
+    """Relative L2 1e-2 as for the gradients of the log-prob (bf16 inputs and dz, fp32 sums)."""
+    d, H, W, y = _inputs(N, V, Hd)
+    rng = np.random.default_rng(N)
+    g = {n: rng.standard_normal(N).astype(np.float32) for n in ("dlogp", "dentropy", "dlse")}
+    gt = {n: torch.tensor(v, device="cuda") for n, v in g.items()}
+    z = LH.logits(f64(d["H"]), f64(d["W"]))
+    _, h, lse = tt.lmhead_token_logprob(H, W, y)
+    for names in (("dlogp",), ("dentropy",), ("dlse",), ("dlogp", "dentropy", "dlse")):
+        err = tt.new_err("cuda")
+        dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, **{n: gt[n] for n in names}, err=err, dw_dtype=dw_dtype)
+        assert int(err.item()) == 0 and dh.dtype == torch.bfloat16 and dw.dtype == dw_dtype
+        dz = TL.token_logprob_grad(z, d["targets"], **{n: g[n] for n in names})
+        assert rel_l2(dev_to_f64(dh), dz @ f64(d["W"])) <= GRAD_RL2, names
+        assert rel_l2(dev_to_f64(dw), dz.T @ f64(d["H"])) <= GRAD_RL2, names
+    again = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, **gt, dw_dtype=dw_dtype)
+    assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
+
+
+def test_log_prob_gradient_equals_the_weighted_call(tt):
+    """dlogp = −g·w is the weighted loss: the two calls form dz in another order of two products, then round to bf16."""
+    d, H, W, y = _inputs(300, 3001, 128)
+    w = torch.rand(300, device="cuda")
+    _, lse, _ = tt.lmhead_logprob(H, W, y, w)
+    a = tt.lmhead_logprob_bwd(H, W, y, lse, w, g=0.5)
+    b = tt.lmhead_token_logprob_bwd(H, W, y, lse, dlogp=-0.5 * w)
+    for x, z in zip(a, b):
+        assert rel_l2(dev_to_f64(x), dev_to_f64(z)) <= 2.0 ** -8
+
+
+def test_bad_target_and_arguments(tt):
+    d, H, W, y = _inputs(40, 700, 64)
+    y[5], y[6] = 700, -1
+    err = tt.new_err("cuda")
+    logp, h, lse = tt.lmhead_token_logprob(H, W, y, err=err)
+    assert int(err.item()) == -1
+    assert torch.isnan(logp).nonzero().flatten().tolist() == [5, 6]
+    assert torch.isfinite(h).all() and torch.isfinite(lse).all()
+    err = tt.new_err("cuda")
+    dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=torch.ones(40, device="cuda"), err=err)
+    assert int(err.item()) == -1 and torch.isfinite(dh).all() and torch.isfinite(dw).all()
+    small = torch.empty(64, dtype=torch.uint8, device="cuda")
+    for bad, code in ((lambda: tt.lmhead_token_logprob(H[:, :32].contiguous(), W[:, :32].contiguous(), y), -3),
+                      (lambda: tt.lmhead_token_logprob(H, W, y, ws=small), -4),
+                      (lambda: tt.lmhead_token_logprob_bwd(H, W, y, lse, ws=small), -4),
+                      (lambda: tt.lmhead_token_logprob_bwd(H, W, y, lse, dentropy=lse), -1)):
+        with pytest.raises(tt.TTError) as e:
+            bad()
+        assert e.value.code == code
+    for bad in (lambda: tt.lmhead_token_logprob(H, W, y[:3]), lambda: tt.lmhead_token_logprob(H, W[:, :32], y),
+                lambda: tt.lmhead_token_logprob_bwd(H, W, y, lse[:3])):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_captured_step(tt):
+    """Forward and backward captured into one graph, replayed on new inputs."""
+    d, H, W, y = _inputs(129, 1000, 128)
+    dev = "cuda"
+    out, grads = tuple(torch.empty(3, 129, device=dev)), (torch.empty_like(H), torch.empty(1000, 128, device=dev))
+    dl, de, err = torch.randn(129, device=dev), torch.randn(129, device=dev), tt.new_err(dev)
+
+    def step(out, grads):
+        logp, h, lse = tt.lmhead_token_logprob(H, W, y, out=out, err=err)
+        return (logp, h, lse) + tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de, out=grads, err=err)
+
+    step(None, None)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(out, grads)
+    H.mul_(0.5)
+    y.copy_(y.flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    ref = step(None, None)
+    assert all(torch.equal(a, b) for a, b in zip(ref, out + grads))
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_policy_step_over_a_tree(tt, axes):
+    """Rotary -> tree attention -> head with log-prob and entropy -> backward of all of it, against the fp64 oracle
+    of the same chain on the bf16 values that each call receives."""
+    sh = synth.tree_shape(0)
+    tab = T.tables(sh.seg_parent, sh.seg_len)
+    N, hq, hkv, d, V = sh.N, 4, 2, 64, 1000
+    rng = np.random.default_rng(axes)
+    qr, kr, v = (to_dev_bf16(synth.normal_bf16(rng, (N, n, d))) for n in (hq, hkv, hkv))
+    W = to_dev_bf16(synth.normal_bf16(rng, (V, hq * d), 0.1))
+    y = torch.tensor(rng.integers(0, V, N), dtype=torch.int32, device="cuda")
+    tree = tt.tree_build(torch.tensor(sh.seg_parent, device="cuda"), torch.tensor(sh.seg_len, device="cuda"))
+    pos = tree.tok_pos if axes == 1 else torch.stack([tree.tok_pos, tree.tok_pos // 4, tree.tok_pos % 4])
+    how = {} if axes == 1 else dict(sections=(12, 10, 10))
+    w = torch.tensor(tab.tok_weight, device="cuda")
+    dlogp, dent = -w, -0.01 * w
+    err = tt.new_err("cuda")
+    # forward
+    q, k = tt.rope(qr, kr, pos, **how)
+    O, LSE = tt.tree_attn_fwd(tree, q, k, v, err=err)
+    hid = O.view(N, hq * d)
+    logp, ent, lse = tt.lmhead_token_logprob(hid, W, y, err=err)
+    # backward
+    dh, dw = tt.lmhead_token_logprob_bwd(hid, W, y, lse, ent, dlogp=dlogp, dentropy=dent, err=err)
+    dO = dh.view(N, hq, d)
+    dq, dk, dv = tt.tree_attn_bwd(tree, q, k, v, O, LSE, dO, err=err)
+    dqr, dkr = tt.rope_bwd(dq, dk, pos, **how)
+    torch.cuda.synchronize()
+    tree.check()
+    assert int(err.item()) == 0
+
+    pn = pos.cpu().numpy().reshape(axes, N)
+    axis = np.zeros(32, int) if axes == 1 else R.axis_of((12, 10, 10))
+    freq = 10000.0 ** (-np.arange(32) / 32)
+    rq, rk = R.rope(dev_to_f64(qr), pn, axis, freq), R.rope(dev_to_f64(kr), pn, axis, freq)
+    rO, _, _, _, _ = A.tree_attention_branches(tab, rq, rk, dev_to_f64(v), np.zeros((N, hq, d)))
+    z = LH.logits(rO.reshape(N, -1), dev_to_f64(W))
+    r_logp, r_ent, _, _, _ = TL.token_logprob(z, y.cpu().numpy())
+    # O is within 2^-8 of its size (bf16 Q, K and O): z, a sum over 256 such terms with |W| ~ 0.1, within 0.02
+    assert np.abs(dev_to_f64(logp) - r_logp).max() <= 0.04 and np.abs(dev_to_f64(ent) - r_ent).max() <= 0.04
+    dz = TL.token_logprob_grad(z, y.cpu().numpy(), dev_to_f64(dlogp), dev_to_f64(dent))
+    r_dh = dz @ dev_to_f64(W)
+    _, _, r_dq, r_dk, r_dv = A.tree_attention_branches(tab, rq, rk, dev_to_f64(v), r_dh.reshape(N, hq, d))
+    # each stage rounds to bf16 (2^-8): four of them lie between the inputs and dq, dk
+    for got, ref in ((dh, r_dh), (dw, dz.T @ rO.reshape(N, -1)), (dv, r_dv),
+                     (dqr, R.rope(r_dq, pn, axis, freq, inverse=True)), (dkr, R.rope(r_dk, pn, axis, freq, inverse=True))):
+        got = dev_to_f64(got).reshape(ref.shape)
+        assert rel_l2(got, ref) <= 2 * GRAD_RL2, rel_l2(got, ref)
+    # the same objective on stored logits: the fused gradient rounds dz to bf16 as this call does
+    zb = (hid.float() @ W.float().T)
+    lp2, e2, lse2, ids, top = tt.token_logprob(zb, y, top_k=5, err=err)
+    assert (lp2 - logp).abs().max().item() <= 1e-4 and (e2 - ent).abs().max().item() <= 2e-4
+    dzb = tt.token_logprob_bwd(zb, lse2, e2, y, dlogp=dlogp, dentropy=dent, err=err)
+    assert rel_l2(dev_to_f64(dh), dev_to_f64(dzb) @ dev_to_f64(W)) <= GRAD_RL2
+    assert int(err.item()) == 0

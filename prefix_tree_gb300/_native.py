@@ -7,7 +7,6 @@ missing libtt.so raises immediately.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -223,12 +222,35 @@ def tree_schedules(tree: Tree) -> dict:
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # TT_DT_*
 
 
-def _on(t, *others):
-    """Context that makes t's device current; the other tensors must be on it."""
+# The raw current stream of a device: a tenth of the cost of a torch.cuda.Stream object, which is
+# a good part of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _device_of(t, *others):
+    """Ordinal of t's device; the other tensors must be on it."""
+    index = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != index:
             raise ValueError(f"tensors on {t.device} and {o.device}")
-    return torch.cuda.device(t.device) if t.device.index != torch.cuda.current_device() else contextlib.nullcontext()
+    return index
+
+
+def _call(what, index, *args):
+    """A C call on the current stream (its last argument) of device `index`, with that device current."""
+    fn = getattr(_LIB or lib(), what)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != TT_OK:
+        raise TTError(rc, what)
 
 
 @functools.lru_cache(maxsize=64)
@@ -248,12 +270,16 @@ def _rope_tables(rot, sections, interleaved, base, inv_freq):
 
 
 def _rope_rows(t, name):
+    """(N, heads, d, elements between tokens) of a tensor of heads."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 3:
         raise TypeError(f"{name} must be a 3-D bf16, fp16 or fp32 CUDA tensor [N, heads, d]")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    if t.is_contiguous():
+        return n, h, d, h * d
+    ld, hd, one = t.stride()
+    if (d > 1 and one != 1) or (h > 1 and hd != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return n, h, d, ld if n > 1 else h * d
 
 
 def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjacent=False, base=10000.0, inv_freq=None,
@@ -265,20 +291,18 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
     or `inv_freq` (rot_dim/2 numbers). `sections`: how many frequencies each axis takes, one after the other or,
     `interleaved`, the axes in turn while their section lasts. q and k may be views of one buffer (tokens any stride
     apart); `out` = (q_out, k_out) may be (q, k). `inverse` turns back."""
-    q_ld = _rope_rows(q, "q")
-    N, hq, d = q.shape
-    hkv, k_ld = 0, 0
+    N, hq, d, q_ld = _rope_rows(q, "q")
+    hkv = k_ld = 0
     if k is not None:
-        k_ld = _rope_rows(k, "k")
-        hkv = k.shape[1]
-        if k.dtype != q.dtype or k.shape[0] != N or k.shape[2] != d:
+        nk, hkv, dk, k_ld = _rope_rows(k, "k")
+        if k.dtype != q.dtype or nk != N or dk != d:
             raise ValueError("q and k must share type, tokens and head dimension")
     if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32:
         raise TypeError("positions must be an int32 CUDA tensor")
-    pos = positions[None] if positions.dim() == 1 else positions
-    if pos.dim() != 2 or pos.shape[1] != N or (N > 1 and pos.stride(1) != 1):
+    many = positions.dim() == 2
+    axes = positions.shape[0] if many else 1
+    if positions.dim() > 2 or positions.dim() == 0 or positions.shape[-1] != N or (N > 1 and positions.stride(-1) != 1):
         raise ValueError("positions must be [N] or [axes, N] with contiguous tokens")
-    axes = pos.shape[0]
     rot = d if rot_dim is None else int(rot_dim)
     if rot < 2 or rot > d or rot % 2:
         raise ValueError("rot_dim must be even and in 2 .. d")
@@ -291,21 +315,19 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
     axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base),
                               None if inv_freq is None else tuple(float(f) for f in inv_freq))
     if out is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        qo = torch.empty((N, hq, d), dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty((N, hkv, d), dtype=q.dtype, device=q.device)
         qo_ld, ko_ld = hq * d, hkv * d
     else:
         qo, ko = out
         if qo.shape != q.shape or qo.dtype != q.dtype or (ko is None) != (k is None) or \
                 (k is not None and (ko.shape != k.shape or ko.dtype != k.dtype)):
             raise ValueError("out must have the shapes and type of q and k")
-        qo_ld = _rope_rows(qo, "q_out")
-        ko_ld = 0 if ko is None else _rope_rows(ko, "k_out")
-    with _on(q, k, pos, qo, ko):
-        rc = lib().tt_rope(_p(q), _p(qo), q_ld, qo_ld, _p(k), _p(ko), k_ld, ko_ld, _DTYPES[q.dtype], N, hq, hkv, d, rot,
-                           _p(pos), pos.stride(0), axes, axis, freq, int(bool(adjacent)), int(bool(inverse)),
-                           _stream(q.device))
-    _check(rc, "tt_rope")
+        qo_ld = _rope_rows(qo, "q_out")[3]
+        ko_ld = 0 if ko is None else _rope_rows(ko, "k_out")[3]
+    _call("tt_rope", _device_of(q, k, positions, qo, ko), q.data_ptr(), qo.data_ptr(), q_ld, qo_ld, _ptr(k), _ptr(ko),
+          k_ld, ko_ld, _DTYPES[q.dtype], N, hq, hkv, d, rot, positions.data_ptr(), positions.stride(0) if many else N,
+          axes, axis, freq, 1 if adjacent else 0, 1 if inverse else 0)
     return qo, ko
 
 
@@ -579,17 +601,22 @@ def _logit_rows(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D bf16, fp16 or fp32 CUDA tensor")
     N, V = t.shape
-    ld = t.stride(0) if N > 1 else V
-    if (V > 1 and t.stride(1) != 1) or ld < V:
+    if t.is_contiguous():
+        return N, V, V
+    ld, one = t.stride()
+    if N <= 1:
+        ld = V
+    if (V > 1 and one != 1) or ld < V:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1, stride(0) >= V)")
     return N, V, ld
 
 
 def _per_row(t, dtype, name, shape):
     if t is not None:
-        _need(t, dtype, name, len(shape))
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}")
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+            raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and have shape {tuple(shape)}")
 
 
 def token_logprob(logits, targets=None, top_k=0, out=None, err=None):
@@ -597,24 +624,24 @@ def token_logprob(logits, targets=None, top_k=0, out=None, err=None):
     tt_token_logprob: fp32 [N] each, and int32 / fp32 [N, top_k] of the top alternatives. logp is None without
     targets, top_ids and top_logp are None with top_k = 0."""
     N, V, ld = _logit_rows(logits, "logits")
-    _per_row(targets, torch.int32, "targets", (N,))
-    dev, k = logits.device, int(top_k)
+    rows, dev, k = (N,), logits.device, int(top_k)
+    _per_row(targets, torch.int32, "targets", rows)
     if out is None:
-        f = torch.empty(3, N, dtype=torch.float32, device=dev)
-        logp, entropy, lse = (f[0] if targets is not None else None), f[1], f[2]
-        ids = torch.empty(N, k, dtype=torch.int32, device=dev) if k > 0 else None
-        top = torch.empty(N, k, dtype=torch.float32, device=dev) if k > 0 else None
+        logp, entropy, lse = torch.empty((3, N), dtype=torch.float32, device=dev).unbind(0)
+        if targets is None:
+            logp = None
+        ids = torch.empty((N, k), dtype=torch.int32, device=dev) if k > 0 else None
+        top = torch.empty((N, k), dtype=torch.float32, device=dev) if k > 0 else None
     else:
         logp, entropy, lse, ids, top = out
         for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
-            _per_row(t, torch.float32, n, (N,))
+            _per_row(t, torch.float32, n, rows)
         _per_row(ids, torch.int32, "top_ids", (N, k))
         _per_row(top, torch.float32, "top_logp", (N, k))
     err = new_err(dev) if err is None else err
-    with _on(logits, targets, logp, entropy, lse, ids, top, err):
-        rc = lib().tt_token_logprob(_p(logits), _DTYPES[logits.dtype], N, V, ld, _p(targets), k, _p(logp), _p(entropy),
-                                    _p(lse), _p(ids), _p(top), _p(err), _stream(dev))
-    _check(rc, "tt_token_logprob")
+    _call("tt_token_logprob", _device_of(logits, targets, logp, entropy, lse, ids, top, err), logits.data_ptr(),
+          _DTYPES[logits.dtype], N, V, ld, _ptr(targets), k, _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(ids), _ptr(top),
+          err.data_ptr())
     return logp, entropy, lse, ids, top
 
 
@@ -624,25 +651,29 @@ def token_logprob_bwd(logits, lse, entropy=None, targets=None, dlogp=None, dentr
     are dlogp, dentropy, dlse [N] and dtop [N, k] (log-probs of top_ids), each optional (tt_token_logprob_bwd). `out`
     may be logits itself, which is then overwritten."""
     N, V, ld = _logit_rows(logits, "logits")
-    _per_row(targets, torch.int32, "targets", (N,))
+    rows = (N,)
+    _need(lse, torch.float32, "lse", 1)
+    _per_row(targets, torch.int32, "targets", rows)
     for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
-        _per_row(t, torch.float32, n, (N,))
+        _per_row(t, torch.float32, n, rows)
     if (top_ids is None) != (dtop is None):
         raise ValueError("top_ids and dtop go together")
-    k = 0 if dtop is None else dtop.shape[-1]
-    _per_row(top_ids, torch.int32, "top_ids", (N, k))
-    _per_row(dtop, torch.float32, "dtop", (N, k))
-    dev = logits.device
+    k = 0
+    if dtop is not None:
+        k = dtop.shape[-1]
+        _per_row(top_ids, torch.int32, "top_ids", (N, k))
+        _per_row(dtop, torch.float32, "dtop", (N, k))
     if out is None:
-        out = torch.empty(N, ld, dtype=logits.dtype, device=dev)[:, :V]
-    elif out.dtype != logits.dtype or out.shape != logits.shape or (N > 1 and out.stride() != logits.stride()):
+        out = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)
+        if ld != V:
+            out = out[:, :V]
+    elif out.dtype != logits.dtype or out.shape != logits.shape or (N > 1 and out.stride() != logits.stride()) or \
+            (V > 1 and out.stride(1) != 1):
         raise ValueError("out must have the type, shape and strides of logits")
-    err = new_err(dev) if err is None else err
-    with _on(logits, lse, entropy, targets, dlogp, dentropy, dlse, top_ids, dtop, out, err):
-        rc = lib().tt_token_logprob_bwd(_p(logits), _DTYPES[logits.dtype], N, V, ld, _p(lse), _p(entropy), _p(targets),
-                                        _p(dlogp), _p(dentropy), _p(dlse), _p(top_ids), _p(dtop), k, _p(out), _p(err),
-                                        _stream(dev))
-    _check(rc, "tt_token_logprob_bwd")
+    err = new_err(logits.device) if err is None else err
+    _call("tt_token_logprob_bwd", _device_of(logits, lse, entropy, targets, dlogp, dentropy, dlse, top_ids, dtop, out, err),
+          logits.data_ptr(), _DTYPES[logits.dtype], N, V, ld, _ptr(lse), _ptr(entropy), _ptr(targets), _ptr(dlogp),
+          _ptr(dentropy), _ptr(dlse), _ptr(top_ids), _ptr(dtop), k, out.data_ptr(), err.data_ptr())
     return out
 
 
@@ -716,7 +747,7 @@ def lmhead_token_logprob(hidden, w_vocab, targets, out=None, ws=None, err=None):
     N, V, Hd = _lmhead_args(hidden, w_vocab, targets)
     dev = hidden.device
     if out is None:
-        out = tuple(torch.empty(3, N, dtype=torch.float32, device=dev))
+        out = torch.empty((3, N), dtype=torch.float32, device=dev).unbind(0)
     logp, entropy, lse = out
     for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
         _need(t, torch.float32, n, 1)
@@ -724,10 +755,9 @@ def lmhead_token_logprob(hidden, w_vocab, targets, out=None, ws=None, err=None):
     if ws is None:
         ws = torch.empty(lib().tt_lmhead_token_logprob_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
     err = new_err(dev) if err is None else err
-    with _on(hidden, w_vocab, targets, logp, entropy, lse, ws, err):
-        rc = lib().tt_lmhead_token_logprob(_p(hidden), _p(w_vocab), N, V, Hd, _p(targets), _p(logp), _p(entropy),
-                                           _p(lse), _p(ws), ws.numel() * ws.element_size(), _p(err), _stream(dev))
-    _check(rc, "tt_lmhead_token_logprob")
+    _call("tt_lmhead_token_logprob", _device_of(hidden, w_vocab, targets, logp, entropy, lse, ws, err),
+          hidden.data_ptr(), w_vocab.data_ptr(), N, V, Hd, targets.data_ptr(), logp.data_ptr(), entropy.data_ptr(),
+          lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr())
     return logp, entropy, lse
 
 
@@ -753,11 +783,11 @@ def lmhead_token_logprob_bwd(hidden, w_vocab, targets, lse, entropy=None, dlogp=
     if ws is None:
         ws = torch.empty(lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
     err = new_err(dev) if err is None else err
-    with _on(hidden, w_vocab, targets, lse, entropy, dlogp, dentropy, dlse, dh, dw, ws, err):
-        rc = lib().tt_lmhead_token_logprob_bwd(_p(hidden), _p(w_vocab), N, V, Hd, _p(targets), _p(lse), _p(entropy),
-                                               _p(dlogp), _p(dentropy), _p(dlse), _p(dh), _p(dw), _DTYPES[dw.dtype],
-                                               _p(ws), ws.numel() * ws.element_size(), _p(err), _stream(dev))
-    _check(rc, "tt_lmhead_token_logprob_bwd")
+    _call("tt_lmhead_token_logprob_bwd",
+          _device_of(hidden, w_vocab, targets, lse, entropy, dlogp, dentropy, dlse, dh, dw, ws, err), hidden.data_ptr(),
+          w_vocab.data_ptr(), N, V, Hd, targets.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
+          _ptr(dlse), dh.data_ptr(), dw.data_ptr(), _DTYPES[dw.dtype], ws.data_ptr(), ws.numel() * ws.element_size(),
+          err.data_ptr())
     return dh, dw
 
 

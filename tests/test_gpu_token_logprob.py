@@ -99,6 +99,43 @@ def test_ties_go_to_the_lower_index(tt, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N,V,stride", [(4, 40009, 256), (700, 4003, 32)])
+def test_best_logits_in_few_places(tt, dtype, N, V, stride):
+    """The best logits crowd into a few 16-byte vectors of every `stride`-th, in ascending, descending and random
+    order: far more candidates than alternatives."""
+    rng = np.random.default_rng(V)
+    vn = 4 if dtype == "fp32" else 8
+    vec = np.arange(V) // vn
+    x = -1.0 - rng.random((N, V))
+    crowd = vec % stride < 3
+    n = int(crowd.sum())
+    for i in range(min(N, 8)):
+        v = rng.permutation(n) if i % 3 == 0 else np.arange(n) if i % 3 == 1 else np.arange(n)[::-1]
+        x[i, crowd] = v // (1 + i // 3)
+    x[N - 1] = -5.0
+    x[N - 1, crowd] = 1.0
+    _check_fwd(tt, _logits(x, dtype), None, 32)
+    _check_fwd(tt, _logits(x[:5], dtype), None, 5)
+
+
+def test_very_long_rows(tt):
+    """More vectors to a slice than 16 bits count, one CTA to a row: ties, and two rows against the oracle."""
+    N, V = 153, 530003
+    g = torch.Generator(device="cuda").manual_seed(0)
+    z = torch.randn(N, V, generator=g, device="cuda").to(torch.bfloat16)
+    z[1] = 0.25
+    z[1, V - 1] = 0.5
+    z[N - 1, 500000:] = 9.0
+    logp, h, lse, ids, top = tt.token_logprob(z, top_k=20)
+    for r in (0, 1, N - 1):
+        _, rh, rl, ri, rt = TL.token_logprob(_f64(z[r:r + 1]), None, 20)
+        assert ids[r].tolist() == ri[0].tolist()
+        # 2071 terms a thread instead of 1024 (see _check_fwd)
+        assert abs(lse[r].item() - rl[0]) <= 2e-4 and np.abs(_f64(top[r]) - rt[0]).max() <= 2e-4
+        assert abs(h[r].item() - rh[0]) <= 2e-4 * (1 + abs(rl[0] - z[r].float().max().item() - rh[0]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_masks_and_extremes(tt, dtype):
     rng = np.random.default_rng(1)
     N, V = 12, 3001

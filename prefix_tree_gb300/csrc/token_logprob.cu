@@ -6,14 +6,15 @@
 // (S >= 1 and U <= 0: the two terms of H have one sign, nothing cancels).
 //
 // Forward: one pass over the row. A thread takes 16-byte vectors and folds
-// them into (m, s, u) with a running maximum; beside it it keeps the vector
-// that holds its largest logit. The k largest logits of the row all lie with
-// the k threads whose largest (value, position) are the row's k best: a
-// thread outside them has k better elements elsewhere for each of its own.
-// So the top alternatives cost the pass one comparison per vector; after it a
-// lower bound of the k-th best of the threads' best is taken, and only the
-// elements of the threads that reach it, little more than k/threads of the
-// row, are read again: those that reach the bound are gathered and sorted.
+// them into (m, s, u) with a running maximum. Over the first part of the row
+// it also keeps the vector that holds its largest logit: the k largest logits
+// of that part lie with the k threads whose largest (value, position) are its
+// k best, since a thread outside them has k better elements elsewhere for each
+// of its own. So after that part a lower bound of the row's k-th best is
+// known; the elements of the few threads that reach it are read again (from
+// the L2 cache) and kept where they reach it, and over the rest of the row
+// whatever exceeds it is kept as it passes: one comparison per vector. What
+// was kept, a few times k, is sorted at the end.
 //
 // Backward: dz_v = p_v·(g_lse − G − g_H·(logp_v + H)) + g_logp·[v = y] + Σ_j g_top_j·[v = id_j],
 // with G = g_logp + Σ_j g_top_j: one read and one write of the row.
@@ -33,8 +34,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // and 0·d stays 0 for a masked logit (d = -inf).
 constexpr float kFloor = -128.f;
 constexpr int kTopMax = 32;
-constexpr int kBlock = 256;
-constexpr int kWarpRow = 512;  // vectors of a row up to which a warp takes a row of its own
+constexpr int kMostCtas = 8;   // CTAs to a row: the portable cluster size
+// A row's first part, for the bound on its alternatives: one in so many. A smaller part makes the bound on the rest
+// looser (candidates kept: k times this), a larger one has more to read again.
+constexpr int kFirstPart = 4;
+// Threads of a block: a group of WARPS warps, or eight groups of one.
+template <int WARPS>
+constexpr int kBlockOf = WARPS == 1 ? 256 : 32 * WARPS;
 
 typedef unsigned long long u64;
 
@@ -46,7 +52,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // ------------------------------------------------------------------ 16-byte vectors of a row
-// Element pairs of a 16-byte vector as floats, and its packed maximum.
+// A 16-byte vector's elements as floats: pair i, element i, the largest one,
+// and raise(): every element at least the type's lowest finite value (a NaN
+// stays).
 template <typename T>
 struct Pairs;
 template <>
@@ -56,34 +64,62 @@ struct Pairs<float> {
     return i ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w))
              : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
   }
+  static __device__ __forceinline__ float element(const uint4& u, int i) {
+    return __uint_as_float(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w);
+  }
   static __device__ __forceinline__ float max(const uint4& u) {
     return fmaxf(tc::fmax3f(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z)), __uint_as_float(u.w));
   }
+  static __device__ __forceinline__ float max(const uint4& a, const uint4& b, const uint4& c, const uint4& d) {
+    return fmaxf(tc::fmax3f(max(a), max(b), max(c)), max(d));
+  }
+};
+// The two 16-bit types: W = the packed pair.
+template <typename W>
+struct PackedPairs {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ uint32_t word(const uint4& u, int i) {
+    return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+  }
+  static __device__ __forceinline__ W packed(uint32_t w) { return *reinterpret_cast<const W*>(&w); }
+  static __device__ __forceinline__ W max2(const uint4& u) {
+    return __hmax2(__hmax2(packed(u.x), packed(u.y)), __hmax2(packed(u.z), packed(u.w)));
+  }
+  static __device__ __forceinline__ float max(const uint4& u) {
+    const W m = max2(u);
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ float max(const uint4& a, const uint4& b, const uint4& c, const uint4& d) {
+    const W m = __hmax2(__hmax2(max2(a), max2(b)), __hmax2(max2(c), max2(d)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ uint32_t raise(uint32_t w, uint32_t low2) {
+    const W m = __hmax2_nan(packed(w), packed(low2));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
 };
 template <>
-struct Pairs<__nv_bfloat16> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ float2 get(const uint4& u, int i) {
-    const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+struct Pairs<__nv_bfloat16> : PackedPairs<__nv_bfloat162> {
+  static constexpr uint32_t kLow2 = 0xff7fff7fu;      // the lowest finite value, twice
+  static constexpr float kPlainLow = -1e38f, kPlainHigh = 1e36f;
+  static __device__ __forceinline__ float2 floats(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  static __device__ __forceinline__ float max(const uint4& u) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+  static __device__ __forceinline__ float2 get(const uint4& u, int i) { return floats(word(u, i)); }
+  static __device__ __forceinline__ float element(const uint4& u, int i) {
+    const float2 p = get(u, i >> 1);
+    return i & 1 ? p.y : p.x;
   }
 };
 template <>
-struct Pairs<__half> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ float2 get(const uint4& u, int i) {
-    const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  }
-  static __device__ __forceinline__ float max(const uint4& u) {
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
-    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+struct Pairs<__half> : PackedPairs<__half2> {
+  static constexpr uint32_t kLow2 = 0xfbfffbffu;
+  static constexpr float kPlainLow = -65000.f, kPlainHigh = INFINITY;
+  static __device__ __forceinline__ float2 floats(uint32_t w) { return __half22float2(packed(w)); }
+  static __device__ __forceinline__ float2 get(const uint4& u, int i) { return floats(word(u, i)); }
+  static __device__ __forceinline__ float element(const uint4& u, int i) {
+    const float2 p = get(u, i >> 1);
+    return i & 1 ? p.y : p.x;
   }
 };
 
@@ -202,69 +238,151 @@ __device__ __forceinline__ void merge(Stat& a, Stat b) {
 // Vectors that a thread folds in at once: one rescaling for all of them.
 constexpr int kBatch = 4;
 
-// Folds kBatch vectors (bm: their largest element) into t.
+// Masked logits (-inf) must add 0 to Σ d·e^d, not 0·(-inf). The plain way of a 16-bit type raises them to the type's
+// lowest finite value first, two elements in one instruction: d stays finite and e^d is 0, unless the row's maximum is
+// itself near the lowest value (then the two must be told apart) or so high that d overflows. Such rows, known by their
+// maximum at the end, are taken again the wide way, which bounds every d (as fp32 rows always are: two instructions for
+// two elements, and half as many elements to the byte).
 template <typename T>
-__device__ __forceinline__ void fold(Stat& t, const uint4 (&u)[kBatch], float bm) {
-  rescale(t, fmaxf(t.m, bm));
-  const float mb = t.m == -INFINITY ? 0.f : t.m;
-  const float2 nm = make_float2(-mb, -mb), l2 = make_float2(kLog2e, kLog2e);
-  float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
+__device__ __forceinline__ bool plain_way_holds(float m) {
+  if constexpr (sizeof(T) == 4) return true;
+  else return (m > Pairs<T>::kPlainLow && m < Pairs<T>::kPlainHigh) || m == -INFINITY;
+}
+// (A maximum of -inf: nothing but masked logits, or NaN; raised logits would give S > 0.)
+
+// Adds one vector to the sums s, q = Σ e^d, Σ d·e^d around nm = −(reference), l2 = log2 e.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void fold(float2& s, float2& q, const uint4& u, float2 nm, float2 l2) {
 #pragma unroll
-  for (int v = 0; v < kBatch; ++v)
-#pragma unroll
-    for (int i = 0; i < Pairs<T>::N; ++i) {
-      float2 d = __fadd2_rn(Pairs<T>::get(u[v], i), nm);
-      d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
-      const float2 x = __fmul2_rn(d, l2);
-      const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-      s = __fadd2_rn(s, e);
-      q = __ffma2_rn(e, d, q);
-    }
-  t.s += s.x + s.y;
-  t.u += q.x + q.y;
+  for (int i = 0; i < Pairs<T>::N; ++i) {
+    float2 x;
+    if constexpr (WIDE || sizeof(T) == 4)
+      x = Pairs<T>::get(u, i);
+    else
+      x = Pairs<T>::floats(Pairs<T>::raise(Pairs<T>::word(u, i), Pairs<T>::kLow2));
+    float2 d = __fadd2_rn(x, nm);
+    if constexpr (WIDE || sizeof(T) == 4) d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
+    const float2 t = __fmul2_rn(d, l2);
+    const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+    s = __fadd2_rn(s, e);
+    q = __ffma2_rn(e, d, q);
+  }
 }
 
-// One thread's share of vectors lo + tid, lo + tid + kGroup, ... < hi; with TOP also its largest logit and the (first)
-// vector that holds it.
-template <typename T, int kGroup, bool TOP>
-__device__ __forceinline__ Stat scan(const Row<T>& z, int lo, int hi, int tid, float& best, int& best_j) {
-  Stat t = {-INFINITY, 0.f, 0.f};
-  best = -INFINITY;
-  best_j = lo + tid;
-  const T none = static_cast<T>(-INFINITY);
-  uint4 pad;
+constexpr int kDepth = 2;  // batches of a thread on their way from memory or in use (3 and 4 took as long)
+
+// Shared memory that a group's vectors pass through: each thread its own places, so no thread waits for another.
+template <int WARPS>
+struct Ring {
+  uint4 at[kDepth][kBatch][WARPS * 32];
+};
+
+// One thread's way over vectors lo + tid, lo + tid + kGroup, ... < hi of a row, kBatch at a time, through asynchronous
+// copies kDepth − 1 batches ahead.
+template <typename T, int WARPS>
+struct Scan {
+  static constexpr int kGroup = WARPS * 32, kD = kDepth;
+  const Row<T>& z;
+  Ring<WARPS>& ring;
+  const int hi, wlo, whi, tid;
+  int j, stage;
+  Stat t;
+  float best;  // largest logit of the batches taken with TRACK, and the first vector that holds it
+  int best_j;
+
+  __device__ __forceinline__ Scan(const Row<T>& z_, Ring<WARPS>& ring_, int lo, int hi_, int tid_)
+      : z(z_), ring(ring_), hi(hi_), wlo(z_.whole_lo()), whi(min(hi_, z_.whole_hi())), tid(tid_), j(lo + tid_), stage(0),
+        t{-INFINITY, 0.f, 0.f}, best(-INFINITY), best_j(lo + tid_) {
 #pragma unroll
-  for (int i = 0; i < Row<T>::VN; ++i) reinterpret_cast<T*>(&pad)[i] = none;
-  const int wlo = z.whole_lo(), whi = min(hi, z.whole_hi());
-  auto load = [&](int j, uint4(&u)[kBatch]) {
-    if (j >= wlo && j + (kBatch - 1) * kGroup < whi) {
+    for (int d = 0; d < kD - 1; ++d) fetch(j + d * kBatch * kGroup, d);
+  }
+  // Starts the batch at vector `at` on its way into `st`.
+  __device__ __forceinline__ void fetch(int at, int st) {
+    if (at >= wlo && at + (kBatch - 1) * kGroup < whi) {
 #pragma unroll
-      for (int v = 0; v < kBatch; ++v) u[v] = z.load_whole(j + v * kGroup);
+      for (int v = 0; v < kBatch; ++v)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring.at[st][v][tid])),
+                     "l"(z.p + z.first(at + v * kGroup))
+                     : "memory");
     } else {
+      uint4 pad;
 #pragma unroll
-      for (int v = 0; v < kBatch; ++v) u[v] = j + v * kGroup < hi ? z.load(j + v * kGroup) : pad;
+      for (int i = 0; i < Row<T>::VN; ++i) reinterpret_cast<T*>(&pad)[i] = static_cast<T>(-INFINITY);
+#pragma unroll
+      for (int v = 0; v < kBatch; ++v) ring.at[st][v][tid] = at + v * kGroup < hi ? z.load(at + v * kGroup) : pad;
     }
-  };
-  uint4 cur[kBatch], next[kBatch];
-  int j = lo + tid;
-  if (j < hi) load(j, cur);
-  while (j < hi) {
-    const int jn = j + kBatch * kGroup;
-    if (jn < hi) load(jn, next);
-    float bm = -INFINITY;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // The batches before vector `end` (all the thread's with end = hi). The lanes of a warp stay together (those past the
+  // end take masked logits). With OVER, over(src) is called by the whole warp for each lane src whose batch has a logit
+  // above `above`.
+  template <bool TRACK, bool OVER, typename F>
+  __device__ __forceinline__ void take(int end, float above, F over) {
+    const int lane = threadIdx.x & 31;
+    while (j - lane < end) {
+      const int ahead = stage == 0 ? kD - 1 : stage - 1;
+      fetch(j + (kD - 1) * kBatch * kGroup, ahead);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
+      uint4 u[kBatch];
 #pragma unroll
-    for (int v = 0; v < kBatch; ++v) {
-      const float vm = Pairs<T>::max(cur[v]);
-      if (TOP && vm > best) {
-        best = vm;
-        best_j = j + v * kGroup;
+      for (int v = 0; v < kBatch; ++v) u[v] = ring.at[stage][v][tid];
+      float bm;
+      if (TRACK) {
+        bm = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < kBatch; ++v) {
+          const float vm = Pairs<T>::max(u[v]);
+          if (vm > best) {
+            best = vm;
+            best_j = j + v * kGroup;
+          }
+          bm = fmaxf(bm, vm);
+        }
+      } else {
+        static_assert(kBatch == 4, "four vectors");
+        bm = Pairs<T>::max(u[0], u[1], u[2], u[3]);
       }
-      bm = fmaxf(bm, vm);
-    }
-    fold<T>(t, cur, bm);
+      if (OVER) {
+        uint32_t m = __ballot_sync(kAll, bm > above);
+        if (m) {
+          __syncwarp();  // the lanes' copies are there for the warp
+          do {
+            over(__ffs(m) - 1);
+            m &= m - 1;
+          } while (m);
+          __syncwarp();
+        }
+      }
+      rescale(t, fmaxf(t.m, bm));
+      const float mb = t.m == -INFINITY ? 0.f : t.m;
+      const float2 nm = make_float2(-mb, -mb), l2 = make_float2(kLog2e, kLog2e);
+      float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < kBatch; ++v) cur[v] = next[v];
-    j = jn;
+      for (int v = 0; v < kBatch; ++v) fold<T, false>(s, q, u[v], nm, l2);
+      t.s += s.x + s.y;
+      t.u += q.x + q.y;
+      j += kBatch * kGroup;
+      stage = stage == kD - 1 ? 0 : stage + 1;
+    }
+  }
+  template <bool TRACK>
+  __device__ __forceinline__ void take_all() {
+    take<TRACK, false>(hi, 0.f, [](int) {});
+  }
+};
+
+// The sums of a thread's vectors taken again the wide way.
+template <typename T, int WARPS>
+__device__ __noinline__ Stat wide_sums(const Row<T>& z, int lo, int hi, int tid) {
+  Stat t = {-INFINITY, 0.f, 0.f};
+  for (int j = lo + tid; j < hi; j += WARPS * 32) {
+    const uint4 u = z.load(j);
+    rescale(t, fmaxf(t.m, Pairs<T>::max(u)));
+    const float mb = t.m == -INFINITY ? 0.f : t.m;
+    float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
+    fold<T, true>(s, q, u, make_float2(-mb, -mb), make_float2(kLog2e, kLog2e));
+    t.s += s.x + s.y;
+    t.u += q.x + q.y;
   }
   return t;
 }
@@ -300,13 +418,19 @@ struct FwdArgs {
 template <int WARPS>
 struct TopShared {
   static constexpr int kGroup = WARPS * 32;
-  static constexpr int kRounds = 8;                   // most of a warp's best that enter the bound
-  static constexpr int kRoom = WARPS == 1 ? 64 : 32 * WARPS;  // candidates kept
-  uint32_t bests[WARPS == 1 ? 1 : WARPS * kRounds];
+  static constexpr int kEntries = 64;                        // most of the warps' best that enter the bound
+  static constexpr int kLists = WARPS < 4 ? 4 : 2 * WARPS;   // candidates are sorted 32 at a time
+  static constexpr int kRoom = 32 * kLists;                  // candidates kept
+  uint32_t bests[WARPS == 1 ? 1 : kEntries];
   uint32_t bound;
-  int chosen, found;  // entries of `threads` and candidates found (possibly more than kRoom)
+  int chosen, found;  // entries of `threads`, and candidates found (possibly more than kRoom)
   uint16_t threads[kGroup];
   u64 keys[kRoom];
+
+  __device__ __forceinline__ void keep(u64 key) {
+    const int at = atomicAdd(&found, 1);
+    if (at < kRoom) keys[at] = key;
+  }
 };
 
 template <int WARPS>
@@ -330,21 +454,17 @@ __device__ __forceinline__ uint32_t sort_warp32(uint32_t key, int lane) {
   return key;
 }
 
-// The k largest logits of vectors [lo, hi) as keys, lane i of warp 0 the i-th (0 = none; other warps: unspecified).
-// best, best_j: the thread's from scan(). Every thread of the group takes part.
+// A lower bound of the k-th largest key (value, element) of vectors [lo, hi), 0 if there are fewer than k elements'
+// worth; best, best_j: the thread's from a Scan over them. Lists the threads that reach it in sh.threads and clears
+// sh.found. Every thread of the group takes part.
 //
-// 1. A 32-bit key of every thread's best (16-bit types: value and vector, so that ties count by position; fp32: the
-//    value alone), 0 = none. A lower bound of the k-th largest of them: the k-th largest of each warp's first few
-//    (exact unless one warp holds more than that many of the k; 4 to a warp for k <= 16, else 8: at least k values).
-// 2. The threads that reach the bound; their vectors, spread over the whole group, are read again, and the elements
-//    that reach it are gathered.
-// 3. More candidates than there is room for (long ties, or rows laid out against the threads): the k-th best of those
-//    kept is a higher bound; read again with it. Each time at least kRoom − k >= 32 candidates fall away.
+// A 32-bit key of every thread's best (16-bit types: value and vector, so that ties count by position; fp32: the value
+// alone), 0 = none. Of these, the k-th largest of each warp's first few, 2·k or more in all: exact unless one warp
+// holds more than its share of the k.
 template <typename T, int WARPS>
-__device__ __forceinline__ u64 top_of_slice(TopShared<WARPS>& sh, const Row<T>& z, int lo, int hi, int tid, int k,
-                                            float best, int best_j) {
+__device__ __forceinline__ u64 bound_of(TopShared<WARPS>& sh, const Row<T>& z, int lo, int hi, int tid, int k,
+                                        float best, int best_j) {
   using S = TopShared<WARPS>;
-  constexpr int VN = Row<T>::VN;
   const int lane = tid & 31, warp = tid >> 5;
   const bool has = lo + tid < hi, by_place = sizeof(T) == 2 && hi - lo <= 65536;
   uint32_t mine = 0;
@@ -360,7 +480,7 @@ __device__ __forceinline__ u64 top_of_slice(TopShared<WARPS>& sh, const Row<T>& 
     bound = __shfl_sync(kAll, sort_warp32(mine, lane), k - 1);
     __syncwarp();
   } else {
-    const int rounds = k <= 4 * WARPS / 2 ? S::kRounds / 2 : S::kRounds;
+    const int rounds = max(4, (2 * k + WARPS - 1) / WARPS);  // entries of a warp: 64 in all at most
     uint32_t left = mine;
     for (int r = 0; r < rounds; ++r) {
       const uint32_t top = __reduce_max_sync(kAll, left);
@@ -381,77 +501,115 @@ __device__ __forceinline__ u64 top_of_slice(TopShared<WARPS>& sh, const Row<T>& 
     bound = sh.bound;
   }
   if (has && mine >= bound) sh.threads[atomicAdd(&sh.chosen, 1)] = (uint16_t)tid;
-  // the same bound on elements
-  u64 tau = 0;
-  if (bound) {
-    if (sizeof(T) == 4) {
-      tau = (u64)bound << 32;
-    } else {
-      const int j = by_place ? lo + (int)(0xffffu - (bound & 0xffffu)) : z.nvec;  // elements of vector j and before
-      tau = make_key(half_value<T>(bound >> 16), (uint32_t)(z.first(j) + VN - 1));
+  group_sync<WARPS>();
+  if (!bound) return 0;
+  if (sizeof(T) == 4) return (u64)bound << 32;
+  const int j = by_place ? lo + (int)(0xffffu - (bound & 0xffffu)) : z.nvec;  // elements of vector j and before
+  return make_key(half_value<T>(bound >> 16), (uint32_t)(z.first(j) + Row<T>::VN - 1));
+}
+
+// Keeps the elements that reach tau of the batch that lane src is at. The whole warp takes part, a lane to an element.
+template <typename T, int WARPS>
+__device__ __forceinline__ void look(TopShared<WARPS>& sh, const Scan<T, WARPS>& scan, int src, u64 tau) {
+  constexpr int VN = Row<T>::VN;
+  const int lane = threadIdx.x & 31;
+  static_assert(kBatch * VN <= 32, "an element to a lane");
+  if (lane < kBatch * VN) {
+    const int v = lane / VN, i = lane % VN;
+    const int e = scan.z.first(scan.j - lane + src + v * (WARPS * 32)) + i;
+    const T x = reinterpret_cast<const T*>(&scan.ring.at[scan.stage][v][scan.tid - lane + src])[i];
+    const u64 key = make_key(static_cast<float>(x), (uint32_t)e);
+    if (key >= tau && e >= 0 && e < scan.z.V) sh.keep(key);
+  }
+}
+
+// Keeps the elements of vectors [lo, hi) of the listed threads whose keys reach tau.
+template <typename T, int WARPS>
+__device__ __forceinline__ void gather(TopShared<WARPS>& sh, const Row<T>& z, int lo, int hi, int tid, u64 tau) {
+  constexpr int kGroup = WARPS * 32, VN = Row<T>::VN;
+  const int per = (hi - lo + kGroup - 1) / kGroup, all = sh.chosen * per;
+  const float tau_v = tau ? value_of(tau) : -INFINITY;
+  constexpr int kAtOnce = 4;  // loads of a thread under way together
+  for (int f0 = tid; f0 < all; f0 += kAtOnce * kGroup) {
+    uint4 u[kAtOnce];
+    int at[kAtOnce];
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      const int f = f0 + n * kGroup, c = f / per;
+      at[n] = f < all ? lo + sh.threads[c] + (f - c * per) * kGroup : hi;
+      if (at[n] < hi) u[n] = z.load(at[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      if (at[n] >= hi) continue;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < VN; ++i) m |= (Pairs<T>::element(u[n], i) >= tau_v) ? 1u << i : 0u;
+      while (m) {
+        const int i = __ffs(m) - 1, e = z.first(at[n]) + i;
+        m &= m - 1;
+        const u64 key = make_key(Pairs<T>::element(u[n], i), (uint32_t)e);
+        if (key >= tau && e >= 0 && e < z.V) sh.keep(key);
+      }
     }
   }
+}
+
+// The 32 largest of what was kept (after a group_sync), descending over the lanes of warp 0 and, where there was more
+// than one list to sort, in sh.keys.
+template <int WARPS>
+__device__ __forceinline__ u64 sort_kept(TopShared<WARPS>& sh, int tid) {
+  using S = TopShared<WARPS>;
+  const int lane = tid & 31, warp = tid >> 5, kept = min(sh.found, S::kRoom);
+  u64 list = 0;
+  for (int at = 32 * warp; at < kept; at += 32 * WARPS) {
+    const u64 more = sort_warp(at + lane < kept ? sh.keys[at + lane] : 0, lane);
+    list = at == 32 * warp ? more : merge_warp(list, more, lane);
+  }
+  if (WARPS > 1 && kept > 32) {
+    sh.keys[tid] = list;  // each warp's own 32 places
+#pragma unroll
+    for (int w = WARPS / 2; w; w >>= 1) {
+      __syncthreads();
+      if (warp < w) sh.keys[tid] = list = merge_warp(list, sh.keys[tid + 32 * w], lane);
+    }
+    __syncthreads();
+  }
+  return list;
+}
+
+// The k largest logits of vectors [lo, hi), lane i of warp 0 the i-th, wherever they lie: for rows where more reached
+// the bound than there is room for (ascending rows, long ties). The thread's best of the whole slice give a bound that
+// only the elements of its threads can reach; while these are still too many, the k-th best of those kept is a higher
+// one. Each time at least kRoom − k >= 96 candidates fall away.
+template <typename T, int WARPS>
+__device__ __noinline__ u64 top_of_slice(TopShared<WARPS>& sh, const Row<T>& z, Ring<WARPS>& ring, int lo, int hi, int tid,
+                                         int k) {
+  Scan<T, WARPS> scan(z, ring, lo, hi, tid);
+  scan.template take_all<true>();
   group_sync<WARPS>();
-  const int chosen = sh.chosen, per = (hi - lo + S::kGroup - 1) / S::kGroup;
-  u64 list;
+  u64 tau = bound_of<T, WARPS>(sh, z, lo, hi, tid, k, scan.best, scan.best_j);
   for (;;) {
-    const float tau_v = tau ? value_of(tau) : -INFINITY;
-    for (int f = tid; f < chosen * per; f += S::kGroup) {
-      const int c = f / per, j = lo + sh.threads[c] + (f - c * per) * S::kGroup;
-      if (j >= hi) continue;
-      const uint4 u = z.load(j);
-      if (Pairs<T>::max(u) < tau_v) continue;
-      const int e0 = z.first(j);
-#pragma unroll
-      for (int i = 0; i < VN; ++i) {
-        const float2 pair = Pairs<T>::get(u, i / 2);
-        const u64 key = make_key(i & 1 ? pair.y : pair.x, (uint32_t)(e0 + i));
-        if (key >= tau && e0 + i >= 0 && e0 + i < z.V) {
-          const int at = atomicAdd(&sh.found, 1);
-          if (at < S::kRoom) sh.keys[at] = key;
-        }
-      }
-    }
+    gather<T, WARPS>(sh, z, lo, hi, tid, tau);
     group_sync<WARPS>();
-    const int found = sh.found, kept = min(found, S::kRoom);
-    // sort what was kept: 32 to a warp, then the lists joined
-    if constexpr (WARPS == 1) {
-      list = sort_warp(lane < kept ? sh.keys[lane] : 0, lane);
-      if (kept > 32) list = merge_warp(list, sort_warp(32 + lane < kept ? sh.keys[32 + lane] : 0, lane), lane);
-    } else {
-      list = 0;
-      if (32 * warp < kept) list = sort_warp(tid < kept ? sh.keys[tid] : 0, lane);
-      if (kept > 32) {
-        sh.keys[tid] = list;  // each warp's own 32 places
-#pragma unroll
-        for (int w = WARPS / 2; w; w >>= 1) {
-          __syncthreads();
-          if (warp < w) {
-            list = merge_warp(list, sh.keys[tid + 32 * w], lane);
-            sh.keys[tid] = list;
-          }
-        }
-        __syncthreads();
-      }
-    }
-    if (found <= S::kRoom) break;
-    tau = sh.keys[k - 1];
-    if constexpr (WARPS == 1) tau = __shfl_sync(kAll, list, k - 1);
+    const u64 list = sort_kept<WARPS>(sh, tid);
+    if (sh.found <= TopShared<WARPS>::kRoom) return list;
+    tau = WARPS == 1 ? __shfl_sync(kAll, list, k - 1) : sh.keys[k - 1];
     group_sync<WARPS>();
     if (tid == 0) sh.found = 0;
     group_sync<WARPS>();
   }
-  return list;
 }
 
 // A row is taken by a group of WARPS warps of each of the CTAs of a cluster
 // (cluster size 1: one group per row). WARPS = 1: the warps of a block take
 // rows of their own.
 template <typename T, int WARPS, bool TOP>
-__global__ void __launch_bounds__(kBlock) token_logprob_kernel(const FwdArgs a, int CL) {
+__global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_kernel(const FwdArgs a, int CL) {
   constexpr int kGroup = WARPS * 32;
-  constexpr int kGroups = kBlock / kGroup;
-  __shared__ Stat part[kBlock / 32];
+  constexpr int kGroups = kBlockOf<WARPS> / kGroup;
+  __shared__ Stat part[WARPS];
+  __shared__ Ring<WARPS> rings[kGroups];
   __shared__ TopShared<WARPS> top[TOP ? kGroups : 1];
   __shared__ Stat cta_stat;
   __shared__ u64 cta_list[WARPS > 1 && TOP ? 32 : 1];
@@ -460,18 +618,36 @@ __global__ void __launch_bounds__(kBlock) token_logprob_kernel(const FwdArgs a, 
   const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kGroups + warp : (int64_t)(blockIdx.x / CL);
   const int rank = WARPS == 1 ? 0 : (int)(blockIdx.x % CL);
   if (WARPS == 1 && row >= a.N) return;
+  Ring<WARPS>& ring = rings[WARPS == 1 ? warp : 0];
   const Row<T> z(static_cast<const T*>(a.z) + row * a.ld, a.V);
   const int lo = (int)((int64_t)z.nvec * rank / CL), hi = (int)((int64_t)z.nvec * (rank + 1) / CL);
 
-  float best;
-  int best_j;
-  Stat t = join_warp(scan<T, kGroup, TOP>(z, lo, hi, tid, best, best_j), lane);
+  Scan<T, WARPS> scan(z, ring, lo, hi, tid);
   u64 list = 0;  // lane i: the i-th best
-  if (WARPS > 1 && lane == 0) part[warp] = t;
   if constexpr (TOP) {
-    list = top_of_slice<T, WARPS>(top[WARPS == 1 ? warp : 0], z, lo, hi, tid, a.k, best, best_j);
+    TopShared<WARPS>& sh = top[WARPS == 1 ? warp : 0];
+    // the first part: whole rounds of batches
+    constexpr int kRound = kBatch * kGroup;
+    const int parts = (hi - lo) / kRound;
+    const int mid = parts < 2 ? hi : lo + (a.k <= 16 ? (parts + kFirstPart - 1) / kFirstPart : (parts + 1) / 2) * kRound;
+    scan.template take<true, false>(mid, 0.f, [](int) {});
+    const u64 tau = bound_of<T, WARPS>(sh, z, lo, mid, tid, a.k, scan.best, scan.best_j);
+    gather<T, WARPS>(sh, z, lo, mid, tid, tau);
+    // (an equal logit further on comes after the k that are known)
+    scan.template take<false, true>(hi, tau ? value_of(tau) : -INFINITY, [&](int src) {
+      look<T, WARPS>(sh, scan, src, tau);
+    });
   } else {
-    group_sync<WARPS>();
+    scan.template take_all<false>();
+  }
+  Stat t = join_warp(scan.t, lane);
+  if (!plain_way_holds<T>(t.m)) t = join_warp(wide_sums<T, WARPS>(z, lo, hi, tid), lane);
+  if (WARPS > 1 && lane == 0) part[warp] = t;
+  group_sync<WARPS>();
+  if constexpr (TOP) {
+    TopShared<WARPS>& sh = top[WARPS == 1 ? warp : 0];
+    list = sh.found <= TopShared<WARPS>::kRoom ? sort_kept<WARPS>(sh, tid)
+                                               : top_of_slice<T, WARPS>(sh, z, ring, lo, hi, tid, a.k);
   }
   if constexpr (WARPS > 1) {
     if (CL == 1) {
@@ -479,7 +655,7 @@ __global__ void __launch_bounds__(kBlock) token_logprob_kernel(const FwdArgs a, 
       t = part[0];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) merge(t, part[w]);
-    } else {
+    } else if constexpr (WARPS == kMostCtas) {
       cg::cluster_group cluster = cg::this_cluster();
       if (warp == 0) {
         t = part[0];
@@ -490,7 +666,6 @@ __global__ void __launch_bounds__(kBlock) token_logprob_kernel(const FwdArgs a, 
       }
       cluster.sync();
       if (rank == 0) {  // warp r takes CTA r's results; the lists are joined pairwise
-        static_assert(WARPS == 8, "a warp for each CTA of a cluster");
         if (warp < CL) {
           if (lane == 0) part[warp] = *cluster.map_shared_rank(&cta_stat, warp);
           if constexpr (TOP) top[0].keys[tid] = list = cluster.map_shared_rank(cta_list, warp)[lane];
@@ -559,13 +734,13 @@ constexpr float kWideLse = 1024.f;
 // thread each after the slice is written, from logits read before it, so that
 // dz may overwrite z; a CTA reads no slice but its own.
 template <typename T, int WARPS>
-__global__ void __launch_bounds__(kBlock) token_logprob_bwd_kernel(const BwdArgs a, int CL) {
+__global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_bwd_kernel(const BwdArgs a, int CL) {
   constexpr int VN = Row<T>::VN;
   constexpr int kGroup = WARPS * 32;
-  constexpr int kGroups = kBlock / kGroup;
+  constexpr int kGroups = kBlockOf<WARPS> / kGroup;
   __shared__ int all_ids[kGroups][kTopMax + 1];
   __shared__ float all_gs[kGroups][kTopMax + 1];
-  __shared__ Stat part[kBlock / 32];
+  __shared__ Stat part[WARPS];
   __shared__ Stat cta_stat;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tid = WARPS == 1 ? lane : (int)threadIdx.x;
@@ -581,9 +756,7 @@ __global__ void __launch_bounds__(kBlock) token_logprob_bwd_kernel(const BwdArgs
   const bool empty = lse == -INFINITY;  // no distribution: its gradient is 0
   float m = lse, log_s = 0.f;           // log p = (z − m) − log_s
   if (!empty && fabsf(lse) >= kWideLse && fabsf(lse) < INFINITY) {
-    float best;
-    int best_j;
-    Stat t = join_warp(scan<T, kGroup, false>(z, lo, hi, tid, best, best_j), lane);
+    Stat t = join_warp(wide_sums<T, WARPS>(z, lo, hi, tid), lane);
     if constexpr (WARPS > 1) {
       if (lane == 0) part[warp] = t;
       __syncthreads();
@@ -703,16 +876,16 @@ int check_logits(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld
   return TT_OK;
 }
 
-// grid CTAs in clusters of CL.
+// grid CTAs of `block` threads in clusters of CL.
 template <typename... P, typename... A>
-int launch(void (*kernel)(P...), int64_t grid, int CL, cudaStream_t st, A... args) {
+int launch(void (*kernel)(P...), int64_t grid, int block, int CL, cudaStream_t st, A... args) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = CL;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kBlock);
+  cfg.blockDim = dim3(block);
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = CL > 1 ? 1 : 0;
@@ -721,29 +894,48 @@ int launch(void (*kernel)(P...), int64_t grid, int CL, cudaStream_t st, A... arg
   return cuda_status(e);
 }
 
-// CTAs to a row: as many (a power of two up to 8) as leave each at least `least` vectors a thread while the rows
-// alone do not fill the GPU's SMs twice.
-int ctas_per_row(int64_t N, int64_t nvec, int least) {
+// How the rows are taken: by a warp each, by a CTA of four or eight warps each, or by 2, 4 or 8 CTAs each. nvec: 16-byte
+// vectors of a row. Measured on bf16 rows of 1000 to 151,936 logits, us for the choice and the next one:
+//   forward, 8 alternatives   60,000 x 1000: warp 81, four warps 293;   3000 x 32,000: warp 47, four 48;
+//                             2000 x 50,000: four 45, eight 49;         12,669 x 151,936: eight 592, four 597;
+//                             1000 x 8000 (rows too few for warps): four 9.3, warp 24.5;
+//                             10,000 x 8000, 20 alternatives: warp 69, four 80; 3000 x 32,000: four 56, warp 75
+//                             1 x 151,936: 8 CTAs 8.0, one 12.5; 76 x 151,936: 2 CTAs 12.2, 4 CTAs 13.6
+//   backward                  60,000 x 1000: warp 78, four 134;         10,000 x 8000: warp 63, four 70;
+//                             2000 x 50,000: eight 78, four 86;         76 x 151,936: 8 CTAs 8.3, 4 CTAs 9.6
+struct Plan {
+  int warps, CL;
+};
+Plan plan_fwd(int64_t N, int64_t nvec, int k) {
+  const int64_t sms = sm_count();
+  if (N >= 16 * sms && nvec <= (k <= 16 ? 4096 : 2048)) return {1, 1};
+  if (N >= 4 * sms && nvec <= 12288) return {nvec <= 256 ? 1 : 4, 1};
+  int CL = 1;  // more CTAs only while each finds an SM of its own
+  while (CL < kMostCtas && 2 * CL * N <= sms + sms / 16 && nvec >= 2 * (int64_t)CL * 1024) CL *= 2;
+  return {8, CL};
+}
+Plan plan_bwd(int64_t N, int64_t nvec) {
+  const int64_t sms = sm_count();
+  if (N >= 16 * sms && nvec <= 4096) return {1, 1};
+  if (N >= 4 * sms && nvec <= 2048) return {4, 1};
   int CL = 1;
-  while (CL < 8 && 2 * CL * N <= 2 * (int64_t)sm_count() && nvec >= 2 * (int64_t)CL * kBlock * least) CL *= 2;
-  return CL;
+  while (CL < kMostCtas && 2 * CL * N <= 4 * sms && nvec >= 2 * (int64_t)CL * 128) CL *= 2;
+  return {8, CL};
 }
 
 template <typename T, bool TOP>
 int launch_fwd(const FwdArgs& a, cudaStream_t st) {
-  const int64_t nvec = a.V / Row<T>::VN + 1;
-  if (nvec <= kWarpRow && a.N >= 4 * (int64_t)sm_count())
-    return launch(token_logprob_kernel<T, 1, TOP>, (a.N + kBlock / 32 - 1) / (kBlock / 32), 1, st, a, 1);
-  const int CL = ctas_per_row(a.N, nvec, 1);
-  return launch(token_logprob_kernel<T, kBlock / 32, TOP>, a.N * CL, CL, st, a, CL);
+  const Plan p = plan_fwd(a.N, a.V / Row<T>::VN + 1, a.k);
+  if (p.warps == 1) return launch(token_logprob_kernel<T, 1, TOP>, (a.N + 7) / 8, kBlockOf<1>, 1, st, a, 1);
+  if (p.warps == 4) return launch(token_logprob_kernel<T, 4, TOP>, a.N, kBlockOf<4>, 1, st, a, 1);
+  return launch(token_logprob_kernel<T, 8, TOP>, a.N * p.CL, kBlockOf<8>, p.CL, st, a, p.CL);
 }
 template <typename T>
 int launch_bwd(const BwdArgs& a, cudaStream_t st) {
-  const int64_t nvec = a.V / Row<T>::VN + 1;
-  if (nvec <= kWarpRow && a.N >= 4 * (int64_t)sm_count())
-    return launch(token_logprob_bwd_kernel<T, 1>, (a.N + kBlock / 32 - 1) / (kBlock / 32), 1, st, a, 1);
-  const int CL = ctas_per_row(a.N, nvec, 1);
-  return launch(token_logprob_bwd_kernel<T, kBlock / 32>, a.N * CL, CL, st, a, CL);
+  const Plan p = plan_bwd(a.N, a.V / Row<T>::VN + 1);
+  if (p.warps == 1) return launch(token_logprob_bwd_kernel<T, 1>, (a.N + 7) / 8, kBlockOf<1>, 1, st, a, 1);
+  if (p.warps == 4) return launch(token_logprob_bwd_kernel<T, 4>, a.N, kBlockOf<4>, 1, st, a, 1);
+  return launch(token_logprob_bwd_kernel<T, 8>, a.N * p.CL, kBlockOf<8>, p.CL, st, a, p.CL);
 }
 
 }  // namespace

@@ -540,10 +540,11 @@ TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab
  *   dw_dtype: TT_DT_F32 or TT_DT_BF16), both written.
  * lse, entropy: the forward's (entropy may be NULL without dentropy). dz is
  * rounded to bf16 and kept in ws (tt_lmhead_token_logprob_bwd_workspace_bytes
- * bytes, 16-byte aligned), as in tt_lmhead_logprob_bwd. A target outside
- * [0, V) sets `err` = TT_ERR_INVALID_ARG and its row's dz omits the one-hot
+ * bytes, 16-byte aligned), as in tt_lmhead_logprob_bwd; where N and Hd give
+ * d_hidden few tiles, its sum over the vocabulary is split and the fp32 parts
+ * are kept there too. A target outside [0, V) sets `err` = TT_ERR_INVALID_ARG and its row's dz omits the one-hot
  * term. */
-TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V);
+TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V, int Hd);
 TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
                                        const int32_t* targets, const float* lse, const float* entropy,
                                        const float* dlogp, const float* dentropy, const float* dlse,

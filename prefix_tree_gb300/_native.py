@@ -85,7 +85,7 @@ _SIGS = {
     "tt_lmhead_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tt_lmhead_token_logprob_workspace_bytes": (_sz, [_i64, _i64]),
     "tt_lmhead_token_logprob": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
-    "tt_lmhead_token_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "tt_lmhead_token_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "tt_lmhead_token_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int] + [_vp] * 8 + [_int, _vp, _sz, _vp, _vp]),
     "tt_status_string": (ctypes.c_char_p, [_int]),
     "tt_version": (_int, []),
@@ -781,7 +781,7 @@ def lmhead_token_logprob_bwd(hidden, w_vocab, targets, lse, entropy=None, dlogp=
         raise TypeError("d_w_vocab must be fp32 or bf16")
     _per_row(dw, dw.dtype, "d_w_vocab", (V, Hd))
     if ws is None:
-        ws = torch.empty(lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
+        ws = torch.empty(lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V, Hd), dtype=torch.uint8, device=dev)
     err = new_err(dev) if err is None else err
     _call("tt_lmhead_token_logprob_bwd",
           _device_of(hidden, w_vocab, targets, lse, entropy, dlogp, dentropy, dlse, dh, dw, ws, err), hidden.data_ptr(),

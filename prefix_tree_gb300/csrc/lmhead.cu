@@ -66,7 +66,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Epilogues: per-row log-sum-exp partials (forward), dz (bf16), plain bf16 / fp32 stores; the partials with an
 // entropy sum beside them, and dz of an objective of log-prob and entropy.
-enum { EPI_LSE = 0, EPI_DZ = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_LSE_H = 4, EPI_DZ_H = 5 };
+// EPI_PART: an fp32 partial product over one of `splits` ranges of K, each to a matrix of its own.
+enum { EPI_LSE = 0, EPI_DZ = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_LSE_H = 4, EPI_DZ_H = 5, EPI_PART = 6 };
 // What stands for a column >= V where an entropy is summed: far below any
 // logit, and finite, so that 0·(z − m) is 0.
 constexpr float kNoColumn = -1e30f;
@@ -112,7 +113,17 @@ struct LhArgs {
   float* pu;             // EPI_LSE_H: [nN][M] Σ 2^x·x, x = (z − m)·log2 e
   const float* entropy;  // EPI_DZ_H, as the next three (each may be NULL): per row
   const float *dlogp, *dentropy, *dlse;
+  bool rows32;  // all stores but EPI_DZ's: rows of ob or of begin on 32-byte boundaries (whole sectors to a store)
+  int splits;   // EPI_PART: ranges of K (tiles = nM·nN·splits)
 };
+
+// 32 bytes in one store: a whole sector, which halves the L2 writes of a
+// thread's row piece against two of 16 (dz of 4001 x 32,003: 202 -> 175 us).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 template <int EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kLhWarps * 32, 1)
@@ -165,7 +176,18 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
     mbar_arrive(&bar[TILE_EMPTY + r]);
     return true;
   };
+  // the K steps of a tile
+  auto k_range = [&](int64_t t, int& k0, int& k1) {
+    k0 = 0;
+    k1 = a.ksteps;
+    if (EPI == EPI_PART) {
+      const int s = (int)(t / ((int64_t)a.nM * a.nN));
+      k0 = (int)((int64_t)a.ksteps * s / a.splits);
+      k1 = (int)((int64_t)a.ksteps * (s + 1) / a.splits);
+    }
+  };
   auto tile_mn = [&](int64_t t, int& m, int& n) {
+    if (EPI == EPI_PART) t %= (int64_t)a.nM * a.nN;
     if (a.n_outer) {
       n = (int)(t / a.nM);
       m = (int)(t % a.nM);
@@ -195,9 +217,10 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
           mbar_arrive(&bar[TILE_FULL + r]);
         }
         if (t >= a.tiles) break;
-        int m, n;
+        int m, n, k0, k1;
         tile_mn(t, m, n);
-        for (int ks = 0; ks < a.ksteps; ++ks, ++kk) {
+        k_range(t, k0, k1);
+        for (int ks = k0; ks < k1; ++ks, ++kk) {
           const int st = (int)(kk % kStages);
           if (kk >= kStages && !mbar_wait(&bar[EMPTY + st], (uint32_t)((kk / kStages - 1) & 1), abort_flag, 1)) {
             ok = false;
@@ -243,7 +266,9 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         if (it >= 2 && !mbar_wait(&bar[ACC_EMPTY + acc], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, 2)) break;
         tc_fence_after();
         const uint32_t dcol = tbase + (uint32_t)acc * kBN;
-        for (int ks = 0; ks < a.ksteps; ++ks, ++kk) {
+        int k0, k1;
+        k_range(t, k0, k1);
+        for (int ks = k0; ks < k1; ++ks, ++kk) {
           const int st = (int)(kk % kStages);
           if (!mbar_wait(&bar[FULL + st], (uint32_t)((kk / kStages) & 1), abort_flag, 3)) {
             ok = false;
@@ -253,7 +278,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
             umma_ss(dcol, desc_at(da, st * kABytes + k * ka), desc_at(db, st * kBBytes + k * kb), idesc,
-                    (ks > 0 || k > 0) ? 1u : 0u);
+                    (ks > k0 || k > 0) ? 1u : 0u);
           umma_commit(&bar[EMPTY + st]);  // stage st free once these MMAs have read it
         }
         if (ok) umma_commit(&bar[ACC_FULL + acc]);
@@ -310,11 +335,21 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         const int64_t nvalid = a.Ncols - col0;  // columns j < nvalid exist
         if (kLse) {
           float cm = -INFINITY;
+          if (kEnt) {
+            if (nvalid < 32) {  // the last tile
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float z = j < nvalid ? __uint_as_float(u[j]) : kEnt ? kNoColumn : -INFINITY;
-            u[j] = __float_as_uint(z);
-            cm = fmaxf(cm, z);
+              for (int j = 0; j < 32; ++j)
+                if (j >= nvalid) u[j] = __float_as_uint(kNoColumn);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) cm = fmax3f(cm, __uint_as_float(u[j]), __uint_as_float(u[j + 1]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float z = j < nvalid ? __uint_as_float(u[j]) : -INFINITY;
+              u[j] = __float_as_uint(z);
+              cm = fmaxf(cm, z);
+            }
           }
           if ((uint64_t)(yc - c * 32) < 32u) {
             // u[jc] by a tree of selects on the bits of jc (no indexed register access)
@@ -350,9 +385,19 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
             if (kEnt) u_run += ent2.x + ent2.y;
             m_run = nm;
           }
-        } else if (EPI == EPI_F32) {
+        } else if (EPI == EPI_F32 || EPI == EPI_PART) {
           if (row_ok) {
             float* dst = a.of + row * a.ldo + col0;
+            if (EPI == EPI_PART) dst += t / ((int64_t)a.nM * a.nN) * a.M * a.ldo;
+            if (a.rows32) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (8 * q < nvalid) {
+                  const uint32_t w8[8] = {u[8 * q],     u[8 * q + 1], u[8 * q + 2], u[8 * q + 3],
+                                          u[8 * q + 4], u[8 * q + 5], u[8 * q + 6], u[8 * q + 7]};
+                  store32(dst + 8 * q, w8);
+                }
+            } else
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               if (4 * q < nvalid)
@@ -396,7 +441,20 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
                 if (j == jc) u[j] = __float_as_uint(__uint_as_float(u[j]) - gw);
             }
           }
-          if (row_ok) {
+          if ((EPI == EPI_DZ_H || EPI == EPI_BF16) && a.rows32) {
+            if (row_ok) {
+              __nv_bfloat16* dst = a.ob + row * a.ldo + col0;
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                if (16 * q < nvalid) {
+                  uint32_t w8[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    w8[i] = pack_bf16(__uint_as_float(u[16 * q + 2 * i]), __uint_as_float(u[16 * q + 2 * i + 1]));
+                  store32(dst + 16 * q, w8);
+                }
+            }
+          } else if (row_ok) {
             __nv_bfloat16* dst = a.ob + row * a.ldo + col0;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -503,24 +561,44 @@ __device__ __forceinline__ void stat_merge(LhStat& a, const LhStat& b) {
   a.s = a.s * fa + b.s * fb;
   a.m = M;
 }
-__global__ void __launch_bounds__(32 * kCombineWarps)
+// A block of 1024 threads takes ROWS consecutive rows and splits their tiles over 1024/ROWS threads each, four of a
+// thread's tiles under way at once; the threads' sums are joined pairwise. (61 rows of 594 tiles: ROWS = 8 4 us, 32
+// 10 us, one tile at a time over 8 warps 57 us.)
+template <int ROWS>
+__global__ void __launch_bounds__(1024)
     lmhead_combine_entropy_kernel(const float* pm, const float* ps, const float* pu, const float* pz, int64_t N, int nV,
                                   int64_t V, const int32_t* targets, float* logp, float* entropy, float* lse,
                                   int32_t* err) {
-  __shared__ LhStat part[kCombineWarps][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  constexpr int kShares = 1024 / ROWS;
+  __shared__ LhStat part[kShares][ROWS];
+  const int r = threadIdx.x % ROWS, w = threadIdx.x / ROWS;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + r;
   LhStat t = {-INFINITY, 0.f, 0.f};
   if (row < N)
-    for (int j = w; j < nV; j += kCombineWarps) {
-      const int64_t at = (int64_t)j * N + row;
-      stat_merge(t, LhStat{pm[at], ps[at], pu[at] * 0.6931471805599453f});
-    }
-  part[w][lane] = t;
-  __syncthreads();
-  if (w != 0 || row >= N) return;
+    for (int j = w; j < nV; j += 4 * kShares) {
+      LhStat p[4];
 #pragma unroll
-  for (int k = 1; k < kCombineWarps; ++k) stat_merge(t, part[k][lane]);
+      for (int i = 0; i < 4; ++i) {
+        const int ji = j + i * kShares;
+        const int64_t at = (int64_t)ji * N + row;
+        p[i] = ji < nV ? LhStat{pm[at], ps[at], pu[at]} : LhStat{-INFINITY, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i].u *= 0.6931471805599453f;
+        stat_merge(t, p[i]);
+      }
+    }
+  part[w][r] = t;
+#pragma unroll
+  for (int d = kShares / 2; d; d >>= 1) {
+    __syncthreads();
+    if (w < d) {
+      stat_merge(t, part[w + d][r]);
+      part[w][r] = t;
+    }
+  }
+  if (w != 0 || row >= N) return;
   const float log_s = logf(t.s);
   const float h = log_s - t.u / t.s;
   entropy[row] = h < 0.f ? 0.f : h;
@@ -622,12 +700,30 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
   return dz_bytes(N, V) + 256;
 }
 
+// The sum of a split product's parts [splits][n] in their order, to bf16 (n a multiple of 4).
+__global__ void __launch_bounds__(256) lmhead_sum_parts_kernel(const float* part, int64_t n, int splits,
+                                                               __nv_bfloat16* out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 p = *reinterpret_cast<const float4*>(part + s * n + i);
+    t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+  }
+  *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+}
+
 namespace {
+// Rows of `bytes` bytes from p begin on 32-byte boundaries.
+bool rows_on_32(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) % 32 == 0; }
+
 // dH = dz·W (bf16) and dW = dzᵀ·H (fp32, or bf16 with dw_dtype = TT_DT_BF16) from dz [N][ldz]; ctr[1], ctr[2]: their
-// tile counters (0 at launch).
+// tile counters (0 at launch). parts: room for `splits` fp32 matrices [N][Hd] where dH's sum over the vocabulary is to
+// be split (splits > 1).
 int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd, const __nv_bfloat16* dz,
-                int* ctr, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, int32_t* err, cudaStream_t st) {
-  const int64_t ldz = dz_ld(V);
+                int64_t ldz, int* ctr, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, float* parts, int splits,
+                int32_t* err, cudaStream_t st) {
   // 2. dH = dz·W: A = dz [N][V] (K-major, K = V); B = W [V][Hd] read MN-major; token-major tiles
   CUtensorMap mdz, mw_mn;
   if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
@@ -635,6 +731,13 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
     return TT_ERR_CUDA;
   LhArgs b = lh_args(N, Hd, V, 0, err);
   b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr + 1;
+  b.rows32 = rows_on_32(b.ob, 2 * Hd);
+  if (splits > 1) {
+    b.of = parts;
+    b.rows32 = rows_on_32(parts, 4 * Hd);
+    b.splits = splits;
+    b.tiles *= splits;
+  }
   // 3. dW = dzᵀ·H: A = dz read MN-major ([K = tokens][M = vocabulary]), B = H [N][Hd] read MN-major
   CUtensorMap mdz_mn, mh_mn;
   if (!make_tmap_bf16_ld(&mdz_mn, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, 64) ||
@@ -646,6 +749,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
     c.ob = static_cast<__nv_bfloat16*>(d_w_vocab);
   else
     c.of = static_cast<float*>(d_w_vocab);
+  c.rows32 = rows_on_32(d_w_vocab, (dw_bf16 ? 2 : 4) * Hd);
   c.ldo = Hd; c.counter = ctr + 2;
   // dH and dW both only read dz: dW runs on a second stream forked after dz,
   // so that its CTAs (which claim tiles as they free up) take the SMs that
@@ -656,13 +760,20 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   cudaStream_t side = nullptr;
   cudaEvent_t fork = nullptr, join = nullptr;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  const bool two = cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
+  // (A split dH leaves none idle.)
+  const bool two = splits <= 1 && cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
                    cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking) == cudaSuccess &&
                    cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) == cudaSuccess &&
                    cudaEventCreateWithFlags(&join, cudaEventDisableTiming) == cudaSuccess &&
                    cudaEventRecord(fork, st) == cudaSuccess && cudaStreamWaitEvent(side, fork, 0) == cudaSuccess;
   if (!two) (void)cudaGetLastError();
-  const int rc = launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
+  int rc = splits > 1 ? launch_gemm<EPI_PART, false, true>(mdz, mw_mn, b, st)
+                      : launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
+  if (!rc && splits > 1) {
+    const int64_t n = N * Hd;
+    lmhead_sum_parts_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(parts, n, splits, b.ob);
+    if (cudaGetLastError() != cudaSuccess) rc = TT_ERR_CUDA;
+  }
   int rc2 = rc;
   if (!rc)
     rc2 = dw_bf16 ? launch_gemm<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
@@ -699,7 +810,7 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
   a.targets = targets; a.weights = weights; a.g = g; a.lse = lse; a.ob = dz; a.ldo = ldz; a.counter = ctr;
   rc = launch_gemm<EPI_DZ, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  return lh_products(hidden, w_vocab, N, V, Hd, dz, ctr, d_hidden, d_w_vocab, TT_DT_F32, err, st);
+  return lh_products(hidden, w_vocab, N, V, Hd, dz, ldz, ctr, d_hidden, d_w_vocab, TT_DT_F32, nullptr, 1, err, st);
 }
 
 TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V) {
@@ -728,14 +839,43 @@ TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab
   a.pu = ws_at<float>(ws, Lw.pu);
   rc = launch_gemm<EPI_LSE_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  lmhead_combine_entropy_kernel<<<(unsigned)((N + 31) / 32), 32 * kCombineWarps, 0, st>>>(
-      a.pm, a.ps, a.pu, a.pz, N, a.nN, V, targets, logp, entropy, lse, err);
+  auto* combine = N <= 2048 ? lmhead_combine_entropy_kernel<8> : lmhead_combine_entropy_kernel<32>;
+  const int rows = N <= 2048 ? 8 : 32;
+  combine<<<(unsigned)((N + rows - 1) / rows), 1024, 0, st>>>(a.pm, a.ps, a.pu, a.pz, N, a.nN, V, targets, logp, entropy,
+                                                             lse, err);
   TT_LAUNCH_CHECK();
   return TT_OK;
 }
 
-TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
-  return tt_lmhead_logprob_bwd_workspace_bytes(N, V);
+namespace {
+// Scratch of the backward with entropy: dz [N][ldz] (rows on 32-byte
+// boundaries), the tile counters, and the parts of a split dH. dH = dz·W has
+// ceil(N/128)·ceil(Hd/256) tiles, each a sum over the whole vocabulary: where
+// these are few the sum is split so that about every SM has a part, of 8 K
+// steps or more (61 x 151,936 x 2048: 8 tiles alone take 790 us). The split
+// goes by sizes alone, on any device as on one of kSplitSms SMs: the
+// workspace and the order of the sums do not depend on the device.
+constexpr int kSplitSms = 152;
+struct LhBwdWs {
+  int64_t ldz;
+  int splits;
+  size_t ctr, parts, total;
+};
+LhBwdWs lh_bwd_layout(int64_t N, int64_t V, int Hd) {
+  LhBwdWs w;
+  w.ldz = (V + 15) / 16 * 16;
+  const int64_t tiles = (N + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN), ksteps = (V + kBK - 1) / kBK;
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSplitSms / tiles, ksteps / 8));
+  w.ctr = align_up((size_t)N * (size_t)w.ldz * 2, 256);
+  w.parts = w.ctr + 256;
+  w.total = w.parts + (w.splits > 1 ? sizeof(float) * (size_t)w.splits * (size_t)N * (size_t)Hd : 0);
+  return w;
+}
+}  // namespace
+
+TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V, int Hd) {
+  if (N < 1 || V < 1 || Hd < 1) return 0;
+  return lh_bwd_layout(N, V, Hd).total;
 }
 
 TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
@@ -748,10 +888,11 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
   if (!lse || (dentropy && !entropy) || !d_hidden || !d_w_vocab || !ws || !aligned16(ws) || !aligned16(d_hidden) ||
       !aligned16(d_w_vocab) || (dw_dtype != TT_DT_F32 && dw_dtype != TT_DT_BF16))
     return TT_ERR_INVALID_ARG;
-  if (ws_bytes < tt_lmhead_token_logprob_bwd_workspace_bytes(N, V)) return TT_ERR_WORKSPACE;
+  const LhBwdWs Lw = lh_bwd_layout(N, V, Hd);
+  if (ws_bytes < Lw.total) return TT_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
-  int* ctr = ws_at<int>(ws, dz_bytes(N, V));  // [3]: dz, dH, dW
+  int* ctr = ws_at<int>(ws, Lw.ctr);  // [3]: dz, dH, dW
   if (cudaMemsetAsync(ctr, 0, 3 * sizeof(int), st) != cudaSuccess) return TT_ERR_CUDA;
   CUtensorMap mh, mw;
   if (!make_tmap_bf16(&mh, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ||
@@ -759,8 +900,9 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
     return TT_ERR_CUDA;
   LhArgs a = lh_args(N, V, Hd, 1, err);
   a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
-  a.ob = dz; a.ldo = dz_ld(V); a.counter = ctr;
+  a.ob = dz; a.ldo = Lw.ldz; a.counter = ctr; a.rows32 = rows_on_32(dz, 2 * Lw.ldz);
   rc = launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  return lh_products(hidden, w_vocab, N, V, Hd, dz, ctr, d_hidden, d_w_vocab, dw_dtype, err, st);
+  return lh_products(hidden, w_vocab, N, V, Hd, dz, Lw.ldz, ctr, d_hidden, d_w_vocab, dw_dtype,
+                     ws_at<float>(ws, Lw.parts), Lw.splits, err, st);
 }

@@ -65,6 +65,33 @@ def test_backward(tt, N, V, Hd, dw_dtype):
     assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("N,V,Hd", [(1, 9000, 64), (61, 32003, 512), (129, 5003, 1024), (130, 20001, 256)])
+def test_backward_of_few_rows(tt, N, V, Hd):
+    """Few tiles of d_hidden: its sum over the vocabulary is split over the SMs. Tolerance as test_backward; a
+    workspace one byte short is refused."""
+    d, H, W, y = _inputs(N, V, Hd)
+    rng = np.random.default_rng(N)
+    dl, de = (rng.standard_normal(N).astype(np.float32) for _ in range(2))
+    _, h, lse = tt.lmhead_token_logprob(H, W, y)
+    args = dict(dlogp=torch.tensor(dl, device="cuda"), dentropy=torch.tensor(de, device="cuda"))
+    dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, **args)
+    dz = TL.token_logprob_grad(LH.logits(f64(d["H"]), f64(d["W"])), d["targets"], dlogp=dl, dentropy=de)
+    assert rel_l2(dev_to_f64(dh), dz @ f64(d["W"])) <= GRAD_RL2
+    assert rel_l2(dev_to_f64(dw), dz.T @ f64(d["H"])) <= GRAD_RL2
+    again = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, **args)
+    assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
+    n = tt.lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V, Hd)
+    with pytest.raises(tt.TTError) as e:
+        tt.lmhead_token_logprob_bwd(H, W, y, lse, h, ws=torch.empty(n - 1, dtype=torch.uint8, device="cuda"), **args)
+    assert e.value.code == -4
+    # a workspace and outputs on 16-byte boundaries only: 16-byte stores, the same values
+    ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")[16:]
+    out = (torch.empty(N * Hd + 8, dtype=torch.bfloat16, device="cuda")[8:].view(N, Hd),
+           torch.empty(V * Hd + 8, dtype=torch.bfloat16, device="cuda")[8:].view(V, Hd))
+    dh2, dw2 = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, out=out, ws=ws, **args)
+    assert torch.equal(dh2, dh) and torch.equal(dw2, dw.to(torch.bfloat16))
+
+
 def test_log_prob_gradient_equals_the_weighted_call(tt):
     """dlogp = −g·w is the weighted loss: the two calls form dz in another order of two products, then round to bf16."""
     d, H, W, y = _inputs(300, 3001, 128)

@@ -75,7 +75,8 @@ def test_token_logprob_bwd_arguments(L, over, code):
 def test_lmhead_token_logprob_arguments(L):
     nb = L.tt_lmhead_token_logprob_workspace_bytes
     assert nb(0, 5) == 0 and nb(300, 1000) >= 12 * 300 * 4 + 4 * 300
-    assert L.tt_lmhead_token_logprob_bwd_workspace_bytes(300, 1000) >= 300 * 1000 * 2
+    bwd_bytes = L.tt_lmhead_token_logprob_bwd_workspace_bytes
+    assert bwd_bytes(0, 1000, 128) == 0 and bwd_bytes(300, 1000, 128) >= 300 * 1000 * 2
     big = 1 << 40
 
     def fwd(h=fake, w=fake, N=300, V=1000, Hd=128, y=fake, logp=fake, ent=fake, lse=fake, ws=fake, n=big, err=fake):

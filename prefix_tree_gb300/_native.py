@@ -315,8 +315,8 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
     axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base),
                               None if inv_freq is None else tuple(float(f) for f in inv_freq))
     if out is None:
-        qo = torch.empty((N, hq, d), dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty((N, hkv, d), dtype=q.dtype, device=q.device)
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
         qo_ld, ko_ld = hq * d, hkv * d
     else:
         qo, ko = out
@@ -627,9 +627,8 @@ def token_logprob(logits, targets=None, top_k=0, out=None, err=None):
     rows, dev, k = (N,), logits.device, int(top_k)
     _per_row(targets, torch.int32, "targets", rows)
     if out is None:
-        logp, entropy, lse = torch.empty((3, N), dtype=torch.float32, device=dev).unbind(0)
-        if targets is None:
-            logp = None
+        logp = torch.empty(N, dtype=torch.float32, device=dev) if targets is not None else None
+        entropy, lse = torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)
         ids = torch.empty((N, k), dtype=torch.int32, device=dev) if k > 0 else None
         top = torch.empty((N, k), dtype=torch.float32, device=dev) if k > 0 else None
     else:
@@ -747,7 +746,7 @@ def lmhead_token_logprob(hidden, w_vocab, targets, out=None, ws=None, err=None):
     N, V, Hd = _lmhead_args(hidden, w_vocab, targets)
     dev = hidden.device
     if out is None:
-        out = torch.empty((3, N), dtype=torch.float32, device=dev).unbind(0)
+        out = tuple(torch.empty(N, dtype=torch.float32, device=dev) for _ in range(3))
     logp, entropy, lse = out
     for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
         _need(t, torch.float32, n, 1)

@@ -41,6 +41,9 @@ constexpr int kFirstPart = 4;
 // Threads of a block: a group of WARPS warps, or eight groups of one.
 template <int WARPS>
 constexpr int kBlockOf = WARPS == 1 ? 256 : 32 * WARPS;
+// CTAs to an SM that the registers are held to: 32 warps (with 40 or 48, spills cost more than the warps give).
+template <int WARPS>
+constexpr int kMinCtas = 1024 / kBlockOf<WARPS>;
 
 typedef unsigned long long u64;
 
@@ -165,15 +168,6 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < VN; ++i) t[i] = (e + i >= 0 && e + i < V) ? p[e + i] : static_cast<T>(-INFINITY);
     return u;
-  }
-  __device__ __forceinline__ void load(int j, float (&f)[VN]) const {
-    const uint4 u = load(j);
-#pragma unroll
-    for (int i = 0; i < VN / 2; ++i) {
-      const float2 x = Pairs<T>::get(u, i);
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
   }
 };
 
@@ -300,18 +294,27 @@ struct Scan {
   __device__ __forceinline__ void fetch(int at, int st) {
     if (at >= wlo && at + (kBatch - 1) * kGroup < whi) {
 #pragma unroll
-      for (int v = 0; v < kBatch; ++v)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring.at[st][v][tid])),
-                     "l"(z.p + z.first(at + v * kGroup))
-                     : "memory");
-    } else {
-      uint4 pad;
+      for (int v = 0; v < kBatch; ++v) copy(at + v * kGroup, st, v);
+    } else {  // the row's ends: only a vector that is not whole is waited for
 #pragma unroll
-      for (int i = 0; i < Row<T>::VN; ++i) reinterpret_cast<T*>(&pad)[i] = static_cast<T>(-INFINITY);
+      for (int v = 0; v < kBatch; ++v) {
+        const int jv = at + v * kGroup;
+        if (jv >= wlo && jv < whi) {
+          copy(jv, st, v);
+        } else {
+          uint4 u;
 #pragma unroll
-      for (int v = 0; v < kBatch; ++v) ring.at[st][v][tid] = at + v * kGroup < hi ? z.load(at + v * kGroup) : pad;
+          for (int i = 0; i < Row<T>::VN; ++i) reinterpret_cast<T*>(&u)[i] = static_cast<T>(-INFINITY);
+          if (jv < hi) u = z.load(jv);
+          ring.at[st][v][tid] = u;
+        }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void copy(int jv, int st, int v) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring.at[st][v][tid])), "l"(z.p + z.first(jv))
+                 : "memory");
   }
   // The batches before vector `end` (all the thread's with end = hi). The lanes of a warp stay together (those past the
   // end take masked logits). With OVER, over(src) is called by the whole warp for each lane src whose batch has a logit
@@ -605,7 +608,7 @@ __device__ __noinline__ u64 top_of_slice(TopShared<WARPS>& sh, const Row<T>& z, 
 // (cluster size 1: one group per row). WARPS = 1: the warps of a block take
 // rows of their own.
 template <typename T, int WARPS, bool TOP>
-__global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_kernel(const FwdArgs a, int CL) {
+__global__ void __launch_bounds__(kBlockOf<WARPS>, kMinCtas<WARPS>) token_logprob_kernel(const FwdArgs a, int CL) {
   constexpr int kGroup = WARPS * 32;
   constexpr int kGroups = kBlockOf<WARPS> / kGroup;
   __shared__ Stat part[WARPS];
@@ -623,7 +626,8 @@ __global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_kernel(const Fw
   const int lo = (int)((int64_t)z.nvec * rank / CL), hi = (int)((int64_t)z.nvec * (rank + 1) / CL);
 
   Scan<T, WARPS> scan(z, ring, lo, hi, tid);
-  u64 list = 0;  // lane i: the i-th best
+  // the target, and after the pass its logit: loads that nothing waits for
+  const int y = a.y && rank == 0 && tid == 0 ? a.y[row] : -1;
   if constexpr (TOP) {
     TopShared<WARPS>& sh = top[WARPS == 1 ? warp : 0];
     // the first part: whole rounds of batches
@@ -640,10 +644,12 @@ __global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_kernel(const Fw
   } else {
     scan.template take_all<false>();
   }
+  const float zy = y >= 0 && y < z.V ? static_cast<float>(z.p[y]) : 0.f;
   Stat t = join_warp(scan.t, lane);
   if (!plain_way_holds<T>(t.m)) t = join_warp(wide_sums<T, WARPS>(z, lo, hi, tid), lane);
   if (WARPS > 1 && lane == 0) part[warp] = t;
   group_sync<WARPS>();
+  u64 list = 0;  // lane i of the first warp: the i-th best
   if constexpr (TOP) {
     TopShared<WARPS>& sh = top[WARPS == 1 ? warp : 0];
     list = sh.found <= TopShared<WARPS>::kRoom ? sort_kept<WARPS>(sh, tid)
@@ -695,12 +701,11 @@ __global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_kernel(const Fw
     a.lse[row] = empty ? -INFINITY : lse;
     a.entropy[row] = empty || h < 0.f ? 0.f : h;
     if (a.y) {
-      const int y = a.y[row];
-      if (y < 0 || y >= a.V) {
+      if (y < 0 || y >= z.V) {
         set_err(a.err, TT_ERR_INVALID_ARG);
         a.logp[row] = __int_as_float(0x7fc00000);
       } else {
-        a.logp[row] = empty ? -INFINITY : (static_cast<float>(z.p[y]) - t.m) - log_s;
+        a.logp[row] = empty ? -INFINITY : (zy - t.m) - log_s;
       }
     }
   }
@@ -752,6 +757,22 @@ __global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_bwd_kernel(cons
   const Row<T> z(static_cast<const T*>(a.z) + row * a.ld, a.V);
   T* out = static_cast<T*>(a.dz) + row * a.ld;
   const int lo = (int)((int64_t)z.nvec * rank / CL), hi = (int)((int64_t)z.nvec * (rank + 1) / CL);
+  const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(z.p) & 15);
+  const int wlo = z.whole_lo(), whi = min(hi, z.whole_hi());
+  // the first vectors, before the loads that wait for one another
+  auto plain = [&](int j) { return same && j >= wlo && j + (kBatch - 1) * kGroup < whi; };
+  uint4 next[kBatch];
+  auto fetch = [&](int j) {
+    if (j >= wlo && j + (kBatch - 1) * kGroup < whi) {
+#pragma unroll
+      for (int v = 0; v < kBatch; ++v) next[v] = z.load_whole(j + v * kGroup);
+    } else {
+#pragma unroll
+      for (int v = 0; v < kBatch; ++v)
+        if (j + v * kGroup < hi) next[v] = z.load(j + v * kGroup);
+    }
+  };
+  fetch(lo + tid);
   const float lse = a.lse[row];
   const bool empty = lse == -INFINITY;  // no distribution: its gradient is 0
   float m = lse, log_s = 0.f;           // log p = (z − m) − log_s
@@ -842,23 +863,24 @@ __global__ void __launch_bounds__(kBlockOf<WARPS>) token_logprob_bwd_kernel(cons
     }
     return r;
   };
-  const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(z.p) & 15);
-  const int wlo = z.whole_lo(), whi = min(hi, z.whole_hi());
   for (int j = lo + tid; j < hi; j += kBatch * kGroup) {
-    if (same && j >= wlo && j + (kBatch - 1) * kGroup < whi) {
-      uint4 u[kBatch];
+    uint4 u[kBatch];
 #pragma unroll
-      for (int v = 0; v < kBatch; ++v) u[v] = z.load_whole(j + v * kGroup);
+    for (int v = 0; v < kBatch; ++v) u[v] = next[v];
+    fetch(j + kBatch * kGroup);
+    if (plain(j)) {
 #pragma unroll
       for (int v = 0; v < kBatch; ++v) *reinterpret_cast<uint4*>(out + z.first(j + v * kGroup)) = turn(u[v]);
     } else {
-      for (int v = 0; v < kBatch && j + v * kGroup < hi; ++v) {
-        const int jj = j + v * kGroup;
-        const uint4 r = turn(z.load(jj));
-        if (same && z.whole(jj))
-          *reinterpret_cast<uint4*>(out + z.first(jj)) = r;
+#pragma unroll
+      for (int v = 0; v < kBatch; ++v) {
+        const int jv = j + v * kGroup;
+        if (jv >= hi) continue;
+        const uint4 r = turn(u[v]);
+        if (same && z.whole(jv))
+          *reinterpret_cast<uint4*>(out + z.first(jv)) = r;
         else
-          put(jj, r);
+          put(jv, r);
       }
     }
   }
@@ -899,7 +921,7 @@ int launch(void (*kernel)(P...), int64_t grid, int block, int CL, cudaStream_t s
 //   forward, 8 alternatives   60,000 x 1000: warp 81, four warps 293;   3000 x 32,000: warp 47, four 48;
 //                             2000 x 50,000: four 45, eight 49;         12,669 x 151,936: eight 592, four 597;
 //                             1000 x 8000 (rows too few for warps): four 9.3, warp 24.5;
-//                             10,000 x 8000, 20 alternatives: warp 69, four 80; 3000 x 32,000: four 56, warp 75
+//                             10,000 x 8000, 20 alternatives: warp 69, four 80; 6000 x 16,000: four 75, warp 90
 //                             1 x 151,936: 8 CTAs 8.0, one 12.5; 76 x 151,936: 2 CTAs 12.2, 4 CTAs 13.6
 //   backward                  60,000 x 1000: warp 78, four 134;         10,000 x 8000: warp 63, four 70;
 //                             2000 x 50,000: eight 78, four 86;         76 x 151,936: 8 CTAs 8.3, 4 CTAs 9.6
@@ -908,7 +930,7 @@ struct Plan {
 };
 Plan plan_fwd(int64_t N, int64_t nvec, int k) {
   const int64_t sms = sm_count();
-  if (N >= 16 * sms && nvec <= (k <= 16 ? 4096 : 2048)) return {1, 1};
+  if (N >= 16 * sms && nvec <= (k <= 16 ? 4096 : 1024)) return {1, 1};
   if (N >= 4 * sms && nvec <= 12288) return {nvec <= 256 ? 1 : 4, 1};
   int CL = 1;  // more CTAs only while each finds an SM of its own
   while (CL < kMostCtas && 2 * CL * N <= sms + sms / 16 && nvec >= 2 * (int64_t)CL * 1024) CL *= 2;

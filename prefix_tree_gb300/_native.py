@@ -611,12 +611,15 @@ def _logit_rows(t, name):
     return N, V, ld
 
 
-def _per_row(t, dtype, name, shape):
-    if t is not None:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
-            raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous and have shape {tuple(shape)}")
+def _per_row(t, dtype, name, shape, required=False):
+    if t is None:
+        if required:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        return
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and have shape {tuple(shape)}")
 
 
 def token_logprob(logits, targets=None, top_k=0, out=None, err=None):
@@ -651,9 +654,9 @@ def token_logprob_bwd(logits, lse, entropy=None, targets=None, dlogp=None, dentr
     may be logits itself, which is then overwritten."""
     N, V, ld = _logit_rows(logits, "logits")
     rows = (N,)
-    _need(lse, torch.float32, "lse", 1)
+    _per_row(lse, torch.float32, "lse", rows, True)
     _per_row(targets, torch.int32, "targets", rows)
-    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
+    for t, n in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
         _per_row(t, torch.float32, n, rows)
     if (top_ids is None) != (dtop is None):
         raise ValueError("top_ids and dtop go together")
@@ -735,8 +738,7 @@ def _lmhead_args(hidden, w_vocab, targets):
     N, Hd = hidden.shape
     if w_vocab.shape[1] != Hd:
         raise ValueError("hidden and w_vocab must share Hd")
-    _need(targets, torch.int32, "targets", 1)
-    _per_row(targets, torch.int32, "targets", (N,))
+    _per_row(targets, torch.int32, "targets", (N,), True)
     return N, w_vocab.shape[0], Hd
 
 
@@ -746,11 +748,11 @@ def lmhead_token_logprob(hidden, w_vocab, targets, out=None, ws=None, err=None):
     N, V, Hd = _lmhead_args(hidden, w_vocab, targets)
     dev = hidden.device
     if out is None:
-        out = tuple(torch.empty(N, dtype=torch.float32, device=dev) for _ in range(3))
-    logp, entropy, lse = out
-    for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
-        _need(t, torch.float32, n, 1)
-        _per_row(t, torch.float32, n, (N,))
+        logp, entropy, lse = (torch.empty(N, dtype=torch.float32, device=dev) for _ in range(3))
+    else:
+        logp, entropy, lse = out
+        for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
+            _per_row(t, torch.float32, n, (N,), True)
     if ws is None:
         ws = torch.empty(lib().tt_lmhead_token_logprob_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
     err = new_err(dev) if err is None else err
@@ -767,18 +769,19 @@ def lmhead_token_logprob_bwd(hidden, w_vocab, targets, lse, entropy=None, dlogp=
     (`dw_dtype`, or the type of out[1])."""
     N, V, Hd = _lmhead_args(hidden, w_vocab, targets)
     dev = hidden.device
-    _need(lse, torch.float32, "lse", 1)
-    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
+    _per_row(lse, torch.float32, "lse", (N,), True)
+    for t, n in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy"), (dlse, "dlse")):
         _per_row(t, torch.float32, n, (N,))
     if out is None:
         if dw_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("dw_dtype must be torch.float32 or torch.bfloat16")
-        out = (torch.empty_like(hidden), torch.empty(V, Hd, dtype=dw_dtype, device=dev))
-    dh, dw = out
-    _per_row(dh, torch.bfloat16, "d_hidden", (N, Hd))
-    if dw.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("d_w_vocab must be fp32 or bf16")
-    _per_row(dw, dw.dtype, "d_w_vocab", (V, Hd))
+        dh, dw = torch.empty_like(hidden), torch.empty((V, Hd), dtype=dw_dtype, device=dev)
+    else:
+        dh, dw = out
+        _per_row(dh, torch.bfloat16, "d_hidden", (N, Hd), True)
+        if dw is None or dw.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("d_w_vocab must be an fp32 or bf16 CUDA tensor")
+        _per_row(dw, dw.dtype, "d_w_vocab", (V, Hd))
     if ws is None:
         ws = torch.empty(lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V, Hd), dtype=torch.uint8, device=dev)
     err = new_err(dev) if err is None else err

@@ -719,18 +719,18 @@ namespace {
 bool rows_on_32(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) % 32 == 0; }
 
 // dH = dz·W (bf16) and dW = dzᵀ·H (fp32, or bf16 with dw_dtype = TT_DT_BF16) from dz [N][ldz]; ctr[1], ctr[2]: their
-// tile counters (0 at launch). parts: room for `splits` fp32 matrices [N][Hd] where dH's sum over the vocabulary is to
-// be split (splits > 1).
+// tile counters (0 at launch; ctr NULL: tiles at a fixed stride). parts: room for `splits` fp32 matrices [N][Hd] where
+// dH's sum over the vocabulary is to be split (splits > 1). fork: dW on a second stream beside dH.
 int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd, const __nv_bfloat16* dz,
                 int64_t ldz, int* ctr, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, float* parts, int splits,
-                int32_t* err, cudaStream_t st) {
+                bool fork_dw, int32_t* err, cudaStream_t st) {
   // 2. dH = dz·W: A = dz [N][V] (K-major, K = V); B = W [V][Hd] read MN-major; token-major tiles
   CUtensorMap mdz, mw_mn;
   if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
       !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
     return TT_ERR_CUDA;
   LhArgs b = lh_args(N, Hd, V, 0, err);
-  b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr + 1;
+  b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr ? ctr + 1 : nullptr;
   b.rows32 = rows_on_32(b.ob, 2 * Hd);
   if (splits > 1) {
     b.of = parts;
@@ -750,7 +750,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   else
     c.of = static_cast<float*>(d_w_vocab);
   c.rows32 = rows_on_32(d_w_vocab, (dw_bf16 ? 2 : 4) * Hd);
-  c.ldo = Hd; c.counter = ctr + 2;
+  c.ldo = Hd; c.counter = ctr ? ctr + 2 : nullptr;
   // dH and dW both only read dz: dW runs on a second stream forked after dz,
   // so that its CTAs (which claim tiles as they free up) take the SMs that
   // dH's last round of tiles (792 tiles of K = V at the benchmarked shape,
@@ -760,8 +760,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   cudaStream_t side = nullptr;
   cudaEvent_t fork = nullptr, join = nullptr;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  // (A split dH leaves none idle.)
-  const bool two = splits <= 1 && cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
+  const bool two = fork_dw && cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
                    cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking) == cudaSuccess &&
                    cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) == cudaSuccess &&
                    cudaEventCreateWithFlags(&join, cudaEventDisableTiming) == cudaSuccess &&
@@ -810,7 +809,7 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
   a.targets = targets; a.weights = weights; a.g = g; a.lse = lse; a.ob = dz; a.ldo = ldz; a.counter = ctr;
   rc = launch_gemm<EPI_DZ, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  return lh_products(hidden, w_vocab, N, V, Hd, dz, ldz, ctr, d_hidden, d_w_vocab, TT_DT_F32, nullptr, 1, err, st);
+  return lh_products(hidden, w_vocab, N, V, Hd, dz, ldz, ctr, d_hidden, d_w_vocab, TT_DT_F32, nullptr, 1, true, err, st);
 }
 
 TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V) {
@@ -893,16 +892,21 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
   int* ctr = ws_at<int>(ws, Lw.ctr);  // [3]: dz, dH, dW
-  if (cudaMemsetAsync(ctr, 0, 3 * sizeof(int), st) != cudaSuccess) return TT_ERR_CUDA;
   CUtensorMap mh, mw;
   if (!make_tmap_bf16(&mh, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ||
       !make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN))
     return TT_ERR_CUDA;
   LhArgs a = lh_args(N, V, Hd, 1, err);
+  // a product with a tile or less to an SM needs no claims: where all three have no more, no counters
+  const int64_t most = std::max(a.tiles, (V + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN));
+  if (most <= sm_count())
+    ctr = nullptr;
+  else if (cudaMemsetAsync(ctr, 0, 3 * sizeof(int), st) != cudaSuccess)
+    return TT_ERR_CUDA;
   a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
   a.ob = dz; a.ldo = Lw.ldz; a.counter = ctr; a.rows32 = rows_on_32(dz, 2 * Lw.ldz);
   rc = launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
   return lh_products(hidden, w_vocab, N, V, Hd, dz, Lw.ldz, ctr, d_hidden, d_w_vocab, dw_dtype,
-                     ws_at<float>(ws, Lw.parts), Lw.splits, err, st);
+                     ws_at<float>(ws, Lw.parts), Lw.splits, /*fork_dw=*/Lw.splits == 1 && ctr, err, st);
 }

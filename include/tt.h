@@ -128,7 +128,8 @@ TT_API int tt_tree_schedules(const void* ws, int64_t N, int32_t* send, int32_t* 
  *      dimensions contiguous), q_out likewise with q_out_ld; k, k_out with
  *      Hkv. All of type dtype (TT_DT_*). A tensor with 0 heads may be NULL.
  *      q_out may be q (with q_out_ld = q_ld), k_out may be k; other overlaps
- *      are not supported. Elements between the rows are neither read nor
+ *      of an output are not supported (TT_ERR_INVALID_ARG where one output
+ *      begins where the other tensor or output does). Elements between the rows are neither read nor
  *      written.
  *   pos: device int32 [axes][N] with axes pos_ld entries apart (>= N, or 0:
  *      every axis reads the same positions); any value, negative ones too.
@@ -452,7 +453,9 @@ TT_API int tt_token_logprob(const void* logits, int dtype, int64_t N, int64_t V,
  * forward's alternatives, or another model's; a repeated id adds up):
  *   dz_tv = p_tv·(dlse − dlogp − Σ_j dtop_j − dentropy·(log p_tv + entropy))
  *           + dlogp·[v == y_t] + Σ_j dtop_j·[v == top_ids_j].
- * lse: the forward's. dlogits: type and ld of logits; it may be logits itself
+ * lse: the forward's (from |lse| = 1024 on, where fp32 is too coarse for
+ * e^(z − lse), the row's own log-sum is taken again from the logits).
+ * dlogits: type and ld of logits; it may be logits itself
  * (overwritten), other overlaps are not supported; columns from V on are left
  * as they are. 0 <= k <= 32. An id outside [0, V) sets `err` =
  * TT_ERR_INVALID_ARG and its one-hot term is omitted. A masked logit gets 0
@@ -538,7 +541,8 @@ TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab
  *   dz_tv = p_tv·(dlse − dlogp − dentropy·(log p_tv + entropy)) + dlogp·[v == y_t],
  *   d_hidden = dz·W ([N][Hd] bf16), d_w_vocab = dzᵀ·H ([V][Hd] of type
  *   dw_dtype: TT_DT_F32 or TT_DT_BF16), both written.
- * lse, entropy: the forward's (entropy may be NULL without dentropy). dz is
+ * lse, entropy: the forward's (entropy may be NULL without dentropy). The
+ * outputs may not overlap the inputs. dz is
  * rounded to bf16 and kept in ws (tt_lmhead_token_logprob_bwd_workspace_bytes
  * bytes, 16-byte aligned), as in tt_lmhead_logprob_bwd; where N and Hd give
  * d_hidden few tiles, its sum over the vocabulary is split and the fp32 parts

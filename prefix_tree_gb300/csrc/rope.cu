@@ -199,6 +199,8 @@ TT_API int tt_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, c
     if ((reinterpret_cast<uintptr_t>(x[w]) | reinterpret_cast<uintptr_t>(y[w])) % es) return TT_ERR_INVALID_ARG;
     if (x[w] == y[w] && ld[w] != ldo[w]) return TT_ERR_INVALID_ARG;
   }
+  // q and k may each be turned in place, not into one another
+  if (Hq > 0 && Hkv > 0 && (q_out == k_out || q_out == k || k_out == q)) return TT_ERR_INVALID_ARG;
   if (!pos || (axes > 1 && pos_ld != 0 && pos_ld < N) || N > (int64_t)INT32_MAX) return TT_ERR_INVALID_ARG;
   a.N = N; a.d = d; a.half = rot / 2; a.pos = pos; a.pos_ld = pos_ld; a.adjacent = adjacent; a.inverse = inverse;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -145,6 +145,28 @@ def test_positions_of_a_tree(tt):
         assert torch.equal(got[rows], alone)
 
 
+def test_offsets_past_32_bits(tt):
+    """More than 2^31 elements before the last tokens: these equal the same tokens alone."""
+    N, hq, d = 420_001, 40, 128
+    q = torch.zeros(N, hq, d, dtype=torch.bfloat16, device="cuda")
+    q[-5:] = torch.randn(5, hq, d, device="cuda")
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    ref, _ = tt.rope(q[-5:].clone(), None, pos[-5:])
+    tt.rope(q, None, pos, out=(q, None))
+    assert torch.equal(q[-5:], ref) and not q[:100].any()
+
+
+def test_one_tensor_twice(tt):
+    """q and k the same tensor: fine into new tensors, refused in place (one would be turned twice)."""
+    q = torch.randn(9, 2, 64, device="cuda")
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    a, b = tt.rope(q, q, pos)
+    assert torch.equal(a, b)
+    with pytest.raises(tt.TTError) as e:
+        tt.rope(q, q, pos, out=(q, q))
+    assert e.value.code == -1
+
+
 def test_refusals(tt):
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     pos = torch.zeros(4, dtype=torch.int32, device="cuda")

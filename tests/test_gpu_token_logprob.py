@@ -372,6 +372,40 @@ def test_gradient_bad_ids(tt):
     assert int(err.item()) == -1
 
 
+def test_offsets_past_32_bits(tt):
+    """More than 2^31 logits before the last rows: these equal the same rows alone, forward, backward and in place."""
+    N, V = 14_200, 151_936
+    z = torch.zeros(N, V, dtype=torch.bfloat16, device="cuda")
+    z[-3:] = torch.randn(3, V, device="cuda") * 2
+    y = torch.arange(N, dtype=torch.int32, device="cuda")
+    g = torch.randn(N, device="cuda")
+    last = z[-3:].clone()
+    logp, h, lse, ids, top = tt.token_logprob(z, y, top_k=3)
+    r_logp, r_h, r_lse, r_ids, r_top = TL.token_logprob(_f64(last), y[-3:].cpu().numpy(), 3)
+    _close(logp[-3:], r_logp, 2e-4)
+    _close(lse[-3:], r_lse, 2e-4)
+    np.testing.assert_array_equal(ids[-3:].cpu().numpy(), r_ids)
+    dz = tt.token_logprob_bwd(last, lse[-3:], h[-3:], y[-3:], dlogp=g[-3:], dentropy=g[-3:])
+    tt.token_logprob_bwd(z, lse, h, y, dlogp=g, dentropy=g, out=z)
+    assert torch.equal(z[-3:], dz)
+
+
+def test_two_streams_at_once(tt):
+    """Calls that overlap share nothing."""
+    zs = [torch.randn(200, 20003, device="cuda").to(torch.bfloat16) for _ in range(4)]
+    ref = [tt.token_logprob(z, top_k=12) for z in zs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in zs]
+    got = [None] * 4
+    for _ in range(5):
+        for i, (s, z) in enumerate(zip(streams, zs)):
+            with torch.cuda.stream(s):
+                got[i] = tt.token_logprob(z, top_k=12)
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert all(torch.equal(x, w) for x, w in zip(a[1:], b[1:]))
+
+
 def test_rows_around_the_batch_stay(tt):
     """Columns from V on and rows outside the view are neither read into the results nor written."""
     buf = torch.full((7, 130), float("nan"), device="cuda", dtype=torch.bfloat16)

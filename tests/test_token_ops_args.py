@@ -16,8 +16,11 @@ def L():
     return lib()
 
 
+fake2 = ctypes.c_void_p(1 << 20)
+
+
 def _rope(L, **over):
-    a = dict(q=fake, qo=fake, q_ld=256, qo_ld=256, k=fake, ko=fake, k_ld=128, ko_ld=128, dt=0, N=5, hq=4, hkv=2, d=64,
+    a = dict(q=fake, qo=fake, q_ld=256, qo_ld=256, k=fake2, ko=fake2, k_ld=128, ko_ld=128, dt=0, N=5, hq=4, hkv=2, d=64,
              rot=64, pos=fake, pos_ld=5, axes=1, axis=(ctypes.c_uint8 * 128)(), freq=(ctypes.c_double * 128)(), adj=0,
              inv=0, st=None)
     a.update(over)
@@ -32,6 +35,7 @@ def _rope(L, **over):
     (dict(hq=1025), UNSUPPORTED), (dict(hkv=-1), BAD), (dict(q=None), BAD), (dict(ko=None), BAD),
     (dict(q_ld=255), BAD), (dict(ko_ld=127), BAD), (dict(q=odd), BAD), (dict(ko=odd), BAD), (dict(pos=None), BAD),
     (dict(qo_ld=320), BAD),                     # in place with another stride
+    (dict(ko=fake), BAD), (dict(qo=fake2), BAD), (dict(k=fake, ko=fake), BAD),  # one into the other
     (dict(axes=3, pos_ld=4), BAD),              # axes overlap
     (dict(axes=1, axis=(ctypes.c_uint8 * 128)(*[1] * 128)), BAD),
     (dict(freq=(ctypes.c_double * 128)(float("nan"))), BAD), (dict(freq=(ctypes.c_double * 128)(float("inf"))), BAD),

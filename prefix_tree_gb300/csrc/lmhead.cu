@@ -562,7 +562,7 @@ __device__ __forceinline__ void stat_merge(LhStat& a, const LhStat& b) {
   a.m = M;
 }
 // A block of 1024 threads takes ROWS consecutive rows and splits their tiles over 1024/ROWS threads each, four of a
-// thread's tiles under way at once; the threads' sums are joined pairwise. (61 rows of 594 tiles: ROWS = 8 4 us, 32
+// thread's tiles under way at once; the threads' sums are joined pairwise. (61 rows of 594 tiles: ROWS = 8 7 us, 32
 // 10 us, one tile at a time over 8 warps 57 us.)
 template <int ROWS>
 __global__ void __launch_bounds__(1024)
@@ -838,8 +838,8 @@ TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab
   a.pu = ws_at<float>(ws, Lw.pu);
   rc = launch_gemm<EPI_LSE_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  auto* combine = N <= 2048 ? lmhead_combine_entropy_kernel<8> : lmhead_combine_entropy_kernel<32>;
-  const int rows = N <= 2048 ? 8 : 32;
+  const int rows = N <= 512 ? 8 : 32;
+  auto* combine = rows == 8 ? lmhead_combine_entropy_kernel<8> : lmhead_combine_entropy_kernel<32>;
   combine<<<(unsigned)((N + rows - 1) / rows), 1024, 0, st>>>(a.pm, a.ps, a.pu, a.pz, N, a.nN, V, targets, logp, entropy,
                                                              lse, err);
   TT_LAUNCH_CHECK();

@@ -13,6 +13,9 @@ the tree-training pages:
   leaves accumulate into the shared prefix).
 * ``oracle.logprob``   — per-branch log-softmax loss averaged over branches and
   the equivalent per-token weighted loss ("Tree Training", Abstract).
+* ``oracle.rope``, ``oracle.token_logprob`` — rotary positions in front of the
+  attention; log-prob, entropy and top alternatives per token with their
+  gradient (operators beside the path).
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s CPU-baseline
 leg may import this package. It shares no code with the CUDA library

@@ -18,6 +18,14 @@
 //
 // Backward: dz_v = p_v·(g_lse − G − g_H·(logp_v + H)) + g_logp·[v = y] + Σ_j g_top_j·[v = id_j],
 // with G = g_logp + Σ_j g_top_j: one read and one write of the row.
+//
+// Bound by memory where rows are many and long: 12,669 x 151,936 bf16 (3.85
+// GB) in 564 us without alternatives, 580 with 8 (1.02 and 0.99 of the
+// measured copy rate), 632 with 20 (issue slots: about 34,000 warp
+// instructions a row for the pass, 500 for each alternative); the gradient
+// (7.7 GB) in 1125 us. Few or short rows are bound by latency: 4.6 us one row
+// in 8 CTAs, 9.3 with 20 alternatives (the joins and the sort); 60,000 rows of
+// 1000 in 42 and, with 8, 77 us.
 #include <cooperative_groups.h>
 
 #include <cuda_fp16.h>

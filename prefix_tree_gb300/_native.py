@@ -83,7 +83,7 @@ _SIGS = {
     "tt_lmhead_logprob": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tt_lmhead_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "tt_lmhead_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
-    "tt_lmhead_token_logprob_workspace_bytes": (_sz, [_i64, _i64]),
+    "tt_lmhead_token_logprob_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "tt_lmhead_token_logprob": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tt_lmhead_token_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "tt_lmhead_token_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int] + [_vp] * 8 + [_int, _vp, _sz, _vp, _vp]),
@@ -754,7 +754,7 @@ def lmhead_token_logprob(hidden, w_vocab, targets, out=None, ws=None, err=None):
         for t, n in ((logp, "logp"), (entropy, "entropy"), (lse, "lse")):
             _per_row(t, torch.float32, n, (N,), True)
     if ws is None:
-        ws = torch.empty(lib().tt_lmhead_token_logprob_workspace_bytes(N, V), dtype=torch.uint8, device=dev)
+        ws = torch.empty(lib().tt_lmhead_token_logprob_workspace_bytes(N, V, Hd), dtype=torch.uint8, device=dev)
     err = new_err(dev) if err is None else err
     _call("tt_lmhead_token_logprob", _device_of(hidden, w_vocab, targets, logp, entropy, lse, ws, err),
           hidden.data_ptr(), w_vocab.data_ptr(), N, V, Hd, targets.data_ptr(), logp.data_ptr(), entropy.data_ptr(),

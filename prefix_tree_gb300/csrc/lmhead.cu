@@ -125,6 +125,7 @@ struct LhArgs {
   const float *dlogp, *dentropy, *dlse;
   bool rows32;  // all stores but EPI_DZ's: rows of ob or of begin on 32-byte boundaries (whole sectors to a store)
   int splits;   // EPI_PART: ranges of K (tiles = nM·nN·splits)
+  int spread;   // EPI_LSE_H, EPI_DZ_H: A is a few rows laid out by K step, so many to a step (0: plain rows)
 };
 
 // 32 bytes in one store: a whole sector, which halves the L2 writes of a
@@ -236,12 +237,15 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
             ok = false;
             break;
           }
-          mbar_expect_tx(&bar[FULL + st], kABytes + kBBytes);
+          const bool spread = kEnt && a.spread;
+          mbar_expect_tx(&bar[FULL + st], (spread ? a.spread * kBK * 2 : kABytes) + kBBytes);
           uint8_t* sa = sm + L::a0 + st * kABytes;
           uint8_t* sb = sm + L::b0 + st * kBBytes;
           if (A_MN) {  // A stored [K][M]: two [64 K][64 M] boxes
 #pragma unroll
             for (int i = 0; i < kBM / 64; ++i) tma_load_2d(sa + i * kBox, &tmA, &bar[FULL + st], m * kBM + 64 * i, ks * kBK);
+          } else if (spread) {  // one [few rows][64 K] box; the tile's other rows give rows that nothing reads
+            tma_load_2d(sa, &tmA, &bar[FULL + st], 0, ks * a.spread);
           } else {  // A stored [M][K]: one [128 M][64 K] box
             tma_load_2d(sa, &tmA, &bar[FULL + st], ks * kBK, m * kBM);
           }
@@ -622,11 +626,33 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// A few rows of H laid out for the GEMM's CTAs, which all read the same ones: [K step][row][64] with each row of 128
+// bytes kSpreadPitch after the one before. Close together they lie in few slices of the L2 cache, whose queues then
+// hold up the reads of W as well (1 x 151,936 x 2048: 134 us, spread 99; 16 rows 116 and 101; from 32 rows on there is
+// no difference). Only where reading W takes long enough (134 MB, about 20 us) to pay for the copy's launch.
+constexpr int kSpreadRows = 31;
+constexpr int64_t kSpreadW = 1 << 26;  // entries of W
+constexpr int kSpreadPitch = 4096 + 128;
+inline int spread_rows(int64_t N, int64_t V, int Hd) {
+  return N <= kSpreadRows && V * Hd >= kSpreadW ? (int)((N + 7) / 8 * 8) : 0;
+}
+inline size_t spread_bytes(int64_t N, int64_t V, int Hd) {
+  return (size_t)spread_rows(N, V, Hd) * (size_t)(Hd / kBK) * kSpreadPitch;
+}
+__global__ void __launch_bounds__(256) lmhead_spread_kernel(const __nv_bfloat16* h, int N, int Hd, int rows, char* out) {
+  const int i = blockIdx.x * 256 + threadIdx.x;  // 16-byte vectors: 8 to a row of a step
+  if (i >= Hd / kBK * rows * 8) return;
+  const int line = i / 8, ks = line / rows, r = line - ks * rows;
+  const uint4 v = r < N ? *reinterpret_cast<const uint4*>(h + (int64_t)r * Hd + ks * kBK + (i % 8) * 8)
+                        : make_uint4(0, 0, 0, 0);
+  *reinterpret_cast<uint4*>(out + (int64_t)line * kSpreadPitch + (i % 8) * 16) = v;
+}
+
 struct LhWs {
   size_t pm, ps, pz, total;
-  size_t pu, total_u;  // with the entropy sums behind the rest
+  size_t pu, spread, total_u;  // with the entropy sums and the spread rows behind the rest
 };
-LhWs lh_layout(int64_t N, int64_t V) {
+LhWs lh_layout(int64_t N, int64_t V, int Hd = 0) {
   const int64_t nV = (V + kBN - 1) / kBN;
   LhWs w;
   size_t o = 0;
@@ -636,6 +662,7 @@ LhWs lh_layout(int64_t N, int64_t V) {
   w.pz = take(sizeof(float) * (size_t)N);
   w.total = o;
   w.pu = take(sizeof(float) * (size_t)nV * (size_t)N);
+  w.spread = take(spread_bytes(N, V, Hd));
   w.total_u = o;
   return w;
 }
@@ -822,9 +849,23 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
   return lh_products(hidden, w_vocab, N, V, Hd, dz, ldz, ctr, d_hidden, d_w_vocab, TT_DT_F32, nullptr, 1, true, err, st);
 }
 
-TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V) {
-  if (N < 1 || V < 1) return 0;
-  return lh_layout(N, V).total_u;
+namespace {
+// The tensor map of H for the z product: plain rows, or the few rows spread into `room` first.
+int map_hidden(const tt_bf16* hidden, int64_t N, int64_t V, int Hd, void* room, LhArgs* a, CUtensorMap* map, cudaStream_t st) {
+  a->spread = spread_rows(N, V, Hd);
+  if (!a->spread)
+    return make_tmap_bf16(map, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ? TT_OK : TT_ERR_CUDA;
+  const int lines = Hd / kBK * a->spread;
+  lmhead_spread_kernel<<<(lines * 8 + 255) / 256, 256, 0, st>>>(reinterpret_cast<const __nv_bfloat16*>(hidden), (int)N,
+                                                               Hd, a->spread, static_cast<char*>(room));
+  if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
+  return make_tmap_bf16_ld(map, room, kBK, (uint64_t)lines, kSpreadPitch / 2, (uint32_t)a->spread) ? TT_OK : TT_ERR_CUDA;
+}
+}  // namespace
+
+TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V, int Hd) {
+  if (N < 1 || V < 1 || Hd < 1) return 0;
+  return lh_layout(N, V, Hd).total_u;
 }
 
 TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
@@ -833,14 +874,13 @@ TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab
   int rc = lh_check(hidden, w_vocab, N, V, Hd, targets, err);
   if (rc) return rc;
   if (!logp || !entropy || !lse || !ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
-  const LhWs Lw = lh_layout(N, V);
+  const LhWs Lw = lh_layout(N, V, Hd);
   if (ws_bytes < Lw.total_u) return TT_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   CUtensorMap mh, mw;
-  if (!make_tmap_bf16(&mh, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ||
-      !make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN))
-    return TT_ERR_CUDA;
+  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN)) return TT_ERR_CUDA;
   LhArgs a = lh_args(N, V, Hd, 1, err);
+  if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
   a.targets = targets;
   a.pm = ws_at<float>(ws, Lw.pm);
   a.ps = ws_at<float>(ws, Lw.ps);
@@ -868,7 +908,7 @@ constexpr int kSplitSms = 152;
 struct LhBwdWs {
   int64_t ldz;
   int splits;
-  size_t ctr, parts, total;
+  size_t ctr, spread, parts, total;
 };
 LhBwdWs lh_bwd_layout(int64_t N, int64_t V, int Hd) {
   LhBwdWs w;
@@ -876,7 +916,8 @@ LhBwdWs lh_bwd_layout(int64_t N, int64_t V, int Hd) {
   const int64_t tiles = (N + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN), ksteps = (V + kBK - 1) / kBK;
   w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSplitSms / tiles, ksteps / 8));
   w.ctr = align_up((size_t)N * (size_t)w.ldz * 2, 256);
-  w.parts = w.ctr + 256;
+  w.spread = w.ctr + 256;
+  w.parts = w.spread + align_up(spread_bytes(N, V, Hd), 256);
   w.total = w.parts + (w.splits > 1 ? sizeof(float) * (size_t)w.splits * (size_t)N * (size_t)Hd : 0);
   return w;
 }
@@ -903,10 +944,9 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
   __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
   int* ctr = ws_at<int>(ws, Lw.ctr);  // [3]: dz, dH, dW
   CUtensorMap mh, mw;
-  if (!make_tmap_bf16(&mh, hidden, (uint64_t)Hd, (uint64_t)N, kBM) ||
-      !make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN))
-    return TT_ERR_CUDA;
+  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN)) return TT_ERR_CUDA;
   LhArgs a = lh_args(N, V, Hd, 1, err);
+  if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
   // a product with a tile or less to an SM needs no claims: where all three have no more, no counters
   const int64_t most = std::max(a.tiles, (V + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN));
   if (most <= sm_count())

@@ -65,6 +65,31 @@ def test_backward(tt, N, V, Hd, dw_dtype):
     assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("N", [1, 5, 8, 31, 32])
+def test_few_rows_of_a_large_head(tt, N):
+    """Where W is large and the rows few (up to 31), the rows are laid out apart for the product: against fp64, and the
+    backward's two products against the dz of the definition; repeatable, with a workspace exactly as large as asked."""
+    V, Hd = 70_001, 1024
+    g = torch.Generator(device="cuda").manual_seed(N)
+    H = torch.randn(N, Hd, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(V, Hd, generator=g, device="cuda") * (2 / 32)).to(torch.bfloat16)
+    y = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    ws = torch.empty(tt.lib().tt_lmhead_token_logprob_workspace_bytes(N, V, Hd), dtype=torch.uint8, device="cuda")
+    logp, h, lse = tt.lmhead_token_logprob(H, W, y, ws=ws)
+    z = (H.double() @ W.double().T).cpu().numpy()
+    r_logp, r_h, r_lse, _, _ = TL.token_logprob(z, y.cpu().numpy())
+    assert np.abs(dev_to_f64(logp) - r_logp).max() <= LOGP_ATOL and np.abs(dev_to_f64(lse) - r_lse).max() <= LOGP_ATOL
+    assert (np.abs(dev_to_f64(h) - r_h) <= LOGP_ATOL * (1 + np.abs(r_lse - z.max(1) - r_h))).all()
+    dl, de = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de)
+    dz = torch.from_numpy(TL.token_logprob_grad(z, y.cpu().numpy(), dev_to_f64(dl), dev_to_f64(de))).cuda()
+    assert rel_l2(dev_to_f64(dh), (dz @ W.double()).cpu().numpy()) <= GRAD_RL2
+    r_dw = dz.T @ H.double()
+    assert ((dw.double() - r_dw).norm() / r_dw.norm()).item() <= GRAD_RL2
+    again = tt.lmhead_token_logprob(H, W, y) + tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de)
+    assert all(torch.equal(a, b) for a, b in zip(again, (logp, h, lse, dh, dw)))
+
+
 @pytest.mark.parametrize("N,V,Hd", [(1, 9000, 64), (61, 32003, 512), (129, 5003, 1024), (130, 20001, 256)])
 def test_backward_of_few_rows(tt, N, V, Hd):
     """Few tiles of d_hidden: its sum over the vocabulary is split over the SMs. Tolerance as test_backward; a

@@ -78,7 +78,7 @@ def test_token_logprob_bwd_arguments(L, over, code):
 
 def test_lmhead_token_logprob_arguments(L):
     nb = L.tt_lmhead_token_logprob_workspace_bytes
-    assert nb(0, 5) == 0 and nb(300, 1000) >= 12 * 300 * 4 + 4 * 300
+    assert nb(0, 5, 64) == nb(5, 5, 0) == 0 and nb(300, 1000, 64) >= 12 * 300 * 4 + 4 * 300
     bwd_bytes = L.tt_lmhead_token_logprob_bwd_workspace_bytes
     assert bwd_bytes(0, 1000, 128) == 0 and bwd_bytes(300, 1000, 128) >= 300 * 1000 * 2
     big = 1 << 40

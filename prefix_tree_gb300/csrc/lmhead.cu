@@ -136,7 +136,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+// BN: columns of a tile (kBN, or half where whole tiles would leave most SMs without one).
+template <int EPI, bool A_MN, bool B_MN, int BN>
 __global__ void __launch_bounds__(kLhWarps * 32, 1)
     lmhead_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const LhArgs a) {
@@ -208,6 +209,9 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
     }
   };
 
+  // the [64][64] boxes of an MN-major B that hold columns (the last tile of Hd columns may have fewer than BN)
+  auto tile_boxes = [&](int n) -> uint32_t { return (uint32_t)min((int64_t)(BN / 64), (a.Ncols - (int64_t)n * BN + 63) / 64); };
+
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -231,6 +235,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         int m, n, k0, k1;
         tile_mn(t, m, n);
         k_range(t, k0, k1);
+        const uint32_t boxes = tile_boxes(n);
         for (int ks = k0; ks < k1; ++ks, ++kk) {
           const int st = (int)(kk % kStages);
           if (kk >= kStages && !mbar_wait(&bar[EMPTY + st], (uint32_t)((kk / kStages - 1) & 1), abort_flag, 1)) {
@@ -238,7 +243,8 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
             break;
           }
           const bool spread = kEnt && a.spread;
-          mbar_expect_tx(&bar[FULL + st], (spread ? a.spread * kBK * 2 : kABytes) + kBBytes);
+          mbar_expect_tx(&bar[FULL + st],
+                         (spread ? a.spread * kBK * 2 : kABytes) + (B_MN ? boxes * kBox : (uint32_t)BN * kBK * 2));
           uint8_t* sa = sm + L::a0 + st * kABytes;
           uint8_t* sb = sm + L::b0 + st * kBBytes;
           if (A_MN) {  // A stored [K][M]: two [64 K][64 M] boxes
@@ -249,11 +255,12 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
           } else {  // A stored [M][K]: one [128 M][64 K] box
             tma_load_2d(sa, &tmA, &bar[FULL + st], ks * kBK, m * kBM);
           }
-          if (B_MN) {  // B stored [K][N]: four [64 K][64 N] boxes
+          if (B_MN) {  // B stored [K][N]: up to four [64 K][64 N] boxes
 #pragma unroll
-            for (int i = 0; i < kBN / 64; ++i) tma_load_2d(sb + i * kBox, &tmB, &bar[FULL + st], n * kBN + 64 * i, ks * kBK);
-          } else {  // B stored [N][K]: one [256 N][64 K] box
-            tma_load_2d(sb, &tmB, &bar[FULL + st], ks * kBK, n * kBN);
+            for (int i = 0; i < BN / 64; ++i)
+              if (i < boxes) tma_load_2d(sb + i * kBox, &tmB, &bar[FULL + st], n * BN + 64 * i, ks * kBK);
+          } else {  // B stored [N][K]: one [BN][64 K] box
+            tma_load_2d(sb, &tmB, &bar[FULL + st], ks * kBK, n * BN);
           }
         }
       }
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(kBM, kBN, A_MN ? 1 : 0, B_MN ? 1 : 0);
+      constexpr uint32_t whole = idesc_bf16(kBM, BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
       // K-major: 128-byte rows of K, 8-row groups 1024 bytes apart, K = 16 is 32 bytes on.
       // MN-major: 64-column boxes kBox apart, 8 K rows 1024 bytes apart, K = 16 is 2048 bytes on.
       const uint64_t da = A_MN ? smem_desc(smem_u32(sm + L::a0), kBox, 1024) : smem_desc(smem_u32(sm + L::a0), 16, 1024);
@@ -279,9 +286,15 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         // the epilogue has read this accumulator's previous tile (it − 2)
         if (it >= 2 && !mbar_wait(&bar[ACC_EMPTY + acc], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, 2)) break;
         tc_fence_after();
-        const uint32_t dcol = tbase + (uint32_t)acc * kBN;
+        const uint32_t dcol = tbase + (uint32_t)acc * BN;
         int k0, k1;
         k_range(t, k0, k1);
+        uint32_t idesc = whole;
+        if (B_MN) {  // N = the columns that are there
+          int m, n;
+          tile_mn(t, m, n);
+          idesc = idesc_bf16(kBM, 64, A_MN ? 1 : 0, 1) + ((tile_boxes(n) - 1) * 64 / 8 << 17);
+        }
         for (int ks = k0; ks < k1; ++ks, ++kk) {
           const int st = (int)(kk % kStages);
           if (!mbar_wait(&bar[FULL + st], (uint32_t)((kk / kStages) & 1), abort_flag, 3)) {
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       int m, n;
       tile_mn(t, m, n);
       const int64_t row = (int64_t)m * kBM + rl;
-      const int64_t c0 = (int64_t)n * kBN;  // first column of the tile
+      const int64_t c0 = (int64_t)n * BN;  // first column of the tile
       const bool row_ok = row < a.M;
       int y = -1;
       float gw = 0.f, lrow = 0.f;
@@ -340,13 +353,14 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       float m_run = -INFINITY, s_run = 0.f, u_run = 0.f, zt = 0.f;
       bool found = false;
 #pragma unroll 1
-      for (int c = 0; c < kBN / 32; ++c) {
-        uint32_t u[32];
-        tmem_ld32(tbase + lane_base + (uint32_t)acc * kBN + c * 32, u);
-        tmem_ld_wait();
-        tmem_pin(u);
+      for (int c = 0; c < BN / 32; ++c) {
         const int64_t col0 = c0 + c * 32;
         const int64_t nvalid = a.Ncols - col0;  // columns j < nvalid exist
+        if ((B_MN || kEnt) && nvalid <= 0) break;
+        uint32_t u[32];
+        tmem_ld32(tbase + lane_base + (uint32_t)acc * BN + c * 32, u);
+        tmem_ld_wait();
+        tmem_pin(u);
         if (kLse) {
           float cm = -INFINITY;
           if (kEnt) {
@@ -503,14 +517,14 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
 }
 
 // One persistent launch (one CTA per SM, at most one per tile).
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, int BN = kBN>
 int launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const LhArgs& a, cudaStream_t st) {
   const int smem = (int)LhSmem::total;
-  if (!smem_attr_set<lmhead_gemm_kernel<EPI, A_MN, B_MN>>(smem)) return TT_ERR_CUDA;
+  if (!smem_attr_set<lmhead_gemm_kernel<EPI, A_MN, B_MN, BN>>(smem)) return TT_ERR_CUDA;
   const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)sm_count());
   {
     KtScope kt(TT_KT_LMHEAD, st);
-    lmhead_gemm_kernel<EPI, A_MN, B_MN><<<(unsigned)grid, kLhWarps * 32, smem, st>>>(ta, tb, a);
+    lmhead_gemm_kernel<EPI, A_MN, B_MN, BN><<<(unsigned)grid, kLhWarps * 32, smem, st>>>(ta, tb, a);
   }
   return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
@@ -652,8 +666,14 @@ struct LhWs {
   size_t pm, ps, pz, total;
   size_t pu, spread, total_u;  // with the entropy sums and the spread rows behind the rest
 };
-LhWs lh_layout(int64_t N, int64_t V, int Hd = 0) {
-  const int64_t nV = (V + kBN - 1) / kBN;
+// Tiles of half the columns for the z product where whole ones would not give half the SMs (of kSplitSms) one each:
+// 374 x 2150 x 1728, 27 tiles: 15.5 us, with 51 half tiles 13.1; 28 x 14,782 x 448, 58 tiles: 9.6 and 8.9.
+constexpr int kSplitSms = 152;
+inline bool half_tiles(int64_t N, int64_t V) {
+  return (N + kBM - 1) / kBM * ((V + kBN - 1) / kBN) <= kSplitSms / 2;
+}
+LhWs lh_layout(int64_t N, int64_t V, int Hd = 0, int BN = kBN) {
+  const int64_t nV = (V + BN - 1) / BN;
   LhWs w;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes, 256); return r; };
@@ -678,11 +698,11 @@ TT_API size_t tt_lmhead_logprob_workspace_bytes(int64_t N, int64_t V) {
 }
 
 namespace {
-LhArgs lh_args(int64_t M, int64_t Ncols, int64_t K, int n_outer, int32_t* err) {
+LhArgs lh_args(int64_t M, int64_t Ncols, int64_t K, int n_outer, int32_t* err, int BN = kBN) {
   LhArgs a = {};
   a.M = M; a.Ncols = Ncols; a.ksteps = (int)((K + kBK - 1) / kBK);
   a.nM = (int)((M + kBM - 1) / kBM);
-  a.nN = (int)((Ncols + kBN - 1) / kBN);
+  a.nN = (int)((Ncols + BN - 1) / BN);
   a.tiles = (int64_t)a.nM * a.nN;
   a.n_outer = n_outer;
   a.err = err;
@@ -737,18 +757,35 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
   return dz_bytes(N, V) + 256;
 }
 
-// The sum of a split product's parts [splits][n] in their order, to bf16 (n a multiple of 4).
-__global__ void __launch_bounds__(256) lmhead_sum_parts_kernel(const float* part, int64_t n, int splits,
-                                                               __nv_bfloat16* out) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
+// The sum of a split product's parts [splits][n], to bf16 (n a multiple of 4). Four entries to a thread; WARPS > 1: the
+// warps of a block share the parts of 128 entries, and their sums are joined in warp order. Many parts (then there are
+// few entries): 16 warps, 3 x 384 entries of 152 parts 4.0 us, with one 21; few parts: one, 374 x 1728 entries of 4
+// parts 4.7 us, with 16 11.8.
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS)
+    lmhead_sum_parts_kernel(const float* part, int64_t n, int splits, __nv_bfloat16* out) {
+  __shared__ float4 sums[WARPS][32];
+  const int lane = threadIdx.x & 31, w = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const int64_t i = (WARPS == 1 ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)blockIdx.x * 32 + lane) * 4;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < n) {
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 p = *reinterpret_cast<const float4*>(part + s * n + i);
-    t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+    for (int s = w; s < splits; s += WARPS) {
+      const float4 p = *reinterpret_cast<const float4*>(part + s * n + i);
+      t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+    }
   }
-  *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+  if constexpr (WARPS > 1) {
+    sums[w][lane] = t;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+      const float4 p = sums[k][lane];
+      t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+    }
+  }
+  if (i < n) *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
 }
 
 namespace {
@@ -807,7 +844,10 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
                       : launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
   if (!rc && splits > 1) {
     const int64_t n = N * Hd;
-    lmhead_sum_parts_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(parts, n, splits, b.ob);
+    if (splits >= 16)
+      lmhead_sum_parts_kernel<16><<<(unsigned)((n + 127) / 128), 512, 0, st>>>(parts, n, splits, b.ob);
+    else
+      lmhead_sum_parts_kernel<1><<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(parts, n, splits, b.ob);
     if (cudaGetLastError() != cudaSuccess) rc = TT_ERR_CUDA;
   }
   int rc2 = rc;
@@ -865,7 +905,7 @@ int map_hidden(const tt_bf16* hidden, int64_t N, int64_t V, int Hd, void* room, 
 
 TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V, int Hd) {
   if (N < 1 || V < 1 || Hd < 1) return 0;
-  return lh_layout(N, V, Hd).total_u;
+  return lh_layout(N, V, Hd, half_tiles(N, V) ? kBN / 2 : kBN).total_u;
 }
 
 TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
@@ -874,19 +914,22 @@ TT_API int tt_lmhead_token_logprob(const tt_bf16* hidden, const tt_bf16* w_vocab
   int rc = lh_check(hidden, w_vocab, N, V, Hd, targets, err);
   if (rc) return rc;
   if (!logp || !entropy || !lse || !ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
-  const LhWs Lw = lh_layout(N, V, Hd);
+  const bool half = half_tiles(N, V);
+  const int BN = half ? kBN / 2 : kBN;
+  const LhWs Lw = lh_layout(N, V, Hd, BN);
   if (ws_bytes < Lw.total_u) return TT_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   CUtensorMap mh, mw;
-  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN)) return TT_ERR_CUDA;
-  LhArgs a = lh_args(N, V, Hd, 1, err);
+  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, BN)) return TT_ERR_CUDA;
+  LhArgs a = lh_args(N, V, Hd, 1, err, BN);
   if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
   a.targets = targets;
   a.pm = ws_at<float>(ws, Lw.pm);
   a.ps = ws_at<float>(ws, Lw.ps);
   a.pz = ws_at<float>(ws, Lw.pz);
   a.pu = ws_at<float>(ws, Lw.pu);
-  rc = launch_gemm<EPI_LSE_H, false, false>(mh, mw, a, st);
+  rc = half ? launch_gemm<EPI_LSE_H, false, false, kBN / 2>(mh, mw, a, st)
+            : launch_gemm<EPI_LSE_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
   const int rows = N <= 512 ? 8 : 32;
   auto* combine = rows == 8 ? lmhead_combine_entropy_kernel<8> : lmhead_combine_entropy_kernel<32>;
@@ -904,7 +947,6 @@ namespace {
 // steps or more (61 x 151,936 x 2048: 8 tiles alone take 790 us). The split
 // goes by sizes alone, on any device as on one of kSplitSms SMs: the
 // workspace and the order of the sums do not depend on the device.
-constexpr int kSplitSms = 152;
 struct LhBwdWs {
   int64_t ldz;
   int splits;
@@ -944,8 +986,10 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
   __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
   int* ctr = ws_at<int>(ws, Lw.ctr);  // [3]: dz, dH, dW
   CUtensorMap mh, mw;
-  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, kBN)) return TT_ERR_CUDA;
-  LhArgs a = lh_args(N, V, Hd, 1, err);
+  const bool half = half_tiles(N, V);
+  const int BN = half ? kBN / 2 : kBN;
+  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, BN)) return TT_ERR_CUDA;
+  LhArgs a = lh_args(N, V, Hd, 1, err, BN);
   if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
   // a product with a tile or less to an SM needs no claims: where all three have no more, no counters
   const int64_t most = std::max(a.tiles, (V + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN));
@@ -955,7 +999,8 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
     return TT_ERR_CUDA;
   a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
   a.ob = dz; a.ldo = Lw.ldz; a.counter = ctr; a.rows32 = rows_on_32(dz, 2 * Lw.ldz);
-  rc = launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
+  rc = half ? launch_gemm<EPI_DZ_H, false, false, kBN / 2>(mh, mw, a, st)
+            : launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
   return lh_products(hidden, w_vocab, N, V, Hd, dz, Lw.ldz, ctr, d_hidden, d_w_vocab, dw_dtype,
                      ws_at<float>(ws, Lw.parts), Lw.splits, /*fork_dw=*/Lw.splits == 1 && ctr, err, st);

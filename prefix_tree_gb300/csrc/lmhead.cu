@@ -45,7 +45,12 @@
 // An MN-major operand is staged as [64 K rows][64 M-or-N columns] boxes with
 // 128-byte swizzle: the UMMA descriptor's leading offset is one box (8 KB,
 // the next 64 columns), its stride 1024 bytes (8 K rows), and each K = 16
-// step advances 2048 bytes.
+// step advances 2048 bytes. dH and dW with long sums go by pairs of CTAs
+// (by_pairs): a tile of 256 x 256 on two SMs' tensor cores, each SM holding
+// its 128 rows of A and half of B, 32 KB a K step instead of 48. The sums run
+// in the same order: the same bits as without. The whole backward (dz, dH,
+// dW) went 547 -> 496 us at 4001 x 32,003 x 1024, 16.1 -> 14.5 ms at
+// 12,669 x 151,936 x 2048.
 //
 // With the entropy (tt_lmhead_token_logprob and its backward): the same
 // kernel with two more epilogues. EPI_LSE_H carries u = Σ 2^x·x, x = (z −
@@ -57,6 +62,7 @@
 // last tile). An epilogue tile takes 2.1 us (EPI_DZ_H 2.8), so up to Hd = 256
 // it bounds the GEMM, above it the tensor pipe (80 % busy at Hd = 1024).
 #include <algorithm>
+#include <atomic>
 
 #include "tc_common.cuh"
 
@@ -64,6 +70,53 @@ namespace tt {
 namespace {
 
 using namespace tc;
+
+// ------------------------------------------------------------------ a pair of CTAs (cta_group::2)
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (+)= A·B over both CTAs: each holds its rows of A and D and half the columns of B, at the same places.
+__device__ __forceinline__ void umma_ss_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once the tcgen05 operations issued so far by this thread complete.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// TMA load into this CTA's shared memory that signals a barrier of either CTA (an address of the cluster).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same without the writes before it (the reader takes tensor memory or a freed slot only).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+// After a wait that another CTA's arrival ended: what that CTA did before it is seen.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 constexpr int kLhWarps = 6;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
@@ -88,15 +141,25 @@ constexpr float kNoColumn = -1e30f;
 // TILE_FULL[r] / TILE_EMPTY[r]: the tile index in ring slot r published by
 // the producer / read by the MMA thread and the 128 epilogue threads.
 constexpr int kTileRing = 4;
-constexpr int FULL = 0, EMPTY = FULL + kStages, ACC_FULL = EMPTY + kStages, ACC_EMPTY = ACC_FULL + 2,
-              FINAL = ACC_EMPTY + 2, TILE_FULL = FINAL + 1, TILE_EMPTY = TILE_FULL + kTileRing,
-              NBAR = TILE_EMPTY + kTileRing;
+template <int STAGES>
+struct LhBars {
+  static constexpr int FULL = 0, EMPTY = FULL + STAGES, ACC_FULL = EMPTY + STAGES, ACC_EMPTY = ACC_FULL + 2,
+                       FINAL = ACC_EMPTY + 2, TILE_FULL = FINAL + 1, TILE_EMPTY = TILE_FULL + kTileRing,
+                       NBAR = TILE_EMPTY + kTileRing;
+};
+// A pair of CTAs (a cluster of two, tcgen05 cta_group::2) on one tile of 256
+// rows: each holds its 128 rows of A and half the columns of B, so that a K
+// step brings 32 KB into an SM instead of 48. The stages are as many as fit.
+constexpr int kPairStages = 6;
+constexpr int kPairSteps = 32;  // the least K steps to a tile (by_pairs)
+constexpr uint32_t kPairBBytes = kBBytes / 2;
+static_assert(kPairStages * (kABytes + kPairBBytes) == kStages * (kABytes + kBBytes) &&
+                  LhBars<kStages>::NBAR <= LhBars<kPairStages>::NBAR, "one layout for both");
 
 struct LhSmem {
   static constexpr uint32_t a0 = 0;
-  static constexpr uint32_t b0 = a0 + kStages * kABytes;
-  static constexpr uint32_t bars = b0 + kStages * kBBytes;
-  static constexpr uint32_t ring = bars + NBAR * 8;  // [kTileRing] int64 tile indices
+  static constexpr uint32_t bars = a0 + kStages * (kABytes + kBBytes);
+  static constexpr uint32_t ring = bars + LhBars<kPairStages>::NBAR * 8;  // [kTileRing] int64 tile indices
   static constexpr uint32_t misc = ring + kTileRing * 8;
   static constexpr uint32_t total = misc + 16 + 1024;  // + slack for 1024-byte alignment
 };
@@ -137,13 +200,24 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 }
 
 // BN: columns of a tile (kBN, or half where whole tiles would leave most SMs without one).
-template <int EPI, bool A_MN, bool B_MN, int BN>
+template <int EPI, bool A_MN, bool B_MN, int BN, bool PAIR>
 __global__ void __launch_bounds__(kLhWarps * 32, 1)
     lmhead_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const LhArgs a) {
   using L = LhSmem;
   constexpr bool kLse = EPI == EPI_LSE || EPI == EPI_LSE_H, kDz = EPI == EPI_DZ || EPI == EPI_DZ_H;
   constexpr bool kEnt = EPI == EPI_LSE_H || EPI == EPI_DZ_H;
+  // PAIR: CTA 0 of the pair leads: its FULL barriers count both CTAs' copies, its MMA thread issues for both, its
+  // ACC_EMPTY and TILE_EMPTY barriers take both CTAs' arrivals; EMPTY, ACC_FULL and FINAL are committed to both.
+  constexpr int kStages = PAIR ? kPairStages : tt::kStages;
+  constexpr uint32_t kBBytes = PAIR ? kPairBBytes : tt::kBBytes;
+  constexpr uint32_t b0 = L::a0 + kStages * kABytes;
+  constexpr int kTileM = PAIR ? 2 * kBM : kBM, kCtas = PAIR ? 2 : 1;
+  constexpr int kOwnN = BN / kCtas;  // columns of B that a CTA holds
+  using Bar = LhBars<kStages>;
+  constexpr int FULL = Bar::FULL, EMPTY = Bar::EMPTY, ACC_FULL = Bar::ACC_FULL, ACC_EMPTY = Bar::ACC_EMPTY,
+                FINAL = Bar::FINAL, TILE_FULL = Bar::TILE_FULL, TILE_EMPTY = Bar::TILE_EMPTY;
+  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;  // clusters are consecutive CTAs
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::bars);
@@ -158,22 +232,45 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar[ACC_FULL + i], 1);
-      mbar_init(&bar[ACC_EMPTY + i], 128);
+      mbar_init(&bar[ACC_EMPTY + i], PAIR ? 2 * 4 : 128);  // PAIR: one arrival of each epilogue warp
     }
     mbar_init(&bar[FINAL], 1);
     for (int i = 0; i < kTileRing; ++i) {
       mbar_init(&bar[TILE_FULL + i], 1);
-      mbar_init(&bar[TILE_EMPTY + i], 1 + 128);
+      mbar_init(&bar[TILE_EMPTY + i], PAIR ? 2 * (1 + 4) : 1 + 128);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+    else
+      tmem_alloc(tmem_slot, kTmemCols);
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_barrier();  // the leader's barriers are there before the other CTA's copies signal them
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const int64_t t_first = blockIdx.x, t_step = gridDim.x;
+  const int64_t t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
+  // the leader's barrier (PAIR: as an address of the cluster)
+  auto lead = [&](int b) { return dsmem_addr(smem_u32(&bar[b]), 0); };
+  // the arrival of a thread, or (whole) of a warp whose lanes are all done
+  auto arrive_lead = [&](int b, bool whole) {
+    if constexpr (PAIR) {
+      if (whole) __syncwarp();
+      if (!whole || lane == 0) mbar_arrive_remote(lead(b));
+    } else {
+      mbar_arrive(&bar[b]);
+    }
+  };
+  // a wait; PAIR: an epilogue warp's lanes give up together, so that its __syncwarp meets them all
+  auto wait = [&](uint64_t* b, uint32_t parity, int site) {
+    bool ok = mbar_wait(b, parity, abort_flag, site);
+    if (PAIR && warp >= 2) ok = __all_sync(~0u, ok);
+    return ok;
+  };
   volatile int64_t* ring = reinterpret_cast<volatile int64_t*>(sm + L::ring);
   // the tile of this CTA's it-th turn (a value >= tiles ends the loop): with
   // a counter, published by the producer through the ring; else fixed stride
@@ -183,9 +280,10 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       return true;
     }
     const int r = it % kTileRing;
-    if (!mbar_wait(&bar[TILE_FULL + r], (uint32_t)((it / kTileRing) & 1), abort_flag, site)) return false;
+    if (!wait(&bar[TILE_FULL + r], (uint32_t)((it / kTileRing) & 1), site)) return false;
+    if constexpr (PAIR) fence_cluster();
     t = ring[r];
-    mbar_arrive(&bar[TILE_EMPTY + r]);
+    arrive_lead(TILE_EMPTY + r, /*whole=*/warp >= 2);
     return true;
   };
   // the K steps of a tile
@@ -210,7 +308,10 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
   };
 
   // the [64][64] boxes of an MN-major B that hold columns (the last tile of Hd columns may have fewer than BN)
-  auto tile_boxes = [&](int n) -> uint32_t { return (uint32_t)min((int64_t)(BN / 64), (a.Ncols - (int64_t)n * BN + 63) / 64); };
+  // (A pair always takes all: columns past the last read 0.)
+  auto tile_boxes = [&](int n) -> uint32_t {
+    return PAIR ? kOwnN / 64 : (uint32_t)min((int64_t)(BN / 64), (a.Ncols - (int64_t)n * BN + 63) / 64);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -221,14 +322,21 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       bool ok = true;
       for (int it = 0; ok; ++it) {
         int64_t t = t_first + (int64_t)it * t_step;
-        if (a.counter) {
-          // claim the next tile and publish it to the MMA thread and the epilogue
+        if (PAIR && rank != 0) {
+          if (!take_tile(it, t, 8)) break;
+        } else if (a.counter) {
+          // claim the next tile and publish it to the MMA thread and the epilogue (PAIR: of both CTAs, and the other's
+          // producer)
           const int r = it % kTileRing;
           if (it >= kTileRing &&
               !mbar_wait(&bar[TILE_EMPTY + r], (uint32_t)((it / kTileRing - 1) & 1), abort_flag, 5))
             break;
           t = (int64_t)atomicAdd(a.counter, 1);
           ring[r] = t;
+          if constexpr (PAIR) {
+            st_cluster_u64(dsmem_addr(smem_u32(const_cast<const int64_t*>(&ring[r])), 1), (uint64_t)t);
+            mbar_arrive_cluster(dsmem_addr(smem_u32(&bar[TILE_FULL + r]), 1));
+          }
           mbar_arrive(&bar[TILE_FULL + r]);
         }
         if (t >= a.tiles) break;
@@ -243,39 +351,56 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
             break;
           }
           const bool spread = kEnt && a.spread;
-          mbar_expect_tx(&bar[FULL + st],
-                         (spread ? a.spread * kBK * 2 : kABytes) + (B_MN ? boxes * kBox : (uint32_t)BN * kBK * 2));
+          if (rank == 0)
+            mbar_expect_tx(&bar[FULL + st], kCtas * ((spread ? a.spread * kBK * 2 : kABytes) +
+                                                     (B_MN ? boxes * kBox : (uint32_t)kOwnN * kBK * 2)));
           uint8_t* sa = sm + L::a0 + st * kABytes;
-          uint8_t* sb = sm + L::b0 + st * kBBytes;
+          uint8_t* sb = sm + b0 + st * kBBytes;
+          const int am = m * kTileM + rank * kBM, bn = n * BN + rank * kOwnN;  // this CTA's rows of A, columns of B
+          auto load = [&](void* dst, const CUtensorMap* map, int x, int y) {
+            if constexpr (PAIR)
+              tma_load_2d_pair(dst, map, lead(FULL + st), x, y);
+            else
+              tma_load_2d(dst, map, &bar[FULL + st], x, y);
+          };
           if (A_MN) {  // A stored [K][M]: two [64 K][64 M] boxes
 #pragma unroll
-            for (int i = 0; i < kBM / 64; ++i) tma_load_2d(sa + i * kBox, &tmA, &bar[FULL + st], m * kBM + 64 * i, ks * kBK);
+            for (int i = 0; i < kBM / 64; ++i) load(sa + i * kBox, &tmA, am + 64 * i, ks * kBK);
           } else if (spread) {  // one [few rows][64 K] box; the tile's other rows give rows that nothing reads
-            tma_load_2d(sa, &tmA, &bar[FULL + st], 0, ks * a.spread);
+            load(sa, &tmA, 0, ks * a.spread);
           } else {  // A stored [M][K]: one [128 M][64 K] box
-            tma_load_2d(sa, &tmA, &bar[FULL + st], ks * kBK, m * kBM);
+            load(sa, &tmA, ks * kBK, am);
           }
           if (B_MN) {  // B stored [K][N]: up to four [64 K][64 N] boxes
 #pragma unroll
-            for (int i = 0; i < BN / 64; ++i)
-              if (i < boxes) tma_load_2d(sb + i * kBox, &tmB, &bar[FULL + st], n * BN + 64 * i, ks * kBK);
-          } else {  // B stored [N][K]: one [BN][64 K] box
-            tma_load_2d(sb, &tmB, &bar[FULL + st], ks * kBK, n * BN);
+            for (int i = 0; i < kOwnN / 64; ++i)
+              if (i < boxes) load(sb + i * kBox, &tmB, bn + 64 * i, ks * kBK);
+          } else {  // B stored [N][K]: one [BN, or half][64 K] box
+            load(sb, &tmB, ks * kBK, bn);
           }
         }
       }
       // every copy issued has landed before the CTA may leave
-      for (int64_t j = kk - 1; j >= 0 && j >= kk - kStages; --j)
+      // (PAIR: the leader waits for both CTAs' copies, and neither leaves before the other)
+      for (int64_t j = kk - 1; rank == 0 && j >= 0 && j >= kk - kStages; --j)
         mbar_drain(&bar[FULL + (int)(j % kStages)], (uint32_t)((j / kStages) & 1), abort_flag);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t whole = idesc_bf16(kBM, BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
+    if (PAIR && rank != 0) {
+      if (lane == 0) mbar_drain(&bar[FINAL], 0, abort_flag);
+    } else if (lane == 0) {
+      constexpr uint32_t whole = idesc_bf16(kTileM, BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
+      auto commit = [&](int b) {
+        if constexpr (PAIR)
+          umma_commit_pair(&bar[b]);
+        else
+          umma_commit(&bar[b]);
+      };
       // K-major: 128-byte rows of K, 8-row groups 1024 bytes apart, K = 16 is 32 bytes on.
       // MN-major: 64-column boxes kBox apart, 8 K rows 1024 bytes apart, K = 16 is 2048 bytes on.
       const uint64_t da = A_MN ? smem_desc(smem_u32(sm + L::a0), kBox, 1024) : smem_desc(smem_u32(sm + L::a0), 16, 1024);
-      const uint64_t db = B_MN ? smem_desc(smem_u32(sm + L::b0), kBox, 1024) : smem_desc(smem_u32(sm + L::b0), 16, 1024);
+      const uint64_t db = B_MN ? smem_desc(smem_u32(sm + b0), kBox, 1024) : smem_desc(smem_u32(sm + b0), 16, 1024);
       constexpr uint32_t ka = A_MN ? 2048 : 32, kb = B_MN ? 2048 : 32;
       int64_t kk = 0;
       bool ok = true;
@@ -285,12 +410,13 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         const int acc = it & 1;
         // the epilogue has read this accumulator's previous tile (it − 2)
         if (it >= 2 && !mbar_wait(&bar[ACC_EMPTY + acc], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, 2)) break;
+        if constexpr (PAIR) fence_cluster();
         tc_fence_after();
         const uint32_t dcol = tbase + (uint32_t)acc * BN;
         int k0, k1;
         k_range(t, k0, k1);
         uint32_t idesc = whole;
-        if (B_MN) {  // N = the columns that are there
+        if (B_MN && !PAIR) {  // N = the columns that are there
           int m, n;
           tile_mn(t, m, n);
           idesc = idesc_bf16(kBM, 64, A_MN ? 1 : 0, 1) + ((tile_boxes(n) - 1) * 64 / 8 << 17);
@@ -304,15 +430,19 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            umma_ss(dcol, desc_at(da, st * kABytes + k * ka), desc_at(db, st * kBBytes + k * kb), idesc,
-                    (ks > k0 || k > 0) ? 1u : 0u);
-          umma_commit(&bar[EMPTY + st]);  // stage st free once these MMAs have read it
+            if constexpr (PAIR)
+              umma_ss_pair(dcol, desc_at(da, st * kABytes + k * ka), desc_at(db, st * kBBytes + k * kb), idesc,
+                           (ks > k0 || k > 0) ? 1u : 0u);
+            else
+              umma_ss(dcol, desc_at(da, st * kABytes + k * ka), desc_at(db, st * kBBytes + k * kb), idesc,
+                      (ks > k0 || k > 0) ? 1u : 0u);
+          commit(EMPTY + st);  // stage st free once these MMAs have read it
         }
-        if (ok) umma_commit(&bar[ACC_FULL + acc]);
+        if (ok) commit(ACC_FULL + acc);
       }
       // completes after every MMA of this CTA (waited for even after an abort:
       // TMEM and shared memory must outlive the MMAs)
-      umma_commit(&bar[FINAL]);
+      commit(FINAL);
       mbar_drain(&bar[FINAL], 0, abort_flag);
     }
   } else {
@@ -326,7 +456,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       const int acc = it & 1;
       int m, n;
       tile_mn(t, m, n);
-      const int64_t row = (int64_t)m * kBM + rl;
+      const int64_t row = (int64_t)m * kTileM + rank * kBM + rl;
       const int64_t c0 = (int64_t)n * BN;  // first column of the tile
       const bool row_ok = row < a.M;
       int y = -1;
@@ -348,7 +478,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         if ((y < 0 || (int64_t)y >= a.Ncols) && n == 0) set_err(a.err, TT_ERR_INVALID_ARG);
       }
       const int64_t yc = (int64_t)y - c0;  // target column within the tile
-      if (!mbar_wait(&bar[ACC_FULL + acc], (uint32_t)((it >> 1) & 1), abort_flag, 4)) break;
+      if (!wait(&bar[ACC_FULL + acc], (uint32_t)((it >> 1) & 1), 4)) break;
       tc_fence_after();
       float m_run = -INFINITY, s_run = 0.f, u_run = 0.f, zt = 0.f;
       bool found = false;
@@ -498,7 +628,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&bar[ACC_EMPTY + acc]);
+      arrive_lead(ACC_EMPTY + acc, true);
       if (kLse && row_ok) {
         a.pm[(int64_t)n * a.M + row] = m_run;
         a.ps[(int64_t)n * a.M + row] = s_run;
@@ -510,9 +640,14 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
   if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  // the other CTA's tensor and shared memory are read and written, its barriers signalled, until here
+  if constexpr (PAIR) cluster_barrier();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, kTmemCols);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tbase, kTmemCols);
+    else
+      tmem_dealloc(tbase, kTmemCols);
   }
 }
 
@@ -520,13 +655,48 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
 template <int EPI, bool A_MN, bool B_MN, int BN = kBN>
 int launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const LhArgs& a, cudaStream_t st) {
   const int smem = (int)LhSmem::total;
-  if (!smem_attr_set<lmhead_gemm_kernel<EPI, A_MN, B_MN, BN>>(smem)) return TT_ERR_CUDA;
+  if (!smem_attr_set<lmhead_gemm_kernel<EPI, A_MN, B_MN, BN, false>>(smem)) return TT_ERR_CUDA;
   const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)sm_count());
   {
     KtScope kt(TT_KT_LMHEAD, st);
-    lmhead_gemm_kernel<EPI, A_MN, B_MN, BN><<<(unsigned)grid, kLhWarps * 32, smem, st>>>(ta, tb, a);
+    lmhead_gemm_kernel<EPI, A_MN, B_MN, BN, false><<<(unsigned)grid, kLhWarps * 32, smem, st>>>(ta, tb, a);
   }
   return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+// The same by pairs of CTAs, as many as are resident at once (a: tiles of 256 rows).
+template <int EPI, bool A_MN, bool B_MN>
+int launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const LhArgs& a, cudaStream_t st) {
+  constexpr auto kern = lmhead_gemm_kernel<EPI, A_MN, B_MN, kBN, true>;
+  const int smem = (int)LhSmem::total;
+  if (!smem_attr_set<kern>(smem)) return TT_ERR_CUDA;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kLhWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2);
+  static std::atomic<int> resident[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0) return TT_ERR_CUDA;
+  int pairs = resident[dev].load(std::memory_order_relaxed);
+  if (pairs == 0) {
+    if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs < 1) return TT_ERR_CUDA;
+    resident[dev].store(pairs, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(a.tiles, pairs)));
+  cudaError_t e;
+  {
+    KtScope kt(TT_KT_LMHEAD, st);
+    e = cudaLaunchKernelEx(&cfg, kern, ta, tb, a);
+  }
+  (void)cudaGetLastError();
+  return cuda_status(e);
 }
 
 // Per row: M = max_j m_j, S = Σ_j s_j·e^(m_j − M) over the nV vocabulary
@@ -687,6 +857,37 @@ LhWs lh_layout(int64_t N, int64_t V, int Hd = 0, int BN = kBN) {
   return w;
 }
 
+// The sum of a split product's parts [splits][n], to bf16 (n a multiple of 4). Four entries to a thread; WARPS > 1: the
+// warps of a block share the parts of 128 entries, and their sums are joined in warp order. Many parts (then there are
+// few entries): 16 warps, 3 x 384 entries of 152 parts 4.0 us, with one 21; few parts: one, 374 x 1728 entries of 4
+// parts 4.7 us, with 16 11.8.
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS)
+    lmhead_sum_parts_kernel(const float* part, int64_t n, int splits, __nv_bfloat16* out) {
+  __shared__ float4 sums[WARPS][32];
+  const int lane = threadIdx.x & 31, w = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const int64_t i = (WARPS == 1 ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)blockIdx.x * 32 + lane) * 4;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < n) {
+#pragma unroll 4
+    for (int s = w; s < splits; s += WARPS) {
+      const float4 p = *reinterpret_cast<const float4*>(part + s * n + i);
+      t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+    }
+  }
+  if constexpr (WARPS > 1) {
+    sums[w][lane] = t;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+      const float4 p = sums[k][lane];
+      t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+    }
+  }
+  if (i < n) *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+}
+
 }  // namespace
 }  // namespace tt
 
@@ -698,10 +899,10 @@ TT_API size_t tt_lmhead_logprob_workspace_bytes(int64_t N, int64_t V) {
 }
 
 namespace {
-LhArgs lh_args(int64_t M, int64_t Ncols, int64_t K, int n_outer, int32_t* err, int BN = kBN) {
+LhArgs lh_args(int64_t M, int64_t Ncols, int64_t K, int n_outer, int32_t* err, int BN = kBN, int BM = kBM) {
   LhArgs a = {};
   a.M = M; a.Ncols = Ncols; a.ksteps = (int)((K + kBK - 1) / kBK);
-  a.nM = (int)((M + kBM - 1) / kBM);
+  a.nM = (int)((M + BM - 1) / BM);
   a.nN = (int)((Ncols + BN - 1) / BN);
   a.tiles = (int64_t)a.nM * a.nN;
   a.n_outer = n_outer;
@@ -757,38 +958,18 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
   return dz_bytes(N, V) + 256;
 }
 
-// The sum of a split product's parts [splits][n], to bf16 (n a multiple of 4). Four entries to a thread; WARPS > 1: the
-// warps of a block share the parts of 128 entries, and their sums are joined in warp order. Many parts (then there are
-// few entries): 16 warps, 3 x 384 entries of 152 parts 4.0 us, with one 21; few parts: one, 374 x 1728 entries of 4
-// parts 4.7 us, with 16 11.8.
-template <int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS)
-    lmhead_sum_parts_kernel(const float* part, int64_t n, int splits, __nv_bfloat16* out) {
-  __shared__ float4 sums[WARPS][32];
-  const int lane = threadIdx.x & 31, w = WARPS == 1 ? 0 : threadIdx.x >> 5;
-  const int64_t i = (WARPS == 1 ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)blockIdx.x * 32 + lane) * 4;
-  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (i < n) {
-#pragma unroll 4
-    for (int s = w; s < splits; s += WARPS) {
-      const float4 p = *reinterpret_cast<const float4*>(part + s * n + i);
-      t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
-    }
-  }
-  if constexpr (WARPS > 1) {
-    sums[w][lane] = t;
-    __syncthreads();
-    if (w != 0) return;
-#pragma unroll
-    for (int k = 1; k < WARPS; ++k) {
-      const float4 p = sums[k][lane];
-      t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
-    }
-  }
-  if (i < n) *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+namespace {
+// Whether pairs of CTAs take a product [M][Ncols] with a sum over K: where a tile's sum is long, its columns are all
+// there, and tiles of 256 rows need no more than 7/6 of the waves. Cycles of a K step, with a CTA alone and with a pair, of
+// 4001 x 32,003 x 1024: dH 736 -> 590 (196 -> 161 us), dW 829 -> 684 (195 -> 169 us). With 16 steps to a tile the z
+// products lost by it (655 -> 717 cycles, 156 -> 173 us; equal at 32 steps), so they are not made by pairs.
+bool by_pairs(int64_t M, int64_t Ncols, int64_t K) {
+  const int64_t cols = Ncols / kBN, sms = sm_count();
+  if (Ncols % kBN || K < kPairSteps * kBK || sms < 2) return false;
+  const int64_t one = (M + kBM - 1) / kBM * cols, two = (M + 2 * kBM - 1) / (2 * kBM) * cols;
+  return ((two + sms / 2 - 1) / (sms / 2)) * 6 <= ((one + sms - 1) / sms) * 7;
 }
 
-namespace {
 // Rows of `bytes` bytes from p begin on 32-byte boundaries.
 bool rows_on_32(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) % 32 == 0; }
 
@@ -803,7 +984,8 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
       !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
     return TT_ERR_CUDA;
-  LhArgs b = lh_args(N, Hd, V, 0, err);
+  const bool pairs_dh = splits == 1 && by_pairs(N, Hd, V), pairs_dw = by_pairs(V, Hd, N);
+  LhArgs b = lh_args(N, Hd, V, 0, err, kBN, pairs_dh ? 2 * kBM : kBM);
   b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr ? ctr + 1 : nullptr;
   b.rows32 = rows_on_32(b.ob, 2 * Hd);
   if (splits > 1) {
@@ -817,7 +999,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   if (!make_tmap_bf16_ld(&mdz_mn, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, 64) ||
       !make_tmap_bf16(&mh_mn, hidden, (uint64_t)Hd, (uint64_t)N, 64))
     return TT_ERR_CUDA;
-  LhArgs c = lh_args(V, Hd, N, 0, err);
+  LhArgs c = lh_args(V, Hd, N, 0, err, kBN, pairs_dw ? 2 * kBM : kBM);
   const bool dw_bf16 = dw_dtype == TT_DT_BF16;
   if (dw_bf16)
     c.ob = static_cast<__nv_bfloat16*>(d_w_vocab);
@@ -841,6 +1023,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
                    cudaEventRecord(fork, st) == cudaSuccess && cudaStreamWaitEvent(side, fork, 0) == cudaSuccess;
   if (!two) (void)cudaGetLastError();
   int rc = splits > 1 ? launch_gemm<EPI_PART, false, true>(mdz, mw_mn, b, st)
+           : pairs_dh ? launch_pairs<EPI_BF16, false, true>(mdz, mw_mn, b, st)
                       : launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
   if (!rc && splits > 1) {
     const int64_t n = N * Hd;
@@ -852,8 +1035,10 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   }
   int rc2 = rc;
   if (!rc)
-    rc2 = dw_bf16 ? launch_gemm<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
-                  : launch_gemm<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st);
+    rc2 = pairs_dw ? (dw_bf16 ? launch_pairs<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
+                              : launch_pairs<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st))
+          : dw_bf16 ? launch_gemm<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
+                    : launch_gemm<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st);
   if (two && (cudaEventRecord(join, side) != cudaSuccess || cudaStreamWaitEvent(st, join, 0) != cudaSuccess))
     rc2 = rc2 ? rc2 : TT_ERR_CUDA;
   if (join) cudaEventDestroy(join);

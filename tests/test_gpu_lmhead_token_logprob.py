@@ -117,6 +117,50 @@ def test_backward_of_few_rows(tt, N, V, Hd):
     assert torch.equal(dh2, dh) and torch.equal(dw2, dw.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("N,V,Hd", [(6001, 2401, 512), (4129, 9999, 1024)])
+def test_backward_of_many_rows(tt, N, V, Hd):
+    """Long sums, which pairs of CTAs take by tiles of 256 rows: an odd number of 128-row tiles, a ragged vocabulary, one
+    wave of tiles and several. Tolerance as test_backward, every row and column by itself too: the roundings to bf16
+    of dz and of the sum are each 2^-8 of a row at most, its terms being independent, the fp32 sums under 1e-4; 1e-2 again. In a captured
+    graph, replayed, and from the weighted call over the same kernels."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    H = torch.randn(N, Hd, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(V, Hd, generator=g, device="cuda") * (2 / Hd ** 0.5)).to(torch.bfloat16)
+    y = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    dl, de = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    z = H.double() @ W.double().T
+    lse = torch.logsumexp(z, 1)
+    lp = z - lse[:, None]
+    p = lp.exp()
+    h = -(p * lp).sum(1)
+    dz = -p * (dl.double()[:, None] + de.double()[:, None] * (lp + h[:, None]))
+    dz[torch.arange(N, device="cuda"), y.long()] += dl.double()
+    r_dh, r_dw = dz @ W.double(), dz.T @ H.double()
+    for dw_dtype in (torch.float32, torch.bfloat16):
+        args = dict(dlogp=dl, dentropy=de, dw_dtype=dw_dtype)
+        err = tt.new_err("cuda")
+        dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse.float(), h.float(), err=err, **args)
+        assert int(err.item()) == 0
+        for x, r in ((dh, r_dh), (dw, r_dw)):
+            e = (x.double() - r).norm(dim=1)
+            assert (e <= GRAD_RL2 * r.norm(dim=1)).all()
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                gh, gw = tt.lmhead_token_logprob_bwd(H, W, y, lse.float(), h.float(), **args)
+            for _ in range(2):
+                gh.zero_(), gw.zero_()
+                graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(gh, dh) and torch.equal(gw, dw)
+    w = torch.rand(N, generator=g, device="cuda")
+    a = tt.lmhead_logprob_bwd(H, W, y, lse.float(), w, g=0.5)
+    b = tt.lmhead_token_logprob_bwd(H, W, y, lse.float(), dlogp=-0.5 * w)
+    for x, t in zip(a, b):
+        assert ((x.double() - t.double()).norm() / t.double().norm()).item() <= 2.0 ** -8
+
+
 def test_log_prob_gradient_equals_the_weighted_call(tt):
     """dlogp = −g·w is the weighted loss: the two calls form dz in another order of two products, then round to bf16."""
     d, H, W, y = _inputs(300, 3001, 128)

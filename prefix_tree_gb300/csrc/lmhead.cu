@@ -49,7 +49,7 @@
 // (by_pairs): a tile of 256 x 256 on two SMs' tensor cores, each SM holding
 // its 128 rows of A and half of B, 32 KB a K step instead of 48. The sums run
 // in the same order: the same bits as without. The whole backward (dz, dH,
-// dW) went 547 -> 496 us at 4001 x 32,003 x 1024, 16.1 -> 14.5 ms at
+// dW) went 547 -> 486 us at 4001 x 32,003 x 1024, 16.1 -> 14.6 ms at
 // 12,669 x 151,936 x 2048.
 //
 // With the entropy (tt_lmhead_token_logprob and its backward): the same
@@ -105,18 +105,24 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "l"(map), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// The same without the writes before it (the reader takes tensor memory or a freed slot only).
+// An arrival on a barrier of either CTA. It carries no writes: the waiter takes tensor memory or a slot that was read.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+// A word for the other CTA, with the arrival on its barrier that the word completes.
+__device__ __forceinline__ void send_u64(uint32_t addr, uint64_t v, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], 8;" ::"r"(bar) : "memory");
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(addr), "l"(v), "r"(bar)
+               : "memory");
 }
-// After a wait that another CTA's arrival ended: what that CTA did before it is seen.
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// After a wait that the other CTA ended: what it sent is seen. (The phase is complete. A fence in its place waits for the
+// warp's own stores too: the backward of 2048 x 65,536 x 2048 took 960 us with fences, 939 so.)
+__device__ __forceinline__ void acquire_cluster(uint64_t* bar, uint32_t parity) {
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n}\n" ::"r"(
+                   smem_u32(bar)),
+               "r"(parity)
+               : "memory");
+}
 
 constexpr int kLhWarps = 6;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
     }
     const int r = it % kTileRing;
     if (!wait(&bar[TILE_FULL + r], (uint32_t)((it / kTileRing) & 1), site)) return false;
-    if constexpr (PAIR) fence_cluster();
+    if (PAIR && rank != 0) acquire_cluster(&bar[TILE_FULL + r], (uint32_t)((it / kTileRing) & 1));
     t = ring[r];
     arrive_lead(TILE_EMPTY + r, /*whole=*/warp >= 2);
     return true;
@@ -334,8 +340,8 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
           t = (int64_t)atomicAdd(a.counter, 1);
           ring[r] = t;
           if constexpr (PAIR) {
-            st_cluster_u64(dsmem_addr(smem_u32(const_cast<const int64_t*>(&ring[r])), 1), (uint64_t)t);
-            mbar_arrive_cluster(dsmem_addr(smem_u32(&bar[TILE_FULL + r]), 1));
+            send_u64(dsmem_addr(smem_u32(const_cast<const int64_t*>(&ring[r])), 1), (uint64_t)t,
+                     dsmem_addr(smem_u32(&bar[TILE_FULL + r]), 1));
           }
           mbar_arrive(&bar[TILE_FULL + r]);
         }
@@ -410,7 +416,6 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         const int acc = it & 1;
         // the epilogue has read this accumulator's previous tile (it − 2)
         if (it >= 2 && !mbar_wait(&bar[ACC_EMPTY + acc], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, 2)) break;
-        if constexpr (PAIR) fence_cluster();
         tc_fence_after();
         const uint32_t dcol = tbase + (uint32_t)acc * BN;
         int k0, k1;
@@ -961,8 +966,9 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
 namespace {
 // Whether pairs of CTAs take a product [M][Ncols] with a sum over K: where a tile's sum is long, its columns are all
 // there, and tiles of 256 rows need no more than 7/6 of the waves. Cycles of a K step, with a CTA alone and with a pair, of
-// 4001 x 32,003 x 1024: dH 736 -> 590 (196 -> 161 us), dW 829 -> 684 (195 -> 169 us). With 16 steps to a tile the z
-// products lost by it (655 -> 717 cycles, 156 -> 173 us; equal at 32 steps), so they are not made by pairs.
+// 4001 x 32,003 x 1024: dH 736 -> 590 (196 -> 161 us), dW 829 -> 684 (195 -> 169 us). The z products are not made by
+// pairs: forward 157 -> 164 us there (16 steps to a tile), 313 -> 305 us at 2048 x 65,536 x 2048, 4.1 -> 4.4 ms at
+// 12,669 x 151,936 x 2048; a CTA alone takes 655 cycles a step, the library's best product about 627.
 bool by_pairs(int64_t M, int64_t Ncols, int64_t K) {
   const int64_t cols = Ncols / kBN, sms = sm_count();
   if (Ncols % kBN || K < kPairSteps * kBK || sms < 2) return false;

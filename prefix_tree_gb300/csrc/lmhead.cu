@@ -45,12 +45,12 @@
 // An MN-major operand is staged as [64 K rows][64 M-or-N columns] boxes with
 // 128-byte swizzle: the UMMA descriptor's leading offset is one box (8 KB,
 // the next 64 columns), its stride 1024 bytes (8 K rows), and each K = 16
-// step advances 2048 bytes. dH and dW with long sums go by pairs of CTAs
-// (by_pairs): a tile of 256 x 256 on two SMs' tensor cores, each SM holding
-// its 128 rows of A and half of B, 32 KB a K step instead of 48. The sums run
-// in the same order: the same bits as without. The whole backward (dz, dH,
-// dW) went 547 -> 486 us at 4001 x 32,003 x 1024, 16.1 -> 14.6 ms at
-// 12,669 x 151,936 x 2048.
+// step advances 2048 bytes. Long sums (dH, dW, and dz of the backward with
+// entropy; by_pairs) are made by pairs of CTAs: a tile of 256 x 256 on two
+// SMs' tensor cores, each SM holding its 128 rows of A and half of B, 32 KB
+// a K step instead of 48. The sums run in the same order: the same bits as
+// without. The whole backward (dz, dH, dW) went 547 -> 470 us at 4001 x
+// 32,003 x 1024, 16.1 -> 14.1 ms at 12,669 x 151,936 x 2048.
 //
 // With the entropy (tt_lmhead_token_logprob and its backward): the same
 // kernel with two more epilogues. EPI_LSE_H carries u = Σ 2^x·x, x = (z −
@@ -157,7 +157,7 @@ struct LhBars {
 // rows: each holds its 128 rows of A and half the columns of B, so that a K
 // step brings 32 KB into an SM instead of 48. The stages are as many as fit.
 constexpr int kPairStages = 6;
-constexpr int kPairSteps = 32;  // the least K steps to a tile (by_pairs)
+constexpr int kPairSteps = 32, kPairStepsDz = 16;  // the least K steps to a tile (by_pairs)
 constexpr uint32_t kPairBBytes = kBBytes / 2;
 static_assert(kPairStages * (kABytes + kPairBBytes) == kStages * (kABytes + kBBytes) &&
                   LhBars<kStages>::NBAR <= LhBars<kPairStages>::NBAR, "one layout for both");
@@ -904,6 +904,19 @@ TT_API size_t tt_lmhead_logprob_workspace_bytes(int64_t N, int64_t V) {
 }
 
 namespace {
+// Whether pairs of CTAs take a product [M][Ncols] with `steps` K steps: where a tile's sum is long enough (`least` steps)
+// and tiles of 256 rows need no more than 7/6 of the waves. With pairs the full GPU takes 680 to 700 cycles a K step
+// whichever the product (32 KB from L2 for each SM: 14 TB/s), a CTA alone 736 (dH), 829 (dW), 762 (dz), 655 (the forward,
+// where SMs that want the same lines at the same time get them once). 4001 x 32,003 x 1024: dH 196 -> 161 us, dW 195 ->
+// 169 (from kPairSteps on), dz 180 -> 164 (from 16 steps on; 9000 x 4001 x 512, 8 steps: the backward 115 -> 117). The
+// forward is not made by pairs: 157 -> 164 us there, 313 -> 305 at 2048 x 65,536 x 2048, 4.1 -> 4.4 ms at 12,669 x 151,936.
+bool by_pairs(int64_t M, int64_t Ncols, int64_t steps, int64_t least) {
+  const int64_t cols = (Ncols + kBN - 1) / kBN, sms = sm_count();
+  if (M <= kBM || steps < least || sms < 2) return false;
+  const int64_t one = (M + kBM - 1) / kBM * cols, two = (M + 2 * kBM - 1) / (2 * kBM) * cols;
+  return ((two + sms / 2 - 1) / (sms / 2)) * 6 <= ((one + sms - 1) / sms) * 7;
+}
+
 LhArgs lh_args(int64_t M, int64_t Ncols, int64_t K, int n_outer, int32_t* err, int BN = kBN, int BM = kBM) {
   LhArgs a = {};
   a.M = M; a.Ncols = Ncols; a.ksteps = (int)((K + kBK - 1) / kBK);
@@ -964,18 +977,6 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
 }
 
 namespace {
-// Whether pairs of CTAs take a product [M][Ncols] with a sum over K: where a tile's sum is long, its columns are all
-// there, and tiles of 256 rows need no more than 7/6 of the waves. Cycles of a K step, with a CTA alone and with a pair, of
-// 4001 x 32,003 x 1024: dH 736 -> 590 (196 -> 161 us), dW 829 -> 684 (195 -> 169 us). The z products are not made by
-// pairs: forward 157 -> 164 us there (16 steps to a tile), 313 -> 305 us at 2048 x 65,536 x 2048, 4.1 -> 4.4 ms at
-// 12,669 x 151,936 x 2048; a CTA alone takes 655 cycles a step, the library's best product about 627.
-bool by_pairs(int64_t M, int64_t Ncols, int64_t K) {
-  const int64_t cols = Ncols / kBN, sms = sm_count();
-  if (Ncols % kBN || K < kPairSteps * kBK || sms < 2) return false;
-  const int64_t one = (M + kBM - 1) / kBM * cols, two = (M + 2 * kBM - 1) / (2 * kBM) * cols;
-  return ((two + sms / 2 - 1) / (sms / 2)) * 6 <= ((one + sms - 1) / sms) * 7;
-}
-
 // Rows of `bytes` bytes from p begin on 32-byte boundaries.
 bool rows_on_32(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) % 32 == 0; }
 
@@ -990,7 +991,9 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
       !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
     return TT_ERR_CUDA;
-  const bool pairs_dh = splits == 1 && by_pairs(N, Hd, V), pairs_dw = by_pairs(V, Hd, N);
+  const bool whole = Hd % kBN == 0;  // a tile by pairs has no columns left out
+  const bool pairs_dh = whole && splits == 1 && by_pairs(N, Hd, V / kBK, kPairSteps);
+  const bool pairs_dw = whole && by_pairs(V, Hd, N / kBK, kPairSteps);
   LhArgs b = lh_args(N, Hd, V, 0, err, kBN, pairs_dh ? 2 * kBM : kBM);
   b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr ? ctr + 1 : nullptr;
   b.rows32 = rows_on_32(b.ob, 2 * Hd);
@@ -1179,8 +1182,9 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
   CUtensorMap mh, mw;
   const bool half = half_tiles(N, V);
   const int BN = half ? kBN / 2 : kBN;
-  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, BN)) return TT_ERR_CUDA;
-  LhArgs a = lh_args(N, V, Hd, 1, err, BN);
+  const bool pairs = !half && by_pairs(N, V, Hd / kBK, kPairStepsDz);
+  if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, pairs ? kBN / 2 : BN)) return TT_ERR_CUDA;
+  LhArgs a = lh_args(N, V, Hd, 1, err, BN, pairs ? 2 * kBM : kBM);
   if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
   // a product with a tile or less to an SM needs no claims: where all three have no more, no counters
   const int64_t most = std::max(a.tiles, (V + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN));
@@ -1190,8 +1194,9 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
     return TT_ERR_CUDA;
   a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
   a.ob = dz; a.ldo = Lw.ldz; a.counter = ctr; a.rows32 = rows_on_32(dz, 2 * Lw.ldz);
-  rc = half ? launch_gemm<EPI_DZ_H, false, false, kBN / 2>(mh, mw, a, st)
-            : launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
+  rc = pairs ? launch_pairs<EPI_DZ_H, false, false>(mh, mw, a, st)
+       : half ? launch_gemm<EPI_DZ_H, false, false, kBN / 2>(mh, mw, a, st)
+              : launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
   return lh_products(hidden, w_vocab, N, V, Hd, dz, Lw.ldz, ctr, d_hidden, d_w_vocab, dw_dtype,
                      ws_at<float>(ws, Lw.parts), Lw.splits, /*fork_dw=*/Lw.splits == 1 && ctr, err, st);

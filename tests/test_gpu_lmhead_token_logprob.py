@@ -117,7 +117,7 @@ def test_backward_of_few_rows(tt, N, V, Hd):
     assert torch.equal(dh2, dh) and torch.equal(dw2, dw.to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("N,V,Hd", [(6001, 2401, 512), (4129, 9999, 1024)])
+@pytest.mark.parametrize("N,V,Hd", [(6001, 2401, 512), (4129, 9999, 1024), (2100, 3001, 1088)])
 def test_backward_of_many_rows(tt, N, V, Hd):
     """Long sums, which pairs of CTAs take by tiles of 256 rows: an odd number of 128-row tiles, a ragged vocabulary, one
     wave of tiles and several. Tolerance as test_backward, every row and column by itself too: the roundings to bf16

@@ -906,7 +906,7 @@ TT_API size_t tt_lmhead_logprob_workspace_bytes(int64_t N, int64_t V) {
 namespace {
 // Whether pairs of CTAs take a product [M][Ncols] with `steps` K steps: where a tile's sum is long enough (`least` steps)
 // and tiles of 256 rows need no more than 7/6 of the waves. With pairs the full GPU takes 680 to 700 cycles a K step
-// whichever the product (32 KB from L2 for each SM: 14 TB/s), a CTA alone 736 (dH), 829 (dW), 762 (dz), 655 (the forward,
+// whichever the product (32 KB from L2 for each SM: 12 to 14 TB/s), a CTA alone 736 (dH), 829 (dW), 762 (dz), 655 (the forward,
 // where SMs that want the same lines at the same time get them once). 4001 x 32,003 x 1024: dH 196 -> 161 us, dW 195 ->
 // 169 (from kPairSteps on), dz 180 -> 164 (from 16 steps on; 9000 x 4001 x 512, 8 steps: the backward 115 -> 117). The
 // forward is not made by pairs: 157 -> 164 us there, 313 -> 305 at 2048 x 65,536 x 2048, 4.1 -> 4.4 ms at 12,669 x 151,936.

@@ -276,3 +276,30 @@ def test_policy_step_over_a_tree(tt, axes):
     dzb = tt.token_logprob_bwd(zb, lse2, e2, y, dlogp=dlogp, dentropy=dent, err=err)
     assert rel_l2(dev_to_f64(dh), dev_to_f64(dzb) @ dev_to_f64(W)) <= GRAD_RL2
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("N,V,Hd", [(513, 4099, 256), (61, 32003, 512), (4129, 9999, 1024)])
+def test_backward_rounds_dz_and_outputs_only(tt, N, V, Hd):
+    """The gradients' error is that of dz's rounding to bf16 and of the outputs' own. A rounding error is spread evenly
+    over at most half a step, 2^-8 of the value: its root mean square is at most 2^-8/sqrt(3). Against 64 bits, with
+    terms of random signs and independent roundings, fp32 dW has one such error and bf16 dH and dW have two: their
+    relative L2 is at most 2^-8/sqrt(3) and sqrt(2) times that. 5 % above for the spread over the few thousand sums
+    that share a row of dz and for the fp32 arithmetic (< 2e-4: see test_backward_of_many_rows)."""
+    g = torch.Generator(device="cuda").manual_seed(N + V)
+    H = torch.randn(N, Hd, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(V, Hd, generator=g, device="cuda") * (2 / Hd ** 0.5)).to(torch.bfloat16)
+    y = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    dl, de = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    z = H.double() @ W.double().T
+    lse = torch.logsumexp(z, 1)
+    lp = z - lse[:, None]
+    p = lp.exp()
+    h = -(p * lp).sum(1)
+    dz = -p * (dl.double()[:, None] + de.double()[:, None] * (lp + h[:, None]))
+    dz[torch.arange(N, device="cuda"), y.long()] += dl.double()
+    r_dh, r_dw = dz @ W.double(), dz.T @ H.double()
+    one = 2.0 ** -8 / 3 ** 0.5 * 1.05
+    for dw_dtype, tol in ((torch.float32, one), (torch.bfloat16, 2 ** 0.5 * one)):
+        dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse.float(), h.float(), dlogp=dl, dentropy=de, dw_dtype=dw_dtype)
+        assert ((dh.double() - r_dh).norm() / r_dh.norm()).item() <= 2 ** 0.5 * one
+        assert ((dw.double() - r_dw).norm() / r_dw.norm()).item() <= tol

@@ -154,12 +154,13 @@ constexpr float kNoColumn = -1e30f;
 // epilogue threads have read it), FINAL (every MMA of the CTA done).
 // TILE_FULL[r] / TILE_EMPTY[r]: the tile index in ring slot r published by
 // the producer / read by the MMA thread and the 128 epilogue threads.
+// STALL: nothing arrives at it (LhArgs::stall_ns).
 constexpr int kTileRing = 4;
 template <int STAGES>
 struct LhBars {
   static constexpr int FULL = 0, EMPTY = FULL + STAGES, ACC_FULL = EMPTY + STAGES, ACC_EMPTY = ACC_FULL + 2,
                        FINAL = ACC_EMPTY + 2, TILE_FULL = FINAL + 1, TILE_EMPTY = TILE_FULL + kTileRing,
-                       NBAR = TILE_EMPTY + kTileRing;
+                       STALL = TILE_EMPTY + kTileRing, NBAR = STALL + 1;
 };
 // A pair of CTAs (a cluster of two, tcgen05 cta_group::2) on one tile of 256
 // rows: each holds its 128 rows of A and half the columns of B, so that a K
@@ -203,6 +204,9 @@ struct LhArgs {
   bool rows32;  // all stores but EPI_DZ's: rows of ob or of begin on 32-byte boundaries (whole sectors to a store)
   int splits;   // EPI_PART: ranges of K (tiles = nM·nN·splits)
   int spread;   // EPI_LSE_H, EPI_DZ_H: A is a few rows laid out by K step, so many to a step (0: plain rows)
+  // EPI_DZ_H, a test of the timeout path, 0 in normal calls: the MMA thread waits so long on STALL before the last K
+  // step of its first tile, and gives up
+  uint64_t stall_ns;
 };
 
 // 32 bytes in one store: a whole sector, which halves the L2 writes of a
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
   constexpr int kOwnN = BN / kCtas;  // columns of B that a CTA holds
   using Bar = LhBars<kStages>;
   constexpr int FULL = Bar::FULL, EMPTY = Bar::EMPTY, ACC_FULL = Bar::ACC_FULL, ACC_EMPTY = Bar::ACC_EMPTY,
-                FINAL = Bar::FINAL, TILE_FULL = Bar::TILE_FULL, TILE_EMPTY = Bar::TILE_EMPTY;
+                FINAL = Bar::FINAL, TILE_FULL = Bar::TILE_FULL, TILE_EMPTY = Bar::TILE_EMPTY, STALL = Bar::STALL;
   const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;  // clusters are consecutive CTAs
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       mbar_init(&bar[ACC_EMPTY + i], PAIR ? 2 * 4 : 128);  // PAIR: one arrival of each epilogue warp
     }
     mbar_init(&bar[FINAL], 1);
+    mbar_init(&bar[STALL], 1);
     for (int i = 0; i < kTileRing; ++i) {
       mbar_init(&bar[TILE_FULL + i], 1);
       mbar_init(&bar[TILE_EMPTY + i], PAIR ? 2 * (1 + 4) : 1 + 128);
@@ -436,7 +441,9 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         }
         for (int ks = k0; ks < k1; ++ks, ++kk) {
           const int st = (int)(kk % kStages);
-          if (!mbar_wait(&bar[FULL + st], (uint32_t)((kk / kStages) & 1), abort_flag, 3)) {
+          if (!mbar_wait(&bar[FULL + st], (uint32_t)((kk / kStages) & 1), abort_flag, 3) ||
+              (EPI == EPI_DZ_H && a.stall_ns && it == 0 && ks == k1 - 1 &&
+               !mbar_wait(&bar[STALL], 0, abort_flag, 9, a.stall_ns))) {
             ok = false;
             break;
           }
@@ -650,11 +657,12 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
       }
     }
   }
-  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   // the other CTA's tensor and shared memory are read and written, its barriers signalled, until here
   if constexpr (PAIR) cluster_barrier();
+  // every role has stopped: a wait that any of them gave up is seen (the producer alone is often done long before)
+  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR)
@@ -918,9 +926,13 @@ namespace {
 // where SMs that want the same lines at the same time get them once). 4001 x 32,003 x 1024: dH 196 -> 161 us, dW 195 ->
 // 169 (from kPairSteps on), dz 180 -> 164 (from 16 steps on; 9000 x 4001 x 512, 8 steps: the backward 115 -> 117). The
 // forward is not made by pairs: 157 -> 164 us there, 313 -> 305 at 2048 x 65,536 x 2048, 4.1 -> 4.4 ms at 12,669 x 151,936.
-bool by_pairs(int64_t M, int64_t Ncols, int64_t steps, int64_t least) {
+// path: a test's choice (kByRule: this rule; one or the other wherever it can).
+enum { kByRule = 0, kSingles = 1, kPairs = 2 };
+bool by_pairs(int path, int64_t M, int64_t Ncols, int64_t steps, int64_t least) {
   const int64_t cols = (Ncols + kBN - 1) / kBN, sms = sm_count();
-  if (M <= kBM || steps < least || sms < 2) return false;
+  if (M <= kBM || sms < 2 || path == kSingles) return false;
+  if (path == kPairs) return true;
+  if (steps < least) return false;
   const int64_t one = (M + kBM - 1) / kBM * cols, two = (M + 2 * kBM - 1) / (2 * kBM) * cols;
   return ((two + sms / 2 - 1) / (sms / 2)) * 6 <= ((one + sms - 1) / sms) * 7;
 }
@@ -993,15 +1005,15 @@ bool rows_on_32(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr
 // dH's sum over the vocabulary is to be split (splits > 1). fork: dW on a second stream beside dH.
 int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd, const __nv_bfloat16* dz,
                 int64_t ldz, int* ctr, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, float* parts, int splits,
-                bool fork_dw, int32_t* err, cudaStream_t st) {
+                bool fork_dw, int path, int32_t* err, cudaStream_t st) {
   // 2. dH = dz·W: A = dz [N][V] (K-major, K = V); B = W [V][Hd] read MN-major; token-major tiles
   CUtensorMap mdz, mw_mn;
   if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
       !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
     return TT_ERR_CUDA;
   const bool whole = Hd % kBN == 0;  // a tile by pairs has no columns left out
-  const bool pairs_dh = whole && splits == 1 && by_pairs(N, Hd, V / kBK, kPairSteps);
-  const bool pairs_dw = whole && by_pairs(V, Hd, N / kBK, kPairSteps);
+  const bool pairs_dh = whole && splits == 1 && by_pairs(path, N, Hd, V / kBK, kPairSteps);
+  const bool pairs_dw = whole && by_pairs(path, V, Hd, N / kBK, kPairSteps);
   LhArgs b = lh_args(N, Hd, V, 0, err, kBN, pairs_dh ? 2 * kBM : kBM);
   b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr ? ctr + 1 : nullptr;
   b.rows32 = rows_on_32(b.ob, 2 * Hd);
@@ -1088,7 +1100,8 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
   a.targets = targets; a.weights = weights; a.g = g; a.lse = lse; a.ob = dz; a.ldo = ldz; a.counter = ctr;
   rc = launch_gemm<EPI_DZ, false, false>(mh, mw, a, st);
   if (rc) return rc;
-  return lh_products(hidden, w_vocab, N, V, Hd, dz, ldz, ctr, d_hidden, d_w_vocab, TT_DT_F32, nullptr, 1, true, err, st);
+  return lh_products(hidden, w_vocab, N, V, Hd, dz, ldz, ctr, d_hidden, d_w_vocab, TT_DT_F32, nullptr, 1, true,
+                     kByRule, err, st);
 }
 
 namespace {
@@ -1172,11 +1185,11 @@ TT_API size_t tt_lmhead_token_logprob_bwd_workspace_bytes(int64_t N, int64_t V, 
   return lh_bwd_layout(N, V, Hd).total;
 }
 
-TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
-                                       const int32_t* targets, const float* lse, const float* entropy,
-                                       const float* dlogp, const float* dentropy, const float* dlse,
-                                       tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws, size_t ws_bytes,
-                                       int32_t* err, tt_stream_t stream) {
+namespace {
+int token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
+                      const int32_t* targets, const float* lse, const float* entropy, const float* dlogp,
+                      const float* dentropy, const float* dlse, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype,
+                      void* ws, size_t ws_bytes, int path, uint64_t stall_ns, int32_t* err, tt_stream_t stream) {
   int rc = lh_check(hidden, w_vocab, N, V, Hd, targets, err);
   if (rc) return rc;
   if (!lse || (dentropy && !entropy) || !d_hidden || !d_w_vocab || !ws || !aligned16(ws) || !aligned16(d_hidden) ||
@@ -1190,7 +1203,7 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
   CUtensorMap mh, mw;
   const bool half = half_tiles(N, V);
   const int BN = half ? kBN / 2 : kBN;
-  const bool pairs = !half && by_pairs(N, V, Hd / kBK, kPairStepsDz);
+  const bool pairs = !half && by_pairs(path, N, V, Hd / kBK, kPairStepsDz);
   if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, pairs ? kBN / 2 : BN)) return TT_ERR_CUDA;
   LhArgs a = lh_args(N, V, Hd, 1, err, BN, pairs ? 2 * kBM : kBM);
   if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
@@ -1202,10 +1215,32 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
     return TT_ERR_CUDA;
   a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
   a.ob = dz; a.ldo = Lw.ldz; a.counter = ctr; a.rows32 = rows_on_32(dz, 2 * Lw.ldz);
+  a.stall_ns = stall_ns;
   rc = pairs ? launch_pairs<EPI_DZ_H, false, false>(mh, mw, a, st)
        : half ? launch_gemm<EPI_DZ_H, false, false, kBN / 2>(mh, mw, a, st)
               : launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
   if (rc) return rc;
   return lh_products(hidden, w_vocab, N, V, Hd, dz, Lw.ldz, ctr, d_hidden, d_w_vocab, dw_dtype,
-                     ws_at<float>(ws, Lw.parts), Lw.splits, /*fork_dw=*/Lw.splits == 1 && ctr, err, st);
+                     ws_at<float>(ws, Lw.parts), Lw.splits, /*fork_dw=*/Lw.splits == 1 && ctr, path, err, st);
+}
+}  // namespace
+
+TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
+                                       const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* dlogp, const float* dentropy, const float* dlse,
+                                       tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws, size_t ws_bytes,
+                                       int32_t* err, tt_stream_t stream) {
+  return token_logprob_bwd(hidden, w_vocab, N, V, Hd, targets, lse, entropy, dlogp, dentropy, dlse, d_hidden, d_w_vocab,
+                           dw_dtype, ws, ws_bytes, kByRule, 0, err, stream);
+}
+
+TT_API int tt_lmhead_token_logprob_bwd_path_test(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V,
+                                                 int Hd, const int32_t* targets, const float* lse, const float* entropy,
+                                                 const float* dlogp, const float* dentropy, const float* dlse,
+                                                 tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws,
+                                                 size_t ws_bytes, int path, int64_t stall_ns, int32_t* err,
+                                                 tt_stream_t stream) {
+  if (path < kByRule || path > kPairs || stall_ns < 0 || stall_ns > 10000000000LL) return TT_ERR_INVALID_ARG;
+  return token_logprob_bwd(hidden, w_vocab, N, V, Hd, targets, lse, entropy, dlogp, dentropy, dlse, d_hidden, d_w_vocab,
+                           dw_dtype, ws, ws_bytes, path, (uint64_t)stall_ns, err, stream);
 }

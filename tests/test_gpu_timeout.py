@@ -66,3 +66,54 @@ def test_stall_test_rejects_bad_limits(tt):
         rc = tt.lib().tt_tree_attn_fwd_stall_test(fake, fake, fake, fake, fake, fake, 128, 1, 1, 64,
                                                    ctypes.c_float(0.125), 1, ns, fake, None)
         assert rc == -1
+
+
+def _head_path_test(tt, H, W, y, lse, h, dl, de, path, stall_ns=0, dw_dtype=torch.float32):
+    """tt_lmhead_token_logprob_bwd_path_test: (return code, error word, d_hidden, d_w_vocab)."""
+    N, Hd = H.shape
+    V = W.shape[0]
+    dh, dw = torch.empty_like(H), torch.empty((V, Hd), dtype=dw_dtype, device="cuda")
+    n = tt.lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V, Hd)
+    ws, err = torch.zeros(n, dtype=torch.uint8, device="cuda"), tt.new_err("cuda")
+    rc = tt.lib().tt_lmhead_token_logprob_bwd_path_test(
+        _vp(H), _vp(W), N, V, Hd, _vp(y), _vp(lse), _vp(h), _vp(dl), _vp(de), None, _vp(dh), _vp(dw),
+        2 if dw_dtype == torch.float32 else 0, _vp(ws), n, path, stall_ns, _vp(err),
+        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    return rc, int(err.item()), dh, dw
+
+
+def _head_inputs(N, V, Hd):
+    g = torch.Generator(device="cuda").manual_seed(N + V)
+    H = torch.randn(N, Hd, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(V, Hd, generator=g, device="cuda") * (2 / Hd ** 0.5)).to(torch.bfloat16)
+    y = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    return H, W, y, torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("N,V,Hd,path", [
+    (300, 3001, 256, 1),    # half tiles, one to a CTA
+    (1000, 4000, 256, 1),   # whole tiles, one to a CTA
+    (1000, 4000, 256, 2),   # one to a pair of CTAs
+    (4129, 9999, 256, 1), (4129, 9999, 256, 2)])  # several to a CTA, to a pair: claimed from a counter
+def test_head_wait_expires_late_in_a_tile_then_calls_recover(tt, N, V, Hd, path):
+    """The head's MMA thread gives up before the last K step of its first tile, when the CTA's producer has issued
+    every copy of it: where a CTA has one tile only, the producer is done by then, and the error must be reported all
+    the same. The next calls on the stream give what calls before gave."""
+    H, W, y, dl, de = _head_inputs(N, V, Hd)
+    _, h, lse = tt.lmhead_token_logprob(H, W, y)
+    before = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de)
+    rc, err, _, _ = _head_path_test(tt, H, W, y, lse, h, dl, de, path, 10_000_000)
+    assert rc == 0 and err == TT_ERR_TIMEOUT
+    err2 = tt.new_err("cuda")
+    after = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de, err=err2)
+    torch.cuda.synchronize()
+    assert int(err2.item()) == 0 and all(torch.equal(a, b) for a, b in zip(before, after))
+
+
+def test_head_path_test_rejects_bad_arguments(tt):
+    f = ctypes.c_void_p(4096)  # rejected before any pointer is used
+    for path, ns in ((3, 0), (-1, 0), (0, -1), (0, 10_000_000_001)):
+        rc = tt.lib().tt_lmhead_token_logprob_bwd_path_test(f, f, 300, 1000, 128, f, f, f, f, f, f, f, f, 2, f, 1 << 40,
+                                                           path, ns, f, None)
+        assert rc == -1

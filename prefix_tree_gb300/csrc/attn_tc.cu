@@ -600,9 +600,10 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 1)
       if (q < a.nq) a.lse[(int64_t)hx * a.lse_ld + q] = l > 0.f ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
     }
   }
-  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  // every role has stopped: a wait that any of them gave up is seen
+  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmemCols);

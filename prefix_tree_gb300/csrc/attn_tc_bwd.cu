@@ -529,9 +529,10 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmdO, const CUtensorMa
       for (int v = 0; v < D / 16; ++v) dst[v] = make_uint4(0, 0, 0, 0);
     }
   }
-  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  // every role has stopped: a wait that any of them gave up is seen
+  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmemCols);
@@ -895,9 +896,10 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmQ, const CUtensorM
       }
     }
   }
-  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  // every role has stopped: a wait that any of them gave up is seen
+  if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmemCols);

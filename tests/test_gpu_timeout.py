@@ -117,3 +117,28 @@ def test_head_path_test_rejects_bad_arguments(tt):
         rc = tt.lib().tt_lmhead_token_logprob_bwd_path_test(f, f, 300, 1000, 128, f, f, f, f, f, f, f, f, 2, f, 1 << 40,
                                                            path, ns, f, None)
         assert rc == -1
+
+
+@pytest.mark.parametrize("tiles", [1, 2])
+@pytest.mark.parametrize("heads", [(2, 1, 64), (4, 2, 128)])
+def test_forward_wait_expires_at_the_last_block(tt, tiles, heads):
+    """One segment of two key blocks: the stall comes before a tile's last block, when the producer may have nothing
+    left to wait for. It is reported all the same."""
+    hq, hkv, d = heads
+    N = 256
+    tree = tt.tree_build(torch.tensor([-1], dtype=torch.int32, device="cuda"),
+                         torch.tensor([N], dtype=torch.int32, device="cuda")).check()
+    g = torch.Generator(device="cuda").manual_seed(d)
+    Q, K, V = (torch.randn(N, n, d, generator=g, device="cuda").to(torch.bfloat16) for n in (hq, hkv, hkv))
+    before = tt.tree_attn_fwd(tree, Q, K, V, tiles=tiles)
+    O, LSE, err = torch.empty_like(Q), torch.empty(hq, N, dtype=torch.float32, device="cuda"), tt.new_err("cuda")
+    rc = tt.lib().tt_tree_attn_fwd_stall_test(_vp(tree.ws), _vp(Q), _vp(K), _vp(V), _vp(O), _vp(LSE), N, hq, hkv, d,
+                                              ctypes.c_float(d ** -0.5), tiles, 10_000_000, _vp(err),
+                                              ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert int(err.item()) == TT_ERR_TIMEOUT
+    err2 = tt.new_err("cuda")
+    after = tt.tree_attn_fwd(tree, Q, K, V, err=err2, tiles=tiles)
+    torch.cuda.synchronize()
+    assert int(err2.item()) == 0 and all(torch.equal(a, b) for a, b in zip(before, after))

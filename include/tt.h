@@ -555,7 +555,8 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
                                        const float* dlogp, const float* dentropy, const float* dlse,
                                        tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws, size_t ws_bytes,
                                        int32_t* err, tt_stream_t stream);
-/* Test of its kernels' paths: the same call, except for path and stall_ns.
+/* Test of its kernels' paths: the same call, except for path, stall_ns and
+ * drain_ns.
  * path: 0 chooses as the call does, 1 makes every product by single CTAs, 2 by
  * pairs of CTAs wherever these can take it (more than 128 rows; Hd a multiple
  * of 256 for d_hidden and d_w_vocab; not a split d_hidden, not dz where its
@@ -566,13 +567,15 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
  * the other roles stop at their next wait (a pair's other CTA after the normal
  * 2 s), what was issued is waited for, tensor memory is freed, and `err`
  * receives TT_ERR_TIMEOUT. The outputs are unspecified then; the context and
- * stream stay usable. */
+ * stream stay usable.
+ * drain_ns > 0 (up to 10^10): the limit, in place of 2 s, of the wait of a
+ * pair's second CTA for the dz product's last MMAs. */
 TT_API int tt_lmhead_token_logprob_bwd_path_test(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V,
                                                  int Hd, const int32_t* targets, const float* lse, const float* entropy,
                                                  const float* dlogp, const float* dentropy, const float* dlse,
                                                  tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws,
-                                                 size_t ws_bytes, int path, int64_t stall_ns, int32_t* err,
-                                                 tt_stream_t stream);
+                                                 size_t ws_bytes, int path, int64_t stall_ns, int64_t drain_ns,
+                                                 int32_t* err, tt_stream_t stream);
 
 /* ---------------------------------------------------------------- launch timing
  * A measurement aid, off by default, and the one state the library keeps

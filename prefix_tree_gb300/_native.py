@@ -88,7 +88,7 @@ _SIGS = {
     "tt_lmhead_token_logprob_bwd_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "tt_lmhead_token_logprob_bwd": (_int, [_vp, _vp, _i64, _i64, _int] + [_vp] * 8 + [_int, _vp, _sz, _vp, _vp]),
     "tt_lmhead_token_logprob_bwd_path_test": (_int, [_vp, _vp, _i64, _i64, _int] + [_vp] * 8 +
-                                              [_int, _vp, _sz, _int, _i64, _vp, _vp]),
+                                              [_int, _vp, _sz, _int, _i64, _i64, _vp, _vp]),
     "tt_status_string": (ctypes.c_char_p, [_int]),
     "tt_version": (_int, []),
     "tt_trie_build": (_int, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),

@@ -207,6 +207,7 @@ struct LhArgs {
   // EPI_DZ_H, a test of the timeout path, 0 in normal calls: the MMA thread waits so long on STALL before the last K
   // step of its first tile, and gives up
   uint64_t stall_ns;
+  uint64_t drain_ns;  // a test's limit of the second CTA's wait for FINAL (0: the normal one)
 };
 
 // 32 bytes in one store: a whole sector, which halves the L2 writes of a
@@ -405,10 +406,8 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
         mbar_drain(&bar[FULL + (int)(j % kStages)], (uint32_t)((j / kStages) & 1), abort_flag);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (PAIR && rank != 0) {
-      if (lane == 0) mbar_drain(&bar[FINAL], 0, abort_flag);
-    } else if (lane == 0) {
+    // ------------------------------------------------------------ MMA issuer (PAIR: the leader's, for both)
+    if (rank == 0 && lane == 0) {
       constexpr uint32_t whole = idesc_bf16(kTileM, BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
       auto commit = [&](int b) {
         if constexpr (PAIR)
@@ -660,7 +659,12 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
   tc_fence_before();
   __syncthreads();
   // the other CTA's tensor and shared memory are read and written, its barriers signalled, until here
-  if constexpr (PAIR) cluster_barrier();
+  if constexpr (PAIR) {
+    cluster_barrier();
+    // The leader has seen its last MMAs complete; their arrival here must not find the CTA gone. (A wait from the
+    // kernel's start would put its limit on the whole product, not on what is under way.)
+    if (rank != 0 && threadIdx.x == 0) mbar_drain(&bar[FINAL], 0, abort_flag, a.drain_ns ? a.drain_ns : kWaitNs);
+  }
   // every role has stopped: a wait that any of them gave up is seen (the producer alone is often done long before)
   if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
   if (warp == 1) {
@@ -1189,7 +1193,8 @@ namespace {
 int token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V, int Hd,
                       const int32_t* targets, const float* lse, const float* entropy, const float* dlogp,
                       const float* dentropy, const float* dlse, tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype,
-                      void* ws, size_t ws_bytes, int path, uint64_t stall_ns, int32_t* err, tt_stream_t stream) {
+                      void* ws, size_t ws_bytes, int path, uint64_t stall_ns, uint64_t drain_ns, int32_t* err,
+                      tt_stream_t stream) {
   int rc = lh_check(hidden, w_vocab, N, V, Hd, targets, err);
   if (rc) return rc;
   if (!lse || (dentropy && !entropy) || !d_hidden || !d_w_vocab || !ws || !aligned16(ws) || !aligned16(d_hidden) ||
@@ -1216,6 +1221,7 @@ int token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, 
   a.targets = targets; a.lse = lse; a.entropy = entropy; a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse;
   a.ob = dz; a.ldo = Lw.ldz; a.counter = ctr; a.rows32 = rows_on_32(dz, 2 * Lw.ldz);
   a.stall_ns = stall_ns;
+  a.drain_ns = drain_ns;
   rc = pairs ? launch_pairs<EPI_DZ_H, false, false>(mh, mw, a, st)
        : half ? launch_gemm<EPI_DZ_H, false, false, kBN / 2>(mh, mw, a, st)
               : launch_gemm<EPI_DZ_H, false, false>(mh, mw, a, st);
@@ -1231,16 +1237,18 @@ TT_API int tt_lmhead_token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_v
                                        tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws, size_t ws_bytes,
                                        int32_t* err, tt_stream_t stream) {
   return token_logprob_bwd(hidden, w_vocab, N, V, Hd, targets, lse, entropy, dlogp, dentropy, dlse, d_hidden, d_w_vocab,
-                           dw_dtype, ws, ws_bytes, kByRule, 0, err, stream);
+                           dw_dtype, ws, ws_bytes, kByRule, 0, 0, err, stream);
 }
 
 TT_API int tt_lmhead_token_logprob_bwd_path_test(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_t V,
                                                  int Hd, const int32_t* targets, const float* lse, const float* entropy,
                                                  const float* dlogp, const float* dentropy, const float* dlse,
                                                  tt_bf16* d_hidden, void* d_w_vocab, int dw_dtype, void* ws,
-                                                 size_t ws_bytes, int path, int64_t stall_ns, int32_t* err,
-                                                 tt_stream_t stream) {
-  if (path < kByRule || path > kPairs || stall_ns < 0 || stall_ns > 10000000000LL) return TT_ERR_INVALID_ARG;
+                                                 size_t ws_bytes, int path, int64_t stall_ns, int64_t drain_ns,
+                                                 int32_t* err, tt_stream_t stream) {
+  constexpr int64_t kMost = 10000000000LL;
+  if (path < kByRule || path > kPairs || stall_ns < 0 || stall_ns > kMost || drain_ns < 0 || drain_ns > kMost)
+    return TT_ERR_INVALID_ARG;
   return token_logprob_bwd(hidden, w_vocab, N, V, Hd, targets, lse, entropy, dlogp, dentropy, dlse, d_hidden, d_w_vocab,
-                           dw_dtype, ws, ws_bytes, path, (uint64_t)stall_ns, err, stream);
+                           dw_dtype, ws, ws_bytes, path, (uint64_t)stall_ns, (uint64_t)drain_ns, err, stream);
 }

@@ -104,12 +104,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // the parity of a phase that has completed or is the current one: a barrier
 // that completed another phase since names the current phase again with the
 // same parity.
-__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           uint64_t limit_ns = kWaitNs) {
   if (mbar_test_now(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1; i < kWaitPolls; ++i) {
     if (mbar_test(bar, parity)) return true;
-    if ((i & 255u) == 0u && global_ns() - t0 > kWaitNs) break;
+    if ((i & 255u) == 0u && global_ns() - t0 > limit_ns) break;
   }
   if (atomicExch(const_cast<int*>(abort), 1) == 0) record_timeout(0xdd, parity);
   return false;

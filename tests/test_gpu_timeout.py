@@ -68,7 +68,7 @@ def test_stall_test_rejects_bad_limits(tt):
         assert rc == -1
 
 
-def _head_path_test(tt, H, W, y, lse, h, dl, de, path, stall_ns=0, dw_dtype=torch.float32):
+def _head_path_test(tt, H, W, y, lse, h, dl, de, path, stall_ns=0, drain_ns=0, dw_dtype=torch.float32):
     """tt_lmhead_token_logprob_bwd_path_test: (return code, error word, d_hidden, d_w_vocab)."""
     N, Hd = H.shape
     V = W.shape[0]
@@ -77,7 +77,7 @@ def _head_path_test(tt, H, W, y, lse, h, dl, de, path, stall_ns=0, dw_dtype=torc
     ws, err = torch.zeros(n, dtype=torch.uint8, device="cuda"), tt.new_err("cuda")
     rc = tt.lib().tt_lmhead_token_logprob_bwd_path_test(
         _vp(H), _vp(W), N, V, Hd, _vp(y), _vp(lse), _vp(h), _vp(dl), _vp(de), None, _vp(dh), _vp(dw),
-        2 if dw_dtype == torch.float32 else 0, _vp(ws), n, path, stall_ns, _vp(err),
+        2 if dw_dtype == torch.float32 else 0, _vp(ws), n, path, stall_ns, drain_ns, _vp(err),
         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
     torch.cuda.synchronize()
     return rc, int(err.item()), dh, dw
@@ -113,9 +113,10 @@ def test_head_wait_expires_late_in_a_tile_then_calls_recover(tt, N, V, Hd, path)
 
 def test_head_path_test_rejects_bad_arguments(tt):
     f = ctypes.c_void_p(4096)  # rejected before any pointer is used
-    for path, ns in ((3, 0), (-1, 0), (0, -1), (0, 10_000_000_001)):
+    for path, ns, drain in ((3, 0, 0), (-1, 0, 0), (0, -1, 0), (0, 10_000_000_001, 0), (0, 0, -1),
+                            (0, 0, 10_000_000_001)):
         rc = tt.lib().tt_lmhead_token_logprob_bwd_path_test(f, f, 300, 1000, 128, f, f, f, f, f, f, f, f, 2, f, 1 << 40,
-                                                           path, ns, f, None)
+                                                           path, ns, drain, f, None)
         assert rc == -1
 
 
@@ -142,3 +143,14 @@ def test_forward_wait_expires_at_the_last_block(tt, tiles, heads):
     after = tt.tree_attn_fwd(tree, Q, K, V, err=err2, tiles=tiles)
     torch.cuda.synchronize()
     assert int(err2.item()) == 0 and all(torch.equal(a, b) for a, b in zip(before, after))
+
+
+def test_head_limit_of_the_last_wait_is_not_that_of_the_product(tt):
+    """The wait of a pair's second CTA for the last MMAs begins when its own work has ended: 0.5 ms are enough for it in
+    a product that cannot take less than 1.9 ms (4.4 TFLOP at the nominal 2.25 PFLOP/s)."""
+    H, W, y, dl, de = _head_inputs(16384, 65536, 2048)
+    _, h, lse = tt.lmhead_token_logprob(H, W, y)
+    ref = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de)
+    rc, err, dh, dw = _head_path_test(tt, H, W, y, lse, h, dl, de, 2, drain_ns=500_000)
+    assert rc == 0 and err == 0
+    assert torch.equal(dh, ref[0]) and torch.equal(dw, ref[1])

@@ -303,3 +303,20 @@ def test_backward_rounds_dz_and_outputs_only(tt, N, V, Hd):
         dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse.float(), h.float(), dlogp=dl, dentropy=de, dw_dtype=dw_dtype)
         assert ((dh.double() - r_dh).norm() / r_dh.norm()).item() <= 2 ** 0.5 * one
         assert ((dw.double() - r_dw).norm() / r_dw.norm()).item() <= tol
+
+
+@pytest.mark.parametrize("N,V,Hd", [
+    (1025, 3900, 512),    # 9 tiles of 128 rows, 31 of 128 vocabulary entries; no more than a tile to a CTA
+    (4129, 9999, 1024),   # tiles claimed from counters, dH and dW on two streams
+    (2100, 3001, 1088)])  # Hd no multiple of 256: pairs for dz alone
+@pytest.mark.parametrize("dw_dtype", [torch.float32, torch.bfloat16])
+def test_pairs_of_ctas_give_the_same_bits(tt, N, V, Hd, dw_dtype):
+    """Every product by single CTAs, by pairs, and as the call chooses: equal bit for bit, on any number of SMs."""
+    from tests.test_gpu_timeout import _head_inputs, _head_path_test
+    H, W, y, dl, de = _head_inputs(N, V, Hd)
+    _, h, lse = tt.lmhead_token_logprob(H, W, y)
+    ref = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, dentropy=de, dw_dtype=dw_dtype)
+    for path in (1, 2):
+        rc, err, dh, dw = _head_path_test(tt, H, W, y, lse, h, dl, de, path, dw_dtype=dw_dtype)
+        assert rc == 0 and err == 0
+        assert torch.equal(dh, ref[0]) and torch.equal(dw, ref[1]), path

@@ -442,3 +442,68 @@ def test_refusals(tt):
         with pytest.raises((tt.TTError, ValueError)) as e:
             bad()
         assert code is None or e.value.code == code
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N,V", [(1, 70_003), (2, 40_001), (9, 131_072)])
+def test_masks_and_extremes_with_several_ctas_to_a_row(tt, dtype, N, V):
+    """Few long rows are cut into slices, one to a CTA of a cluster: whole slices masked, rows at the type's lowest and
+    highest value, one token left, one dominant, NaN and infinity in one slice alone, each forward and backward."""
+    rng = np.random.default_rng(V)
+    low, high = float(torch.finfo(DT[dtype]).min), float(torch.finfo(DT[dtype]).max)
+    half, rows = V // 2, []
+    x = np.full(V, -INF)                          # nothing left
+    rows.append(x)
+    x = np.full(V, -INF)
+    x[V - 2] = 3.0                                # one token, in the last slice
+    rows.append(x)
+    x = rng.standard_normal(V) * 2
+    x[:half + 5] = -INF                           # the first slices masked
+    rows.append(x)
+    x = rng.standard_normal(V) * 2
+    x[half - 5:] = -INF                           # the last ones
+    rows.append(x)
+    rows.append(np.full(V, low))                  # masked with the lowest value throughout: uniform
+    x = np.full(V, low)
+    x[half:] = -INF                               # the lowest value in some slices, -inf in the others
+    rows.append(x)
+    x = np.full(V, low)
+    x[7] = 1.0                                    # one plain logit among lowest ones
+    rows.append(x)
+    x = rng.standard_normal(V)
+    x[half] = high                                # one slice far above the others
+    rows.append(x)
+    x = np.zeros(V)
+    x[V - 1] = 60.0
+    rows.append(x)
+    for i in range(0, len(rows), N):
+        part = np.stack((rows[i:i + N] + rows)[:N])
+        y = np.array([V - 2 if np.isneginf(r[7]) or r[7] == 1.0 else 7 for r in part])
+        z = _logits(part, dtype)
+        logp, h, lse, ids, top = _check_fwd(tt, z, y, 20)
+        for r in range(N):
+            if np.isneginf(part[r]).all():
+                assert lse[r] == -INF and h[r] == 0 and ids[r].tolist() == list(range(20))
+        one = torch.ones(N, device="cuda")
+        dz = tt.token_logprob_bwd(z, lse, h, torch.tensor(y, dtype=torch.int32, device="cuda"), dlogp=one, dentropy=one)
+        ref = TL.token_logprob_grad(_f64(z), y, np.ones(N), np.ones(N))
+        # p off by 1.1e-4 and the entropy by 1e-4·(1 + 1.5·|U/S|), |U/S| <= log V < 12 here, both times p <= 1 (see
+        # _check_bwd); p·|log p + H| < 12
+        assert (np.abs(_f64(dz) - ref) <= 1.1e-4 * 13 + 2e-3 + torch.finfo(DT[dtype]).eps / 2 * np.abs(ref)).all()
+        assert (dz[np.isneginf(part) & (np.arange(V) != y[:, None])] == 0).all()
+    for bad, where in ((np.nan, 3), (np.nan, V - 1), (INF, half), (np.nan, None)):
+        x = rng.standard_normal((N, V))
+        if where is None:
+            x[0] = bad
+        else:
+            x[0, where] = bad
+            if where == V - 1:
+                x[0, :half] = -INF
+        z = _logits(x, dtype)
+        y = torch.full((N,), 5, dtype=torch.int32, device="cuda")
+        logp, h, lse, ids, top = tt.token_logprob(z, y, top_k=4)
+        for t in (logp, h, lse, top):
+            assert torch.isnan(t[0]).all() and torch.isfinite(t[1:]).all()
+        assert ((ids >= 0) & (ids < V)).all()
+        dz = tt.token_logprob_bwd(z, lse, h, y, dlogp=torch.ones(N, device="cuda"))
+        assert torch.isnan(dz[0]).all() and torch.isfinite(dz[1:]).all()

@@ -135,7 +135,7 @@ TT_API int tt_tree_schedules(const void* ws, int64_t N, int32_t* send, int32_t* 
  *      every axis reads the same positions); any value, negative ones too.
  *   axis_host: host uint8 [rot/2], each < axes; freq_host: host double
  *      [rot/2], finite. Both are read before the call returns. Angles are
- *      exact to 2^-23 of a turn at every int32 position.
+ *      exact to 2^-23 of a turn at every int32 position and frequency.
  * Limits (TT_ERR_UNSUPPORTED): d and rot even, d <= 1024, rot <= 256, at most
  * 4 axes and 1024 heads each. N = 0 does nothing. 16-byte accesses when all
  * bases and strides are 16-byte multiples and rot and d multiples of 32 bytes;

@@ -7,6 +7,9 @@ Test infrastructure only: fp64, as a product of complex numbers.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+from functools import lru_cache
+
 import numpy as np
 
 
@@ -34,3 +37,30 @@ def rope(x, pos, axis, freq, adjacent=False, inverse=False):
     y = x.copy()
     y[..., i1], y[..., i2] = z.real, z.imag
     return y
+
+
+_PLACES = 1400
+
+
+@lru_cache(maxsize=None)
+def _digits_of_one_turn():
+    """1/2π in units of 2^-_PLACES, from π = 16 atan(1/5) − 4 atan(1/239) in whole numbers."""
+    def atan_inv(n):
+        term = total = (1 << _PLACES) // n
+        k, sign = 1, -1
+        while term:
+            term //= n * n
+            k += 2
+            total += sign * (term // k)
+            sign = -sign
+        return total
+    return (1 << (2 * _PLACES - 1)) // (16 * atan_inv(5) - 4 * atan_inv(239))
+
+
+def angle(pos, freq):
+    """pos·freq reduced to less than half a turn (radians), for any int32 position and any double: the product's turns
+    are reduced as whole numbers, where a product in fp64 is off by 2^-53 of itself."""
+    f = Fraction(float(freq))
+    one = 1 << _PLACES
+    t = int(pos) * f.numerator * _digits_of_one_turn() // f.denominator % one
+    return float(Fraction(t - one if 2 * t >= one else t, one)) * 2.0 * np.pi

@@ -10,8 +10,11 @@
 // Angles. f_i/2π modulo 1 is held as a 64-bit binary fraction of a turn, so
 // pos·f_i modulo one turn is one wrapping 64-bit product: no large argument
 // is ever rounded to fp32 (at position 10^6 an fp32 angle is off by up to
-// 0.03 rad), and no fp64 instruction is needed. The top 32 bits, as a signed
-// fraction of half a turn, go to sincospif.
+// 0.03 rad), and no fp64 instruction is needed. The fraction comes from the
+// digits of 1/2π (turns_of), so that it holds for every frequency: an fp64
+// division would leave 2^-53 of the frequency's turns, which the position
+// multiplies. The top 32 bits, as a signed fraction of half a turn, go to
+// sincospif.
 //
 // Bound by memory: each of q and k once in, once out. A block forms the sines
 // and cosines of its tokens once, in shared memory, for all their heads; a
@@ -138,6 +141,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
+// |f|/2π modulo 1 in units of 2^-64, negated for f < 0, cut off below 2^-64 (then at position 2^31 the angle is off by
+// 2^-33 of a turn). As Payne and Hanek reduce large arguments: f = mant·2^s with a whole mant of 53 bits, and of the
+// product with 1/2π only the digits that matter are formed: 2^s/2π modulo 1 to 128 binary places, which are 128
+// consecutive digits of 1/2π, times mant modulo 2^128.
+uint64_t turns_of(double f) {
+  // the first 1152 binary digits of 1/2π: a double's exponent leaves out up to 971 of them
+  static const uint64_t digits[18] = {
+      0x28be60db9391054a, 0x7f09d5f47d4d3770, 0x36d8a5664f10e410, 0x7f9458eaf7aef158, 0x6dc91b8e909374b8,
+      0x01924bba82746487, 0x3f877ac72c4a69cf, 0xba208d7d4baed121, 0x3a671c09ad17df90, 0x4e64758e60d4ce7d,
+      0x272117e2ef7e4a0e, 0xc7fe25fff7816603, 0xfbcbc462d6829b47, 0xdb4d9fb3c9f2c26d, 0xd3d18fd9a797fa8b,
+      0x5d49eeb1faf97c5e, 0xcf41ce7de294a4ba, 0x9afed7ec47e35742};
+  typedef unsigned __int128 u128;
+  int e;
+  const uint64_t mant = (uint64_t)std::ldexp(std::frexp(std::fabs(f), &e), 53);
+  const int s = e - 53;
+  u128 x = 0;
+  if (s >= 0) {
+    const int j = s / 64, o = s % 64;
+    x = (u128)digits[j] << 64 | digits[j + 1];
+    if (o) x = x << o | digits[j + 2] >> (64 - o);
+  } else if (s > -128) {
+    x = ((u128)digits[0] << 64 | digits[1]) >> -s;
+  }
+  const uint64_t t = (uint64_t)((mant * x) >> 64);
+  return f < 0 ? 0 - t : t;
+}
+
 template <typename T>
 int launch_rope(RopeArgs& a, int rot, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T);
@@ -181,9 +211,7 @@ TT_API int tt_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, c
   RopeArgs a = {};
   for (int i = 0; i < rot / 2; ++i) {
     if (axis_host[i] >= axes || !std::isfinite(freq_host[i])) return TT_ERR_INVALID_ARG;
-    double t = freq_host[i] / 6.283185307179586476925;
-    t -= std::floor(t);
-    a.turn[i] = t < 1.0 ? (uint64_t)(t * 0x1p64) : 0;
+    a.turn[i] = turns_of(freq_host[i]);
     a.axis[i] = axis_host[i];
   }
   if (N == 0 || Hq + Hkv == 0) return TT_OK;

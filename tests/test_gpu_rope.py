@@ -184,3 +184,22 @@ def test_refusals(tt):
     with pytest.raises(tt.TTError) as e:
         tt.rope(q[:1].expand(4, 2, 64), None, pos)  # rows on top of each other
     assert e.value.code == -1
+
+
+def test_angles_of_any_frequency_at_far_positions(tt):
+    """(1, 0) turned is (cos θ, sin θ), against angles reduced in whole numbers. θ is within 2^-24 of a turn: the
+    fraction of a turn is cut off at 2^-64 (times a position up to 2^31) and at 2^-32, and rounded to fp32 (2^-25 of a
+    turn at half a turn); sincospif is within 2^-23."""
+    pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 10 ** 6, 123456789, -987654321], np.int32)
+    freq = np.array([1.0, 0.0, -0.5, 2 * np.pi, 7.0, -7.0, 100.0, 1000.0, 0.1, 3e-5, 1e6 + 0.1, 1e17, -1e300, 1.7e308,
+                     5e-324, 1e-12])
+    q = torch.zeros(8, 1, 32, device="cuda")
+    q[..., :16] = 1
+    got, _ = tt.rope(q, None, torch.from_numpy(pos).cuda(), inv_freq=freq)
+    back, _ = tt.rope_bwd(q, None, torch.from_numpy(pos).cuda(), inv_freq=freq)
+    theta = np.array([[R.angle(p, f) for f in freq] for p in pos])
+    tol = 2 * np.pi * 2.0 ** -24 + 2.0 ** -23
+    for x, sign in ((got, 1), (back, -1)):
+        x = _f64(x)[:, 0]
+        assert np.abs(x[:, :16] - np.cos(theta)).max() <= tol
+        assert np.abs(x[:, 16:] - sign * np.sin(theta)).max() <= tol

@@ -87,3 +87,19 @@ def test_rotation_properties(adjacent):
     # one frequency, one quarter turn, by hand
     q = R.rope(np.array([[[1.0, 2.0]]]), np.array([[1]]), [0], [np.pi / 2], adjacent)
     np.testing.assert_allclose(q, [[[-2.0, 1.0]]], atol=1e-15)
+
+
+def test_angles_reduced_in_whole_numbers():
+    """Against fp64 where its product is exact enough, and by doubling and adding angles where it is not."""
+    for p in (0, 1, -5, 1000):
+        for f in (1.0, 0.25, -3.5, 1e-4):
+            d = R.angle(p, f) - p * f
+            assert abs(d - 2 * np.pi * round(d / (2 * np.pi))) < 1e-12
+    assert abs(R.angle(1, 2 * np.pi) + 2.4492935982947064e-16) < 1e-30  # 2π as a double is below 2π by this much
+    # doubling the frequency doubles the angle, at any size
+    for f in (7.0, 1e17, 1e300):
+        d = R.angle(1, 2 * f) - 2 * R.angle(1, f)
+        assert abs(d - 2 * np.pi * round(d / (2 * np.pi))) < 1e-14
+    # two positions' angles add up
+    d = R.angle(2 ** 31 - 1, 7.0) - (R.angle(2 ** 30, 7.0) + R.angle(2 ** 30 - 1, 7.0))
+    assert abs(d - 2 * np.pi * round(d / (2 * np.pi))) < 1e-14

@@ -1001,6 +1001,19 @@ TT_API size_t tt_lmhead_logprob_bwd_workspace_bytes(int64_t N, int64_t V) {
 }
 
 namespace {
+// Whether pairs make dH and dW. (A tile by pairs has no columns left out; a split dH is made by single CTAs.)
+bool pairs_dh(int path, int64_t N, int64_t V, int Hd, int splits) {
+  return Hd % kBN == 0 && splits == 1 && by_pairs(path, N, Hd, V / kBK, kPairSteps);
+}
+bool pairs_dw(int path, int64_t N, int64_t V, int Hd) {
+  return Hd % kBN == 0 && by_pairs(path, V, Hd, N / kBK, kPairSteps);
+}
+// Whether a product [M][Ncols] has more tiles (of BN columns, in `splits` parts) than CTAs, or pairs, that run at once.
+bool has_waves(int64_t M, int64_t Ncols, int BN, bool pairs, int splits) {
+  const int64_t rows = pairs ? 2 * kBM : kBM;
+  return (M + rows - 1) / rows * ((Ncols + BN - 1) / BN) * splits > sm_count() / (pairs ? 2 : 1);
+}
+
 // Rows of `bytes` bytes from p begin on 32-byte boundaries.
 bool rows_on_32(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) % 32 == 0; }
 
@@ -1015,10 +1028,8 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   if (!make_tmap_bf16_ld(&mdz, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, kBM) ||
       !make_tmap_bf16(&mw_mn, w_vocab, (uint64_t)Hd, (uint64_t)V, 64))
     return TT_ERR_CUDA;
-  const bool whole = Hd % kBN == 0;  // a tile by pairs has no columns left out
-  const bool pairs_dh = whole && splits == 1 && by_pairs(path, N, Hd, V / kBK, kPairSteps);
-  const bool pairs_dw = whole && by_pairs(path, V, Hd, N / kBK, kPairSteps);
-  LhArgs b = lh_args(N, Hd, V, 0, err, kBN, pairs_dh ? 2 * kBM : kBM);
+  const bool dh_pairs = pairs_dh(path, N, V, Hd, splits), dw_pairs = pairs_dw(path, N, V, Hd);
+  LhArgs b = lh_args(N, Hd, V, 0, err, kBN, dh_pairs ? 2 * kBM : kBM);
   b.ob = reinterpret_cast<__nv_bfloat16*>(d_hidden); b.ldo = Hd; b.counter = ctr ? ctr + 1 : nullptr;
   b.rows32 = rows_on_32(b.ob, 2 * Hd);
   if (splits > 1) {
@@ -1032,7 +1043,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   if (!make_tmap_bf16_ld(&mdz_mn, dz, (uint64_t)V, (uint64_t)N, (uint64_t)ldz, 64) ||
       !make_tmap_bf16(&mh_mn, hidden, (uint64_t)Hd, (uint64_t)N, 64))
     return TT_ERR_CUDA;
-  LhArgs c = lh_args(V, Hd, N, 0, err, kBN, pairs_dw ? 2 * kBM : kBM);
+  LhArgs c = lh_args(V, Hd, N, 0, err, kBN, dw_pairs ? 2 * kBM : kBM);
   const bool dw_bf16 = dw_dtype == TT_DT_BF16;
   if (dw_bf16)
     c.ob = static_cast<__nv_bfloat16*>(d_w_vocab);
@@ -1056,7 +1067,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
                    cudaEventRecord(fork, st) == cudaSuccess && cudaStreamWaitEvent(side, fork, 0) == cudaSuccess;
   if (!two) (void)cudaGetLastError();
   int rc = splits > 1 ? launch_gemm<EPI_PART, false, true>(mdz, mw_mn, b, st)
-           : pairs_dh ? launch_pairs<EPI_BF16, false, true>(mdz, mw_mn, b, st)
+           : dh_pairs ? launch_pairs<EPI_BF16, false, true>(mdz, mw_mn, b, st)
                       : launch_gemm<EPI_BF16, false, true>(mdz, mw_mn, b, st);
   if (!rc && splits > 1) {
     const int64_t n = N * Hd;
@@ -1068,7 +1079,7 @@ int lh_products(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, int64_
   }
   int rc2 = rc;
   if (!rc)
-    rc2 = pairs_dw ? (dw_bf16 ? launch_pairs<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
+    rc2 = dw_pairs ? (dw_bf16 ? launch_pairs<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
                               : launch_pairs<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st))
           : dw_bf16 ? launch_gemm<EPI_BF16, true, true>(mdz_mn, mh_mn, c, two ? side : st)
                     : launch_gemm<EPI_F32, true, true>(mdz_mn, mh_mn, c, two ? side : st);
@@ -1212,9 +1223,10 @@ int token_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, int64_t N, 
   if (!make_tmap_bf16(&mw, w_vocab, (uint64_t)Hd, (uint64_t)V, pairs ? kBN / 2 : BN)) return TT_ERR_CUDA;
   LhArgs a = lh_args(N, V, Hd, 1, err, BN, pairs ? 2 * kBM : kBM);
   if ((rc = map_hidden(hidden, N, V, Hd, ws_at<char>(ws, Lw.spread), &a, &mh, st)) != TT_OK) return rc;
-  // a product with a tile or less to an SM needs no claims: where all three have no more, no counters
-  const int64_t most = std::max(a.tiles, (V + kBM - 1) / kBM * ((Hd + kBN - 1) / kBN));
-  if (most <= sm_count())
+  // a product with a tile or less to a CTA (pair) needs no claims, and leaves no last round of tiles for dW to run
+  // beside: where all three are such, no counters and no second stream
+  if (!has_waves(N, V, BN, pairs, 1) && !has_waves(N, Hd, kBN, pairs_dh(path, N, V, Hd, Lw.splits), Lw.splits) &&
+      !has_waves(V, Hd, kBN, pairs_dw(path, N, V, Hd), 1))
     ctr = nullptr;
   else if (cudaMemsetAsync(ctr, 0, 3 * sizeof(int), st) != cudaSuccess)
     return TT_ERR_CUDA;

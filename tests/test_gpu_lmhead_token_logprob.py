@@ -320,3 +320,29 @@ def test_pairs_of_ctas_give_the_same_bits(tt, N, V, Hd, dw_dtype):
         rc, err, dh, dw = _head_path_test(tt, H, W, y, lse, h, dl, de, path, dw_dtype=dw_dtype)
         assert rc == 0 and err == 0
         assert torch.equal(dh, ref[0]) and torch.equal(dw, ref[1]), path
+
+
+@pytest.mark.parametrize("N,V,Hd,claims", [
+    (40, 700, 64, False),       # a tile or less to a CTA in all three products
+    (19000, 256, 8192, True),   # dH alone has several waves of tiles
+    (2100, 3001, 1088, True)])  # 108 pair tiles of dz, of which one to two SMs run at a time
+def test_tiles_are_claimed_where_a_product_has_several_waves(tt, N, V, Hd, claims):
+    """Tiles are claimed from counters, behind dz in the workspace, where any of the three products has more tiles than
+    run at once; each counter ends at its product's tiles or above, and is not touched otherwise."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    H = torch.randn(N, Hd, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(V, Hd, generator=g, device="cuda") * (2 / Hd ** 0.5)).to(torch.bfloat16)
+    y = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    _, h, lse = tt.lmhead_token_logprob(H, W, y)
+    dl = torch.randn(N, generator=g, device="cuda")
+    ws = torch.full((tt.lib().tt_lmhead_token_logprob_bwd_workspace_bytes(N, V, Hd),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    dh, dw = tt.lmhead_token_logprob_bwd(H, W, y, lse, h, dlogp=dl, ws=ws)
+    at = (N * ((V + 15) // 16 * 16) * 2 + 255) // 256 * 256
+    counters = ws[at:at + 12].clone().view(torch.int32).tolist()
+    assert all(c > 0 for c in counters) if claims else counters == [-1] * 3
+    z = H.float() @ W.float().T
+    dz = -torch.softmax(z, 1) * dl[:, None]
+    dz[torch.arange(N, device="cuda"), y.long()] += dl
+    for x, r in ((dh, dz @ W.float()), (dw, dz.T @ H.float())):
+        assert ((x.float() - r).norm() / r.norm()).item() <= GRAD_RL2

@@ -529,8 +529,9 @@ TT_API int tt_lmhead_logprob_bwd(const tt_bf16* hidden, const tt_bf16* w_vocab, 
 /* The LM head fused with the per-token log-prob and entropy (the quantities of
  * tt_token_logprob without the top alternatives; logits never stored):
  *   z = hidden·w_vocabᵀ;  lse, logp, entropy as there, fp32 [N] each, all written.
- * Arguments, limits and errors as tt_lmhead_logprob (targets required; hidden
- * and w_vocab finite). ws: tt_lmhead_token_logprob_workspace_bytes(N, V, Hd)
+ * Arguments, limits and errors as tt_lmhead_logprob (targets required; N = 0 is
+ * refused too, with TT_ERR_INVALID_ARG). hidden and w_vocab finite; a row whose
+ * logits have a NaN gives NaN in all three outputs. ws: tt_lmhead_token_logprob_workspace_bytes(N, V, Hd)
  * bytes (12·N·ceil(V/256) + 4·N, twice that where the tiles are few; under 32
  * rows of a large head a copy of hidden; and padding), 16-byte aligned. */
 TT_API size_t tt_lmhead_token_logprob_workspace_bytes(int64_t N, int64_t V, int Hd);

@@ -542,13 +542,17 @@ __global__ void __launch_bounds__(kLhWarps * 32, 1)
             found = true;
           }
           const float nm = fmaxf(m_run, cm);
-          if (nm != -INFINITY) {
+          if (kEnt || nm != -INFINITY) {
+            // (With the entropy, columns that are NaN throughout have no maximum either, and must reach the sums.)
+            const float ref = kEnt && nm == -INFINITY ? 0.f : nm;
             if (kEnt) {  // Σ 2^x·x around the new maximum (its offset kept finite while m_run is still -inf)
-              const float dx = fmaxf((m_run - nm) * kLog2e, kNoColumn);
-              u_run = fmaf(dx, s_run, u_run) * fast_exp2(dx);
+              const float dx = fmaxf((m_run - ref) * kLog2e, kNoColumn), f = fast_exp2(dx);
+              u_run = fmaf(dx, s_run, u_run) * f;
+              s_run *= f;
+            } else {
+              s_run *= fast_exp2((m_run - nm) * kLog2e);  // 0 while m_run is still -inf (s_run is 0 then)
             }
-            s_run *= fast_exp2((m_run - nm) * kLog2e);  // 0 while m_run is still -inf (s_run is 0 then)
-            const float2 l2 = make_float2(kLog2e, kLog2e), nn = make_float2(-nm, -nm);
+            const float2 l2 = make_float2(kLog2e, kLog2e), nn = make_float2(-ref, -ref);
             float2 acc2 = make_float2(0.f, 0.f), ent2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -777,7 +781,10 @@ struct LhStat {
 };
 __device__ __forceinline__ void stat_merge(LhStat& a, const LhStat& b) {
   const float M = fmaxf(a.m, b.m);
-  if (M == -INFINITY) return;
+  if (M == -INFINITY) {  // nothing yet (0), or nothing but NaN
+    a.s += b.s;
+    return;
+  }
   const float da = fmaxf(a.m - M, kNoColumn), db = fmaxf(b.m - M, kNoColumn);
   const float fa = expf(da), fb = expf(db);
   a.u = fmaf(da, a.s, a.u) * fa + fmaf(db, b.s, b.u) * fb;

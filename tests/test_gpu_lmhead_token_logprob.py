@@ -346,3 +346,29 @@ def test_tiles_are_claimed_where_a_product_has_several_waves(tt, N, V, Hd, claim
     dz[torch.arange(N, device="cuda"), y.long()] += dl
     for x, r in ((dh, dz @ W.float()), (dw, dz.T @ H.float())):
         assert ((x.float() - r).norm() / r.norm()).item() <= GRAD_RL2
+
+
+@pytest.mark.parametrize("N,V,Hd", [(3, 1, 64), (77, 1000, 64), (300, 3001, 128), (40, 70_001, 1024), (2000, 20_001, 256)])
+def test_nan_in_hidden_and_in_the_vocabulary(tt, N, V, Hd):
+    """A row of hidden with a NaN has nothing but NaN logits: its three outputs are NaN (an lse of -inf would say that
+    the row has no distribution); the other rows keep their bits. A row of W with a NaN gives NaN in every row, alone or with the whole vector of
+    columns that an epilogue step takes."""
+    from tests.test_gpu_timeout import _head_inputs
+    H, W, y, _, _ = _head_inputs(N, V, Hd)
+    ref = tt.lmhead_token_logprob(H, W, y)
+    rows = sorted({0, N // 2, N - 1})
+    bad = H.clone()
+    for i, r in enumerate(rows):
+        bad[r, (17 * i) % Hd] = float("nan")
+    bad[rows[-1]] = float("nan")
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[rows] = False
+    err = tt.new_err("cuda")
+    for t, r in zip(tt.lmhead_token_logprob(bad, W, y, err=err), ref):
+        assert torch.isnan(t[rows]).all() and torch.equal(t[keep], r[keep])
+    assert int(err.item()) == 0
+    for lo, hi in ((V - 1, V), (0, min(V, 32)), (V // 64 * 32, V // 64 * 32 + 32)):
+        w = W.clone()
+        w[lo:hi, 3] = float("nan")
+        for t in tt.lmhead_token_logprob(H, w, y):
+            assert torch.isnan(t).all(), (lo, hi)

@@ -271,6 +271,18 @@ def _rope_tables(rot, sections, interleaved, base, inv_freq):
     return (ctypes.c_uint8 * half)(*axis), (ctypes.c_double * half)(*freq)
 
 
+def _frequencies(inv_freq):
+    """inv_freq as the key of _rope_tables. A tensor on a device is refused: to read it back would make every call wait
+    for the stream, and fail in a capture."""
+    if inv_freq is None:
+        return None
+    if isinstance(inv_freq, torch.Tensor):
+        if inv_freq.device.type != "cpu":
+            raise TypeError("inv_freq must be on the host: read it back once (inv_freq.tolist()) and keep the list")
+        inv_freq = inv_freq.tolist()
+    return tuple(float(f) for f in inv_freq)
+
+
 def _rope_rows(t, name):
     """(N, heads, d, elements between tokens) of a tensor of heads."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 3:
@@ -290,7 +302,7 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
 
     `positions`: int32 [N] (one axis, e.g. Tree.tok_pos) or [axes, N]. The first `rot_dim` (default d) dimensions turn,
     in the pairs (i, i + rot_dim/2) or, `adjacent`, (2i, 2i + 1), by positions times the frequencies base^(-2i/rot_dim)
-    or `inv_freq` (rot_dim/2 numbers). `sections`: how many frequencies each axis takes, one after the other or,
+    or `inv_freq` (rot_dim/2 numbers on the host). `sections`: how many frequencies each axis takes, one after the other or,
     `interleaved`, the axes in turn while their section lasts. q and k may be views of one buffer (tokens any stride
     apart); `out` = (q_out, k_out) may be (q, k). `inverse` turns back."""
     N, hq, d, q_ld = _rope_rows(q, "q")
@@ -314,8 +326,7 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
         sections = (rot // 2,)
     elif len(sections) != axes:
         raise ValueError("positions and sections must agree on the number of axes")
-    axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base),
-                              None if inv_freq is None else tuple(float(f) for f in inv_freq))
+    axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base), _frequencies(inv_freq))
     if out is None:
         qo = torch.empty_like(q, memory_format=torch.contiguous_format)
         ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)

@@ -203,3 +203,18 @@ def test_angles_of_any_frequency_at_far_positions(tt):
         x = _f64(x)[:, 0]
         assert np.abs(x[:, :16] - np.cos(theta)).max() <= tol
         assert np.abs(x[:, 16:] - sign * np.sin(theta)).max() <= tol
+
+
+def test_frequencies_on_the_device_are_refused(tt):
+    q = torch.randn(4, 2, 8, device="cuda")
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    f = torch.tensor([1.0, 0.1, 0.01, 0.001])
+    with pytest.raises(TypeError):
+        tt.rope(q, None, pos, inv_freq=f.cuda())
+    a, b = tt.rope(q, None, pos, inv_freq=f)[0], tt.rope(q, None, pos, inv_freq=f.tolist())[0]
+    assert torch.equal(a, b)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(q)
+    with torch.cuda.graph(graph):
+        tt.rope(q, None, pos, inv_freq=f, out=(out, None))
+    graph.replay()
+    assert torch.equal(out, a)

@@ -113,3 +113,15 @@ def test_binding_refuses_cpu_tensors_and_bad_tables():
             _rope_tables(8, bad[0], False, 1e4, bad[1])
     axis, freq = _rope_tables(8, (2, 1, 1), True, 1e4, None)
     assert list(axis) == [0, 1, 2, 0] and list(freq) == [1e4 ** (-i / 4) for i in range(4)]
+
+
+def test_frequencies_are_host_numbers():
+    """A tensor on a device would be read back at every call; one on the host, an array or a list gives the same key."""
+    from prefix_tree_gb300._native import _frequencies
+    f = [1.0, 0.5, 0.25]
+    want = tuple(f)
+    assert _frequencies(None) is None
+    assert _frequencies(f) == _frequencies(torch.tensor(f)) == _frequencies(torch.tensor(f).numpy()) == want
+    for t in (torch.float32, torch.float64):
+        with pytest.raises(TypeError, match="host"):
+            _frequencies(torch.empty(3, dtype=t, device="meta"))

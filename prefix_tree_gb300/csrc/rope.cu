@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 namespace tt {
 namespace {
@@ -153,9 +154,12 @@ uint64_t turns_of(double f) {
       0x272117e2ef7e4a0e, 0xc7fe25fff7816603, 0xfbcbc462d6829b47, 0xdb4d9fb3c9f2c26d, 0xd3d18fd9a797fa8b,
       0x5d49eeb1faf97c5e, 0xcf41ce7de294a4ba, 0x9afed7ec47e35742};
   typedef unsigned __int128 u128;
-  int e;
-  const uint64_t mant = (uint64_t)std::ldexp(std::frexp(std::fabs(f), &e), 53);
-  const int s = e - 53;
+  // mant and s from f's bits (frexp and ldexp took 0.7 us for the 64 frequencies of a call)
+  uint64_t bits;
+  std::memcpy(&bits, &f, 8);
+  const int e = (int)(bits >> 52 & 0x7ff);
+  const uint64_t mant = (bits & ((uint64_t(1) << 52) - 1)) | (uint64_t)(e != 0) << 52;
+  const int s = (e ? e : 1) - 1075;
   u128 x = 0;
   if (s >= 0) {
     const int j = s / 64, o = s % 64;
@@ -165,7 +169,7 @@ uint64_t turns_of(double f) {
     x = ((u128)digits[0] << 64 | digits[1]) >> -s;
   }
   const uint64_t t = (uint64_t)((mant * x) >> 64);
-  return f < 0 ? 0 - t : t;
+  return bits >> 63 ? 0 - t : t;
 }
 
 template <typename T>

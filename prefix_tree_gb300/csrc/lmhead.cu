@@ -67,7 +67,7 @@
 // The added sum costs the forward nothing: 12,669 x 151,936 x 2048 in 4.0 ms
 // for a few passes and 4.3 under the power cap, where the log-prob alone takes
 // 4.1 and 4.4 (its epilogue masks every column, this one only those of the
-// last tile). An epilogue tile takes 2.1 us (EPI_DZ_H 2.8), so up to Hd = 256
+// last tile). An epilogue tile takes 2.2 us (EPI_DZ_H 2.8), so up to Hd = 256
 // it bounds the GEMM, above it the tensor pipe (80 % busy at Hd = 1024).
 #include <algorithm>
 #include <atomic>

@@ -271,7 +271,9 @@ __device__ __forceinline__ void fold(float2& s, float2& q, const uint4& u, float
   }
 }
 
-constexpr int kDepth = 2;  // batches of a thread on their way from memory or in use (3 and 4 took as long)
+// Batches of a thread on their way from memory or in use. (3 and 4 took as long where four warps take a row of 1000 to
+// 151,936 logits; three for eight warps are 48 KB, more than there is beside the alternatives' lists.)
+constexpr int kDepth = 2;
 
 // Shared memory that a group's vectors pass through: each thread its own places, so no thread waits for another.
 template <int WARPS>

@@ -146,6 +146,44 @@ TT_API int tt_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, c
                    int64_t pos_ld, int axes, const uint8_t* axis_host, const double* freq_host, int adjacent,
                    int inverse, tt_stream_t stream);
 
+/* ------------------------------- norm of the heads with rotary positions
+ * RMS norm of every head of Q and K, and the rotary positions of tt_rope
+ * behind it, in one pass (nothing is rounded between the two):
+ *   r = (Σ_j x_j²/d + eps)^-1/2,   n_j = w_j·x_j·r,   out = R(pos)·n,
+ * for every head of every token, with one weight for all heads of q and one
+ * for those of k: [d] of type w_dtype (dtype or TT_DT_F32), NULL = ones.
+ * q, k, their outputs and strides, pos, axes, tables and adjacent as in
+ * tt_rope; rot = 0: the norm alone (pos and the tables may be NULL). An
+ * output may be its own input (same stride), not another tensor's.
+ * Sums are fp32: a head's sum of squares has to stay below 3e38. A head of
+ * zeros gives zeros with eps > 0 (NaN with eps = 0).
+ * Limits (TT_ERR_UNSUPPORTED): d and rot even, d <= 512, rot <= 256, at most 4
+ * axes and 1024 heads each. N = 0 does nothing. 16-byte accesses under the
+ * rule of tt_rope; results of both kinds of access agree to fp32 rounding of
+ * the sum. */
+TT_API int tt_qk_norm_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, const void* k, void* k_out,
+                           int64_t k_ld, int64_t k_out_ld, int dtype, int64_t N, int Hq, int Hkv, int d,
+                           const void* q_weight, const void* k_weight, int w_dtype, float eps, int rot,
+                           const int32_t* pos, int64_t pos_ld, int axes, const uint8_t* axis_host,
+                           const double* freq_host, int adjacent, tt_stream_t stream);
+/* Its backward. dq_out, dk_out: the gradients of the outputs; q, k: the
+ * forward's inputs; dq, dk: the gradients of those, all of type dtype with a
+ * stride each. With g = R(−pos)·d_out, h = w·g:
+ *   dx = r·h − x·r³·(Σ_j h_j·x_j)/d,   dw_j = Σ_{tokens, heads} g_j·x_j·r.
+ * dq may be dq_out or q (same stride), likewise dk. dq_weight, dk_weight:
+ * fp32 [d], written (NULL = not wanted); of a tensor with 0 heads, zeros.
+ * ws: tt_qk_norm_rope_bwd_workspace_bytes(d) bytes, 16-byte aligned, needed
+ * where a weight's gradient is wanted. The sums over tokens are fp32, in an
+ * order that the sizes and the device fix: repeated calls agree bitwise. */
+TT_API size_t tt_qk_norm_rope_bwd_workspace_bytes(int d);
+TT_API int tt_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_ld, const void* q, int64_t q_ld, void* dq, int64_t dq_ld,
+                               const void* dk_out, int64_t dk_out_ld, const void* k, int64_t k_ld, void* dk,
+                               int64_t dk_ld, int dtype, int64_t N, int Hq, int Hkv, int d, const void* q_weight,
+                               const void* k_weight, int w_dtype, float eps, int rot, const int32_t* pos,
+                               int64_t pos_ld, int axes, const uint8_t* axis_host, const double* freq_host,
+                               int adjacent, float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes,
+                               tt_stream_t stream);
+
 /* ---------------------------------------------------------- tree attention
  * Forward ("Tree Training", Abstract: attention adapted so each token's
  * result equals independent per-branch causal attention):
@@ -464,6 +502,66 @@ TT_API int tt_token_logprob_bwd(const void* logits, int dtype, int64_t N, int64_
                                 const float* entropy, const int32_t* targets, const float* dlogp,
                                 const float* dentropy, const float* dlse, const int32_t* top_ids, const float* dtop,
                                 int k, void* dlogits, int32_t* err, tt_stream_t stream);
+
+/* ------------------------------------------------ clipped policy objective
+ * The objective of a policy step over a tree's tokens, as a loss:
+ *   r_t = e^(logp_t − old_logp_t),   x_t = ref_logp_t − logp_t,
+ *   loss = Σ_t w_t·( −gain_t·min(r_t, 1 + clip_hi)
+ *                    + cost_t·min(max(r_t, 1 − clip_lo), dual_clip)
+ *                    + kl_coef·(e^x_t − 1 − x_t) − entropy_coef·entropy_t ).
+ * A token of a shared prefix belongs to rollouts with advantages A_b of both
+ * signs, and the sum of min(r·A_b, clip(r)·A_b) over them needs gain = Σ A_b
+ * over the positive and cost = Σ |A_b| over the negative ones: adv = gain and
+ * adv_neg = cost. With adv_neg NULL, adv is one signed advantage per token:
+ * gain = max(adv, 0), cost = max(−adv, 0).
+ * Gradients (times g): d/dlogp = w·( −gain·r·[r <= 1 + clip_hi] +
+ * cost·r·[1 − clip_lo <= r <= dual_clip] − kl_coef·(e^x − 1) ), d/dentropy =
+ * −w·entropy_coef.
+ * All arrays fp32 [N]: old_logp, adv; adv_neg; ref_logp (NULL: no KL term);
+ * weights (NULL: ones). A token of weight 0 is masked: it adds nothing, its
+ * gradients are 0 and its other inputs are not regarded. NaN or infinite
+ * inputs of other tokens give what the formulas give (a sum may be NaN).
+ * sums: fp32 [4], written: loss, Σ w·(the gain and cost terms), Σ w·(e^x − 1
+ * − x), Σ w·entropy, all without g; summed in about 48 bits in a fixed order
+ * and rounded once. Repeated calls agree bitwise.
+ * Limits (TT_ERR_INVALID_ARG): 0 <= clip_lo <= 1, clip_hi >= 0, dual_clip >= 1
+ * or 0 (no such bound), all coefficients finite. */
+typedef struct tt_policy {
+  float clip_lo, clip_hi; /* the ratio's range is [1 − clip_lo, 1 + clip_hi] */
+  float dual_clip;        /* most that a negative advantage is multiplied by; 0: no bound */
+  float kl_coef, entropy_coef;
+  float g;                /* the gradients are those of g·loss */
+} tt_policy;
+/* From log-probs (tt_token_logprob, tt_lmhead_token_logprob) and, for the
+ * entropy term, entropies (NULL: entropy_coef must be 0, sums[3] = 0). dlogp,
+ * dentropy: written, each may be NULL; they are what the backward calls of
+ * those take. policy: host struct, read before the call returns. ws:
+ * tt_policy_loss_workspace_bytes(N) bytes (0 up to 8192 tokens), 16-byte
+ * aligned. N = 0: sums = 0. */
+TT_API size_t tt_policy_loss_workspace_bytes(int64_t N);
+TT_API int tt_policy_loss(const float* logp, const float* entropy, const float* old_logp, const float* adv,
+                          const float* adv_neg, const float* ref_logp, const float* weights, int64_t N,
+                          const tt_policy* policy, float* sums, float* dlogp, float* dentropy, void* ws,
+                          size_t ws_bytes, tt_stream_t stream);
+/* From logits z [N][ld] of type dtype, any element alignment of the rows, with
+ * the gradient with respect to them, in one read:
+ *   dz_v = p_v·(−dlogp − dentropy·(log p_v + entropy)) + dlogp·[v = y].
+ * logp, entropy: fp32 [N], written. dlogits: type and ld of logits, NULL = not
+ * wanted; it may be logits itself; columns from V on are left as they are.
+ * A masked row (weight 0) is not read: its logp and entropy are 0 and its
+ * dlogits zeros. A target outside [0, V) (of a row that is not masked) sets
+ * `err` = TT_ERR_INVALID_ARG, the row's logp (hence the loss) is NaN and its
+ * dlogits zeros. Masked logits (−inf), rows with nothing but −inf (logp = −inf,
+ * entropy 0, dlogits zeros) and rows with a NaN or +inf (NaN) as in
+ * tt_token_logprob. ws: tt_policy_loss_logits_workspace_bytes(N) bytes,
+ * 16-byte aligned. Limit (TT_ERR_UNSUPPORTED): a row has to fit the shared
+ * memory of eight CTAs: V up to 900,000 (16-bit types) or 450,000 (fp32). */
+TT_API size_t tt_policy_loss_logits_workspace_bytes(int64_t N);
+TT_API int tt_policy_loss_logits(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* targets,
+                                 const float* old_logp, const float* adv, const float* adv_neg, const float* ref_logp,
+                                 const float* weights, const tt_policy* policy, float* sums, float* logp,
+                                 float* entropy, void* dlogits, void* ws, size_t ws_bytes, int32_t* err,
+                                 tt_stream_t stream);
 
 /* ---------------------------------------------------------------- trie build (host)
  * The step before tt_tree_build: the prefix tree of a task's rollouts from

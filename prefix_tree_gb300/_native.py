@@ -77,6 +77,15 @@ _SIGS = {
     "tt_weighted_logprob": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp]),
     "tt_rope": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _int, _i64, _int, _int, _int, _int, _vp, _i64, _int,
                        _vp, _vp, _int, _int, _vp]),
+    "tt_qk_norm_rope": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _int, _i64, _int, _int, _int, _vp, _vp, _int,
+                               _f32, _int, _vp, _i64, _int, _vp, _vp, _int, _vp]),
+    "tt_qk_norm_rope_bwd_workspace_bytes": (_sz, [_int]),
+    "tt_qk_norm_rope_bwd": (_int, [_vp, _i64] * 6 + [_int, _i64, _int, _int, _int, _vp, _vp, _int, _f32, _int, _vp, _i64,
+                                                     _int, _vp, _vp, _int, _vp, _vp, _vp, _sz, _vp]),
+    "tt_policy_loss_workspace_bytes": (_sz, [_i64]),
+    "tt_policy_loss": (_int, [_vp] * 7 + [_i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "tt_policy_loss_logits_workspace_bytes": (_sz, [_i64]),
+    "tt_policy_loss_logits": (_int, [_vp, _int, _i64, _i64, _i64] + [_vp] * 12 + [_sz, _vp, _vp]),
     "tt_token_logprob": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "tt_token_logprob_bwd": (_int, [_vp, _int, _i64, _i64, _i64] + [_vp] * 8 + [_int, _vp, _vp, _vp]),
     "tt_lmhead_logprob_workspace_bytes": (_sz, [_i64, _i64]),
@@ -296,21 +305,8 @@ def _rope_rows(t, name):
     return n, h, d, ld if n > 1 else h * d
 
 
-def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjacent=False, base=10000.0, inv_freq=None,
-         out=None, inverse=False):
-    """Rotary positions of q [N,Hq,d] and k [N,Hkv,d] (tt_rope; k may be None): returns (q_out, k_out).
-
-    `positions`: int32 [N] (one axis, e.g. Tree.tok_pos) or [axes, N]. The first `rot_dim` (default d) dimensions turn,
-    in the pairs (i, i + rot_dim/2) or, `adjacent`, (2i, 2i + 1), by positions times the frequencies base^(-2i/rot_dim)
-    or `inv_freq` (rot_dim/2 numbers on the host). `sections`: how many frequencies each axis takes, one after the other or,
-    `interleaved`, the axes in turn while their section lasts. q and k may be views of one buffer (tokens any stride
-    apart); `out` = (q_out, k_out) may be (q, k). `inverse` turns back."""
-    N, hq, d, q_ld = _rope_rows(q, "q")
-    hkv = k_ld = 0
-    if k is not None:
-        nk, hkv, dk, k_ld = _rope_rows(k, "k")
-        if k.dtype != q.dtype or nk != N or dk != d:
-            raise ValueError("q and k must share type, tokens and head dimension")
+def _rope_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq):
+    """Checked positions, their stride between axes, the axes, rot and the host tables of tt_rope."""
     if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32:
         raise TypeError("positions must be an int32 CUDA tensor")
     many = positions.dim() == 2
@@ -327,6 +323,25 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
     elif len(sections) != axes:
         raise ValueError("positions and sections must agree on the number of axes")
     axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base), _frequencies(inv_freq))
+    return positions, positions.stride(0) if many else N, axes, rot, axis, freq
+
+
+def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjacent=False, base=10000.0, inv_freq=None,
+         out=None, inverse=False):
+    """Rotary positions of q [N,Hq,d] and k [N,Hkv,d] (tt_rope; k may be None): returns (q_out, k_out).
+
+    `positions`: int32 [N] (one axis, e.g. Tree.tok_pos) or [axes, N]. The first `rot_dim` (default d) dimensions turn,
+    in the pairs (i, i + rot_dim/2) or, `adjacent`, (2i, 2i + 1), by positions times the frequencies base^(-2i/rot_dim)
+    or `inv_freq` (rot_dim/2 numbers on the host). `sections`: how many frequencies each axis takes, one after the other or,
+    `interleaved`, the axes in turn while their section lasts. q and k may be views of one buffer (tokens any stride
+    apart); `out` = (q_out, k_out) may be (q, k). `inverse` turns back."""
+    N, hq, d, q_ld = _rope_rows(q, "q")
+    hkv = k_ld = 0
+    if k is not None:
+        nk, hkv, dk, k_ld = _rope_rows(k, "k")
+        if k.dtype != q.dtype or nk != N or dk != d:
+            raise ValueError("q and k must share type, tokens and head dimension")
+    positions, pos_ld, axes, rot, axis, freq = _rope_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq)
     if out is None:
         qo = torch.empty_like(q, memory_format=torch.contiguous_format)
         ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
@@ -339,14 +354,117 @@ def rope(q, k, positions, rot_dim=None, sections=None, interleaved=False, adjace
         qo_ld = _rope_rows(qo, "q_out")[3]
         ko_ld = 0 if ko is None else _rope_rows(ko, "k_out")[3]
     _call("tt_rope", _device_of(q, k, positions, qo, ko), q.data_ptr(), qo.data_ptr(), q_ld, qo_ld, _ptr(k), _ptr(ko),
-          k_ld, ko_ld, _DTYPES[q.dtype], N, hq, hkv, d, rot, positions.data_ptr(), positions.stride(0) if many else N,
-          axes, axis, freq, 1 if adjacent else 0, 1 if inverse else 0)
+          k_ld, ko_ld, _DTYPES[q.dtype], N, hq, hkv, d, rot, positions.data_ptr(), pos_ld, axes, axis, freq,
+          1 if adjacent else 0, 1 if inverse else 0)
     return qo, ko
 
 
 def rope_bwd(dq, dk, positions, **how):
     """Gradients of the unrotated q and k from those of rope's outputs (the inverse rotation; arguments as rope's)."""
     return rope(dq, dk, positions, inverse=True, **how)
+
+
+# --------------------------------------------------------------------------- norm of the heads with rotary positions
+def _norm_pair(q, k):
+    """Checked (N, hq, hkv, d, stride of q, stride of k)."""
+    N, hq, d, q_ld = _rope_rows(q, "q")
+    if k is None:
+        return N, hq, 0, d, q_ld, 0
+    nk, hkv, dk, k_ld = _rope_rows(k, "k")
+    if k.dtype != q.dtype or nk != N or dk != d:
+        raise ValueError("q and k must share type, tokens and head dimension")
+    return N, hq, hkv, d, q_ld, k_ld
+
+
+def _norm_weights(q, q_weight, k_weight, d):
+    """TT_DT_* of the weights: one type for both, q's or fp32."""
+    kind = None
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype not in (q.dtype, torch.float32) or \
+                (kind is not None and w.dtype != kind):
+            raise TypeError(f"{n} must be a CUDA tensor of q's type or fp32, one type for both weights")
+        if w.shape != (d,) or not w.is_contiguous():
+            raise ValueError(f"{n} must be contiguous and have shape ({d},)")
+        kind = w.dtype
+    return _DTYPES[q.dtype if kind is None else kind]
+
+
+def _like_heads(t, like, name):
+    """Stride between tokens of a tensor with the shape and type of `like`."""
+    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} must have the shape and type of its input")
+    return _rope_rows(t, name)[3]
+
+
+def _norm_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq):
+    """As _rope_how; rot_dim = 0: no positions."""
+    if rot_dim is not None and int(rot_dim) == 0:
+        return None, 0, 1, 0, None, None
+    return _rope_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq)
+
+
+def qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, eps=1e-6, rot_dim=None, sections=None,
+                 interleaved=False, adjacent=False, base=10000.0, inv_freq=None, out=None):
+    """RMS norm of every head of q [N,Hq,d] and k [N,Hkv,d] and their rotary positions in one pass (tt_qk_norm_rope; k
+    may be None): returns (q_out, k_out). Weights [d] (q's type or fp32; None = ones) are shared by the heads. Positions
+    and tables as in `rope`; rot_dim = 0 leaves the rotation out (positions may be None). `out` = (q_out, k_out) may be
+    (q, k)."""
+    N, hq, hkv, d, q_ld, k_ld = _norm_pair(q, k)
+    w_dtype = _norm_weights(q, q_weight, k_weight, d)
+    positions, pos_ld, axes, rot, axis, freq = _norm_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq)
+    if out is None:
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        qo_ld, ko_ld = hq * d, hkv * d
+    else:
+        qo, ko = out
+        if (ko is None) != (k is None):
+            raise ValueError("out must have the shapes and type of q and k")
+        qo_ld = _like_heads(qo, q, "q_out")
+        ko_ld = 0 if ko is None else _like_heads(ko, k, "k_out")
+    _call("tt_qk_norm_rope", _device_of(q, k, positions, q_weight, k_weight, qo, ko), q.data_ptr(), qo.data_ptr(), q_ld,
+          qo_ld, _ptr(k), _ptr(ko), k_ld, ko_ld, _DTYPES[q.dtype], N, hq, hkv, d, _ptr(q_weight), _ptr(k_weight), w_dtype,
+          eps, rot, _ptr(positions), pos_ld, axes, axis, freq, 1 if adjacent else 0)
+    return qo, ko
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, rot_dim=None,
+                     sections=None, interleaved=False, adjacent=False, base=10000.0, inv_freq=None, out=None, ws=None,
+                     want_dw=True):
+    """Gradients of qk_norm_rope (tt_qk_norm_rope_bwd): from those of its outputs and its inputs q, k, returns (dq, dk,
+    dq_weight, dk_weight), the last two fp32 [d] (None without `want_dw`, and dk_weight without k). `out` = (dq, dk) may
+    be (dq_out, dk_out) or (q, k)."""
+    N, hq, hkv, d, q_ld, k_ld = _norm_pair(q, k)
+    w_dtype = _norm_weights(q, q_weight, k_weight, d)
+    positions, pos_ld, axes, rot, axis, freq = _norm_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq)
+    if (dk_out is None) != (k is None):
+        raise ValueError("dk_out goes with k")
+    dqo_ld = _like_heads(dq_out, q, "dq_out")
+    dko_ld = 0 if k is None else _like_heads(dk_out, k, "dk_out")
+    if out is None:
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        dk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        dq_ld, dk_ld = hq * d, hkv * d
+    else:
+        dq, dk = out
+        if (dk is None) != (k is None):
+            raise ValueError("out must have the shapes and type of q and k")
+        dq_ld = _like_heads(dq, q, "dq")
+        dk_ld = 0 if dk is None else _like_heads(dk, k, "dk")
+    dwq = dwk = None
+    if want_dw:
+        dwq = torch.empty(d, dtype=torch.float32, device=q.device)
+        dwk = None if k is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = torch.empty(lib().tt_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=q.device)
+    _call("tt_qk_norm_rope_bwd", _device_of(q, k, dq_out, dk_out, positions, q_weight, k_weight, dq, dk, ws),
+          dq_out.data_ptr(), dqo_ld, q.data_ptr(), q_ld, dq.data_ptr(), dq_ld, _ptr(dk_out), dko_ld, _ptr(k), k_ld,
+          _ptr(dk), dk_ld, _DTYPES[q.dtype], N, hq, hkv, d, _ptr(q_weight), _ptr(k_weight), w_dtype, eps, rot,
+          _ptr(positions), pos_ld, axes, axis, freq, 1 if adjacent else 0, _ptr(dwq), _ptr(dwk), _ptr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return dq, dk, dwq, dwk
 
 
 # --------------------------------------------------------------------------- attention
@@ -743,6 +861,97 @@ def lmhead_logprob_bwd(hidden, w_vocab, targets, lse, weights=None, g=1.0, out=N
                                      _p(dw), _p(ws), ws.numel(), _p(err), _stream(dev))
     _check(rc, "tt_lmhead_logprob_bwd")
     return dh, dw
+
+
+class _Policy(ctypes.Structure):
+    _fields_ = [(n, _f32) for n in ("clip_lo", "clip_hi", "dual_clip", "kl_coef", "entropy_coef", "g")]
+
+
+@functools.lru_cache(maxsize=64)
+def _policy(clip, dual_clip, kl_coef, entropy_coef, g):
+    lo, hi = clip
+    return ctypes.byref(_Policy(lo, hi, 0.0 if dual_clip is None else dual_clip, kl_coef, entropy_coef, g))
+
+
+def _policy_of(clip, dual_clip, kl_coef, entropy_coef, g):
+    """The host struct tt_policy. clip: one number for both sides, or (below, above)."""
+    if not isinstance(clip, (tuple, list)):
+        clip = (clip, clip)
+    if dual_clip is not None and not dual_clip >= 1:
+        raise ValueError("dual_clip must be at least 1 (None: no such bound)")
+    return _policy(tuple(clip), dual_clip, kl_coef, entropy_coef, g)
+
+
+def policy_loss(logp, old_logp, adv, adv_neg=None, ref_logp=None, entropy=None, weights=None, clip=0.2, dual_clip=None,
+                kl_coef=0.0, entropy_coef=0.0, g=1.0, out=None, ws=None):
+    """Clipped policy objective from log-probs [N] (tt_policy_loss): (sums, dlogp, dentropy), all fp32: sums [4] = loss,
+    policy, KL and entropy terms; dlogp [N] and dentropy [N] (None without `entropy`) the gradients of g·loss, which
+    token_logprob_bwd and lmhead_token_logprob_bwd take. adv: a signed advantage per token, or with `adv_neg` the sums
+    of the positive and of the negative advantages (magnitudes) of the rollouts through it. Tokens of weight 0 are
+    masked."""
+    _per_row(logp, torch.float32, "logp", (logp.numel(),) if isinstance(logp, torch.Tensor) else (0,), True)
+    N = logp.numel()
+    for t, n, need in ((old_logp, "old_logp", True), (adv, "adv", True), (adv_neg, "adv_neg", False),
+                       (ref_logp, "ref_logp", False), (entropy, "entropy", False), (weights, "weights", False)):
+        _per_row(t, torch.float32, n, (N,), need)
+    dev = logp.device
+    policy = _policy_of(clip, dual_clip, kl_coef, entropy_coef, g)
+    if out is None:
+        sums, dlogp = torch.empty(4, dtype=torch.float32, device=dev), torch.empty_like(logp)
+        dent = None if entropy is None else torch.empty_like(logp)
+    else:
+        sums, dlogp, dent = out
+        _per_row(sums, torch.float32, "sums", (4,), True)
+        _per_row(dlogp, torch.float32, "dlogp", (N,))
+        _per_row(dent, torch.float32, "dentropy", (N,))
+    if ws is None:
+        nbytes = lib().tt_policy_loss_workspace_bytes(N)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call("tt_policy_loss", _device_of(logp, old_logp, adv, adv_neg, ref_logp, entropy, weights, sums, dlogp, dent, ws),
+          logp.data_ptr(), _ptr(entropy), old_logp.data_ptr(), adv.data_ptr(), _ptr(adv_neg), _ptr(ref_logp),
+          _ptr(weights), N, policy, sums.data_ptr(), _ptr(dlogp), _ptr(dent), _ptr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return sums, dlogp, dent
+
+
+def policy_loss_logits(logits, targets, old_logp, adv, adv_neg=None, ref_logp=None, weights=None, clip=0.2,
+                       dual_clip=None, kl_coef=0.0, entropy_coef=0.0, g=1.0, want_dlogits=True, out=None, ws=None,
+                       err=None):
+    """Clipped policy objective from logits [N,V] (bf16, fp16 or fp32; rows may be padded) with the gradient with respect
+    to them, in one read (tt_policy_loss_logits): (sums, logp, entropy, dlogits). Arguments as in policy_loss; `out` =
+    (sums, logp, entropy, dlogits), whose dlogits may be logits itself. A masked row (weight 0) is not read: its logp,
+    entropy and dlogits are 0."""
+    N, V, ld = _logit_rows(logits, "logits")
+    rows, dev = (N,), logits.device
+    _per_row(targets, torch.int32, "targets", rows, True)
+    for t, n, need in ((old_logp, "old_logp", True), (adv, "adv", True), (adv_neg, "adv_neg", False),
+                       (ref_logp, "ref_logp", False), (weights, "weights", False)):
+        _per_row(t, torch.float32, n, rows, need)
+    policy = _policy_of(clip, dual_clip, kl_coef, entropy_coef, g)
+    if out is None:
+        sums, logp, entropy = (torch.empty(n, dtype=torch.float32, device=dev) for n in (4, N, N))
+        dl = None
+        if want_dlogits:
+            dl = torch.empty((N, ld), dtype=logits.dtype, device=dev)
+            if ld != V:
+                dl = dl[:, :V]
+    else:
+        sums, logp, entropy, dl = out
+        _per_row(sums, torch.float32, "sums", (4,), True)
+        _per_row(logp, torch.float32, "logp", rows, True)
+        _per_row(entropy, torch.float32, "entropy", rows, True)
+        if dl is not None and (dl.dtype != logits.dtype or dl.shape != logits.shape or
+                               (N > 1 and dl.stride() != logits.stride()) or (V > 1 and dl.stride(1) != 1)):
+            raise ValueError("dlogits must have the type, shape and strides of logits")
+    if ws is None:
+        ws = torch.empty(max(1, lib().tt_policy_loss_logits_workspace_bytes(N)), dtype=torch.uint8, device=dev)
+    err = new_err(dev) if err is None else err
+    _call("tt_policy_loss_logits",
+          _device_of(logits, targets, old_logp, adv, adv_neg, ref_logp, weights, sums, logp, entropy, dl, ws, err),
+          logits.data_ptr(), _DTYPES[logits.dtype], N, V, ld, targets.data_ptr(), old_logp.data_ptr(), adv.data_ptr(),
+          _ptr(adv_neg), _ptr(ref_logp), _ptr(weights), policy, sums.data_ptr(), logp.data_ptr(), entropy.data_ptr(),
+          _ptr(dl), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr())
+    return sums, logp, entropy, dl
 
 
 def _lmhead_args(hidden, w_vocab, targets):

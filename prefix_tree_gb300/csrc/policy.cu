@@ -1,0 +1,610 @@
+// Clipped policy objective with a KL term and an entropy bonus over the tokens
+// of rollout trees, from per-token log-probs, or from logits together with the
+// gradient with respect to them.
+//
+//   r = e^{logp − old},  x = ref − logp
+//   L = Σ_t w·( −gain·min(r, 1 + ε_hi) + cost·min(max(r, 1 − ε_lo), c) + β·(e^x − 1 − x) − γ·H )
+//   dlogp = g·w·( −gain·r·[r <= 1 + ε_hi] + cost·r·[1 − ε_lo <= r <= c] − β·(e^x − 1) ),   dH = −g·w·γ
+//   dz_v = p_v·(−dlogp − dH·(log p_v + H)) + dlogp·[v = y]
+//
+// A token of a shared prefix belongs to several rollouts with advantages A_b
+// of both signs; min(r·A, clip(r)·A) is A·min(r, 1 + ε_hi) for A > 0 and
+// A·max(r, 1 − ε_lo) for A < 0, so the sum over them needs two numbers only:
+// gain = Σ A_b over the positive, cost = Σ |A_b| over the negative ones.
+//
+// The form on log-probs is elementwise plus three sums: bound by latency up to
+// some 10^5 tokens, then by memory. The form on logits reads a row once into
+// shared memory, takes (max, Σe^d, Σd·e^d) there, joins them over the CTAs
+// of the row's cluster, and forms dz from the same shared memory: one read of
+// the logits and one write of the gradient, bound by memory.
+//
+// Where the numbers need it: logp − old is formed from (z_y − m), log S and
+// old by exact two-sums, with log S as a pair, since rounding logp (about 12)
+// to fp32 first would leave 5e-7 in the ratio; e^x − 1 − x by its series
+// below 1/2, where the difference cancels. The sums over tokens are carried as
+// pairs of floats (about 48 bits), in a fixed order.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "logit_rows.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace tt {
+namespace {
+
+// ------------------------------------------------------------------ sums in pairs of floats
+struct F2 {
+  float hi, lo;
+};
+__device__ __forceinline__ F2 two_sum(float a, float b) {
+  const float s = a + b, bb = s - a;
+  return {s, (a - (s - bb)) + (b - bb)};
+}
+__device__ __forceinline__ F2 add(F2 x, F2 y) {
+  F2 s = two_sum(x.hi, y.hi);
+  s.lo += x.lo + y.lo;
+  return two_sum(s.hi, s.lo);
+}
+__device__ __forceinline__ void add(F2& x, float y) {
+  const F2 s = two_sum(x.hi, y);
+  x.hi = s.hi;
+  x.lo += s.lo;
+}
+// Policy, KL and entropy terms.
+struct Sums {
+  F2 v[3];
+};
+
+// The warp's sums in lane 0.
+__device__ __forceinline__ void sum_warp(Sums& s) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      s.v[i] = add(s.v[i], {__shfl_down_sync(kAll, s.v[i].hi, o), __shfl_down_sync(kAll, s.v[i].lo, o)});
+}
+// The block's sums in thread 0. A multiple of 32 threads, up to 1024; `room`: a Sums per warp.
+__device__ __forceinline__ void sum_block(Sums& s, Sums* room) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  sum_warp(s);
+  if (lane == 0) room[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    s = lane < warps ? room[lane] : Sums{};
+    sum_warp(s);
+  }
+}
+
+// ------------------------------------------------------------------ the objective of one token
+struct Policy {
+  float lo, hi, dual, kl, ent, g;  // 1 − ε_lo, 1 + ε_hi, c, β, γ, g
+};
+struct Inputs {  // per token, fp32 [N] each
+  const float *old_logp, *adv, *adv_neg, *ref_logp, *weights;
+};
+struct Token {
+  float old_logp, gain, cost, ref_logp, w;
+};
+__device__ __forceinline__ void split(Token& t, float adv, bool two_sided, float adv_neg) {
+  t.gain = two_sided || !(adv < 0.f) ? adv : 0.f;
+  t.cost = two_sided ? adv_neg : adv < 0.f ? -adv : 0.f;
+}
+
+// e^x − 1 − x
+__device__ __forceinline__ float exp_rest(float x, float em1) {
+  if (fabsf(x) >= 0.5f) return em1 - x;
+  // x²·Σ x^i/(i + 2)!: the first term left out is below 2^-25 of the sum
+  float p = 2.48015873e-5f;
+  p = fmaf(p, x, 1.98412698e-4f);
+  p = fmaf(p, x, 1.38888889e-3f);
+  p = fmaf(p, x, 8.33333333e-3f);
+  p = fmaf(p, x, 4.16666667e-2f);
+  p = fmaf(p, x, 1.66666667e-1f);
+  p = fmaf(p, x, 0.5f);
+  return p * x * x;
+}
+
+// move = logp − old, x = ref − logp (has_ref). Terms without the weight; slope = dL/dlogp without g and w. Comparisons
+// are such that a NaN stays one.
+__device__ __forceinline__ void objective(const Policy& c, float gain, float cost, float move, bool has_ref, float x,
+                                          float& policy, float& kl, float& slope) {
+  const float r = expf(move);
+  policy = -gain * (r > c.hi ? c.hi : r);
+  slope = r > c.hi ? 0.f : -gain * r;
+  if (cost != 0.f) {
+    const float b = r < c.lo ? c.lo : r;
+    policy = fmaf(cost, b > c.dual ? c.dual : b, policy);
+    if (!(r < c.lo) && !(r > c.dual)) slope = fmaf(cost, r, slope);
+  }
+  kl = 0.f;
+  if (has_ref) {
+    const float em1 = expm1f(x);
+    kl = exp_rest(x, em1);
+    if (c.kl != 0.f) slope = fmaf(-c.kl, em1, slope);
+  }
+}
+
+// sums[4] = loss, policy, KL, entropy
+__device__ __forceinline__ void finish(const Sums& s, const Policy& c, float* sums) {
+  const double p = (double)s.v[0].hi + (double)s.v[0].lo, k = (double)s.v[1].hi + (double)s.v[1].lo,
+               h = (double)s.v[2].hi + (double)s.v[2].lo;
+  double loss = p;
+  if (c.kl != 0.f) loss += (double)c.kl * k;
+  if (c.ent != 0.f) loss -= (double)c.ent * h;
+  sums[0] = (float)loss;
+  sums[1] = (float)p;
+  sums[2] = (float)k;
+  sums[3] = (float)h;
+}
+
+// ------------------------------------------------------------------ on log-probs
+struct LogpArgs {
+  const float *logp, *entropy;
+  Inputs in;
+  int64_t N;
+  Policy c;
+  float *sums, *dlogp, *dentropy;
+  Sums* parts;
+};
+constexpr int kTokenThreads = 256, kPerThread = 4, kTokens = kTokenThreads * kPerThread;
+constexpr int kOneLaunch = 8;  // blocks whose sums one launch joins (a cluster)
+
+// VEC: 16-byte accesses (all arrays aligned to 16 bytes).
+template <bool VEC>
+__global__ void __launch_bounds__(kTokenThreads) policy_tokens_kernel(const LogpArgs a) {
+  __shared__ Sums room[kTokenThreads / 32];
+  __shared__ Sums of_ctas[kOneLaunch];
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  Sums s = {};
+  auto get = [&](const float* p, float (&v)[kPerThread], int64_t t, bool whole) {
+    if (VEC && whole) {
+      const float4 f = *reinterpret_cast<const float4*>(p + t);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        const int64_t u = VEC ? t + i : t + i * kTokenThreads;
+        v[i] = u < a.N ? p[u] : 0.f;
+      }
+    }
+  };
+  auto put = [&](float* p, const float (&v)[kPerThread], int64_t t, bool whole) {
+    if (VEC && whole) {
+      *reinterpret_cast<float4*>(p + t) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        const int64_t u = VEC ? t + i : t + i * kTokenThreads;
+        if (u < a.N) p[u] = v[i];
+      }
+    }
+  };
+  const int64_t t = t0 + (VEC ? kPerThread * (int)threadIdx.x : (int)threadIdx.x);
+  const bool whole = VEC && t + kPerThread <= a.N;
+  float lp[kPerThread], old[kPerThread], adv[kPerThread], dl[kPerThread], dh[kPerThread];
+  float neg[kPerThread] = {}, ref[kPerThread] = {}, w[kPerThread] = {}, h[kPerThread] = {};
+  get(a.logp, lp, t, whole);
+  get(a.in.old_logp, old, t, whole);
+  get(a.in.adv, adv, t, whole);
+  if (a.in.adv_neg) get(a.in.adv_neg, neg, t, whole);
+  if (a.in.ref_logp) get(a.in.ref_logp, ref, t, whole);
+  if (a.in.weights) get(a.in.weights, w, t, whole);
+  if (a.entropy) get(a.entropy, h, t, whole);
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int64_t u = VEC ? t + i : t + i * kTokenThreads;
+    const float wt = u < a.N ? (a.in.weights ? w[i] : 1.f) : 0.f;
+    dl[i] = dh[i] = 0.f;
+    if (wt == 0.f) continue;  // a masked token, whatever its other inputs hold
+    Token k;
+    split(k, adv[i], a.in.adv_neg != nullptr, neg[i]);
+    float policy, kl, slope;
+    objective(a.c, k.gain, k.cost, lp[i] - old[i], a.in.ref_logp != nullptr, a.in.ref_logp ? ref[i] - lp[i] : 0.f,
+              policy, kl, slope);
+    add(s.v[0], wt * policy);
+    add(s.v[1], wt * kl);
+    if (a.entropy) add(s.v[2], wt * h[i]);
+    dl[i] = a.c.g * wt * slope;
+    dh[i] = a.c.ent != 0.f ? -a.c.g * wt * a.c.ent : 0.f;
+  }
+  if (a.dlogp) put(a.dlogp, dl, t, whole);
+  if (a.dentropy) put(a.dentropy, dh, t, whole);
+  sum_block(s, room);
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0) finish(s, a.c, a.sums);
+  } else if (a.parts) {
+    if (threadIdx.x == 0) a.parts[blockIdx.x] = s;
+  } else {  // the grid is one cluster: its first CTA adds up
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();  // every CTA has started
+    if (threadIdx.x == 0) *cluster.map_shared_rank(&of_ctas[blockIdx.x], 0) = s;
+    cluster.sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      for (unsigned r = 1; r < gridDim.x; ++r)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s.v[i] = add(s.v[i], of_ctas[r].v[i]);
+      finish(s, a.c, a.sums);
+    }
+  }
+}
+
+// The sums of n parts in order: of blocks of tokens (ROWS = false), or of rows of logits (a float4 each).
+constexpr int kSumThreads = 1024;
+template <bool ROWS>
+__global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const void* parts, int64_t n, const Policy c, float* sums) {
+  __shared__ Sums room[kSumThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Sums s = {};
+  for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
+    if (ROWS) {
+      const float4 f = static_cast<const float4*>(parts)[i];
+      add(s.v[0], f.x);
+      add(s.v[1], f.y);
+      add(s.v[2], f.z);
+    } else {
+      const Sums p = static_cast<const Sums*>(parts)[i];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) s.v[q] = add(s.v[q], p.v[q]);
+    }
+  }
+  sum_block(s, room);
+  if (threadIdx.x == 0) finish(s, c, sums);
+}
+
+// ------------------------------------------------------------------ on logits
+struct LogitsArgs {
+  const void* z;
+  void* dz;  // NULL: no gradient
+  int64_t N, V, ld;
+  const int32_t* y;
+  Inputs in;
+  Policy c;
+  float *logp, *entropy;
+  float4* rows;  // the row's terms
+  int32_t* err;
+};
+
+// log s for s >= 1 (or 0, inf, NaN) as a pair: s = 2^k·f with f in [1/√2, √2), log s = k·ln 2 + log f. ln 2 is split so
+// that k times its first part is exact.
+__device__ __forceinline__ F2 log_pair(float s) {
+  const uint32_t b = __float_as_uint(s);
+  if (!(s > 0.f) || s == INFINITY) return {logf(s), 0.f};
+  const int k = (int)((b - 0x3f3504f3u) & 0xff800000u) >> 23;  // (the bits of 1/√2)
+  const float f = __uint_as_float(b - ((uint32_t)k << 23));
+  constexpr float kHi = 0.693145751953125f, kLo = 1.42860682e-6f;  // ln 2 to 15 bits, and the rest
+  F2 l = two_sum((float)k * kHi, logf(f));
+  l.lo = fmaf((float)k, kLo, l.lo);
+  return l;
+}
+
+// What the CTAs of a row tell each other: (m, s, u) of the slice and the target's logit, where it lies there.
+struct Slice {
+  Stat t;
+  float zy;
+};
+
+constexpr int kBatch = 4;   // vectors of a thread at once: one rescaling for all of them
+constexpr int kAhead = 4;   // batches on their way beside the one in use
+constexpr int kCtasMost = 8;
+template <int WARPS>
+constexpr int kGroups = WARPS == 1 ? 4 : 1;  // groups of a block: each takes rows of its own
+
+// A row is taken by a group of WARPS warps of each of the CL CTAs of a cluster (WARPS < 8: CL = 1). `room`: vectors of a
+// group's slice in shared memory; a thread copies, sums and turns its own vectors, so that the copies need no barrier.
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_kernel(const LogitsArgs a, int CL, int room) {
+  constexpr int VN = Row<T>::VN, kGroup = 32 * WARPS;
+  extern __shared__ __align__(16) uint4 slices[];
+  __shared__ Slice part[WARPS * kGroups<WARPS>];
+  __shared__ Slice of_ctas[kCtasMost];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, group = threadIdx.x / kGroup;
+  const int tid = threadIdx.x % kGroup;
+  const int64_t row = kGroups<WARPS> > 1 ? (int64_t)blockIdx.x * kGroups<WARPS> + group : (int64_t)(blockIdx.x / CL);
+  const int rank = WARPS == 8 ? (int)(blockIdx.x % CL) : 0;
+  if (row >= a.N) return;  // (groups of one warp only)
+  if (WARPS == 8 && CL > 1) cg::this_cluster().barrier_arrive();  // waited for before the CTAs write to one another
+  const float w = a.in.weights ? a.in.weights[row] : 1.f;
+  const Row<T> z(static_cast<const T*>(a.z) + row * a.ld, a.V);
+  T* out = static_cast<T*>(a.dz) + row * a.ld;
+  const int lo = (int)((int64_t)z.nvec * rank / CL), hi = (int)((int64_t)z.nvec * (rank + 1) / CL);
+  const bool same = a.dz && (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(z.p) & 15);
+  const int wlo = z.whole_lo(), whi = z.whole_hi();
+  auto put = [&](int j, const uint4& u) {
+    if (same && j >= wlo && j < whi) {
+      *reinterpret_cast<uint4*>(out + z.first(j)) = u;
+    } else {
+      const int e = z.first(j);
+      const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int i = 0; i < VN; ++i)
+        if (e + i >= 0 && e + i < z.V) out[e + i] = t[i];
+    }
+  };
+  if (w == 0.f) {  // a masked row: its logits are not read
+    if (a.dz)
+      for (int j = lo + tid; j < hi; j += kGroup) put(j, make_uint4(0, 0, 0, 0));
+    if (rank == 0 && tid == 0) {
+      a.logp[row] = a.entropy[row] = 0.f;
+      a.rows[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (WARPS == 8 && CL > 1) cg::this_cluster().barrier_wait();
+    return;
+  }
+  uint4* buf = slices + group * room - lo;  // buf[j]: vector j
+  const int y = a.y[row];
+  const bool y_ok = y >= 0 && y < z.V;
+  auto fetch = [&](int at) {
+#pragma unroll
+    for (int v = 0; v < kBatch; ++v) {
+      const int j = at + v * kGroup;
+      if (j >= wlo && j < min(hi, whi))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf + j)), "l"(z.p + z.first(j))
+                     : "memory");
+      else if (j < hi)
+        buf[j] = z.load(j);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) fetch(lo + tid + b * kBatch * kGroup);
+  Stat t = {-INFINITY, 0.f, 0.f};
+  const float2 l2 = make_float2(kLog2e, kLog2e);
+  uint4 masked;
+#pragma unroll
+  for (int i = 0; i < VN; ++i) reinterpret_cast<T*>(&masked)[i] = static_cast<T>(-INFINITY);
+  for (int j = lo + tid; j < hi; j += kBatch * kGroup) {
+    fetch(j + kAhead * kBatch * kGroup);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    uint4 u[kBatch];
+#pragma unroll
+    for (int v = 0; v < kBatch; ++v) u[v] = j + v * kGroup < hi ? buf[j + v * kGroup] : masked;
+    static_assert(kBatch == 4, "four vectors");
+    rescale(t, fmaxf(t.m, Pairs<T>::max(u[0], u[1], u[2], u[3])));
+    const float mb = t.m == -INFINITY ? 0.f : t.m;
+    const float2 nm = make_float2(-mb, -mb);
+    float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < kBatch; ++v) fold<T, false>(s, q, u[v], nm, l2);
+    t.s += s.x + s.y;
+    t.u += q.x + q.y;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  t = join_warp(t, lane);
+  if (!plain_way_holds<T>(t.m)) {  // (see fold: extreme rows, again with every difference bounded)
+    t = {-INFINITY, 0.f, 0.f};
+    for (int j = lo + tid; j < hi; j += kGroup) {
+      const uint4 u = buf[j];
+      rescale(t, fmaxf(t.m, Pairs<T>::max(u)));
+      const float mb = t.m == -INFINITY ? 0.f : t.m;
+      float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
+      fold<T, true>(s, q, u, make_float2(-mb, -mb), l2);
+      t.s += s.x + s.y;
+      t.u += q.x + q.y;
+    }
+    t = join_warp(t, lane);
+  }
+  // the target's logit, by the thread that holds it
+  const int jy = y_ok ? (y + z.shift) / VN : -1;
+  const bool mine = jy >= lo && jy < hi && (jy - lo) % kGroup == tid;
+  float zy = -INFINITY;
+  if (mine) zy = static_cast<float>(reinterpret_cast<const T*>(buf + jy)[(y + z.shift) % VN]);
+  if constexpr (WARPS == 1) {
+    zy = __shfl_sync(kAll, zy, jy >= lo && jy < hi ? (jy - lo) % kGroup : 0);
+  } else {
+    Slice* p = part + group * WARPS;
+    zy = __shfl_sync(kAll, zy, jy >= lo && jy < hi ? (jy - lo) % 32 : 0);  // (its lane; the other warps' are unused)
+    if (lane == 0) p[warp] = {t, zy};
+    __syncthreads();
+    t = p[0].t;
+#pragma unroll
+    for (int q = 1; q < WARPS; ++q) merge(t, p[q].t);
+    zy = p[jy >= lo && jy < hi ? (jy - lo) % kGroup / 32 : 0].zy;
+  }
+  if constexpr (WARPS == 8) {
+    if (CL > 1) {
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.barrier_wait();  // every CTA has started
+      if (tid < CL) *cluster.map_shared_rank(&of_ctas[rank], tid) = {t, zy};
+      cluster.sync();
+      t = of_ctas[0].t;
+      int owner = 0;
+      for (int r = 0; r < CL; ++r) {
+        if (r) merge(t, of_ctas[r].t);
+        if ((int64_t)z.nvec * r / CL <= jy) owner = r;
+      }
+      zy = of_ctas[owner].zy;
+    }
+  }
+  // ---------------------------------------------------------------- the row
+  const bool empty = t.m == -INFINITY && t.s == 0.f;  // every logit is -inf: no distribution
+  const F2 ls = log_pair(t.s);
+  const float log_s = ls.hi + ls.lo;
+  const float h = empty ? 0.f : log_s - t.u / t.s, H = h < 0.f ? 0.f : h;
+  // log-prob, and its difference to another one, by exact sums
+  const F2 a0 = two_sum(zy, -t.m), a1 = two_sum(a0.hi, -ls.hi);
+  const float logp = empty ? -INFINITY : !y_ok ? __int_as_float(0x7fc00000)
+                                               : zy == -INFINITY ? zy - log_s : a1.hi + (a0.lo + a1.lo - ls.lo);
+  auto from = [&](float other) {  // logp − other
+    if (!(fabsf(logp) < INFINITY)) return logp - other;
+    const F2 b0 = two_sum(a0.hi, -other), b1 = two_sum(b0.hi, -ls.hi);
+    return b1.hi + (a0.lo + b0.lo + b1.lo - ls.lo);
+  };
+  Token k;
+  split(k, a.in.adv[row], a.in.adv_neg != nullptr, a.in.adv_neg ? a.in.adv_neg[row] : 0.f);
+  float policy, kl, slope;
+  objective(a.c, k.gain, k.cost, from(a.in.old_logp[row]), a.in.ref_logp != nullptr,
+            a.in.ref_logp ? -from(a.in.ref_logp[row]) : 0.f, policy, kl, slope);
+  if (rank == 0 && tid == 0) {
+    if (!y_ok) set_err(a.err, TT_ERR_INVALID_ARG);
+    a.logp[row] = logp;
+    a.entropy[row] = H;
+    a.rows[row] = make_float4(w * policy, w * kl, w * H, 0.f);
+  }
+  if (!a.dz) return;
+  const bool none = empty || !y_ok;  // no gradient
+  const float gl = a.c.g * w * slope, gh = a.c.ent != 0.f ? -a.c.g * w * a.c.ent : 0.f;
+  const float b = fmaf(gh, H, gl);
+  const float2 nm = make_float2(-t.m, -t.m), ns = make_float2(-log_s, -log_s), nh = make_float2(-gh, -gh),
+               nb = make_float2(-b, -b);
+  auto grad = [&](float2 x) {
+    float2 lp = __fadd2_rn(__fadd2_rn(x, nm), ns);
+    lp = make_float2(max_nan(lp.x, kFloor), max_nan(lp.y, kFloor));
+    const float2 e = __fmul2_rn(lp, l2);
+    return __fmul2_rn(make_float2(fast_exp2(e.x), fast_exp2(e.y)), __ffma2_rn(nh, lp, nb));
+  };
+  for (int j = lo + tid; j < hi; j += kGroup) {
+    const uint4 u = buf[j];
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (!none) {
+      T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+      for (int i = 0; i < VN / 2; ++i) {
+        const float2 g = grad(Pairs<T>::get(u, i));
+        e[2 * i] = static_cast<T>(g.x);
+        e[2 * i + 1] = static_cast<T>(g.y);
+      }
+    }
+    put(j, r);
+  }
+  if (mine && !none) out[y] = static_cast<T>(grad(make_float2(zy, zy)).x + gl);  // behind this thread's own store
+}
+
+int check_policy(const tt_policy* p, Policy* c) {
+  if (!p) return TT_ERR_INVALID_ARG;
+  const float v[5] = {p->clip_lo, p->clip_hi, p->kl_coef, p->entropy_coef, p->g};
+  for (float f : v)
+    if (!std::isfinite(f)) return TT_ERR_INVALID_ARG;
+  if (p->clip_lo < 0.f || p->clip_lo > 1.f || p->clip_hi < 0.f) return TT_ERR_INVALID_ARG;
+  if (p->dual_clip != 0.f && !(p->dual_clip >= 1.f)) return TT_ERR_INVALID_ARG;
+  *c = {1.f - p->clip_lo, 1.f + p->clip_hi, p->dual_clip == 0.f ? INFINITY : p->dual_clip, p->kl_coef, p->entropy_coef,
+        p->g};
+  return TT_OK;
+}
+
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, int CL, bool dependent, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (CL > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = CL;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {  // may be scheduled while the kernel before it runs; it waits at its first instruction
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  (void)cudaGetLastError();
+  return cuda_status(e);
+}
+
+// Most shared memory of a CTA for its slice: what is left of 227 KB beside the static part.
+constexpr int kSliceMost = 224 * 1024;
+
+template <typename T, int WARPS>
+int launch_rows(const LogitsArgs& a, int CL, cudaStream_t st) {
+  const int nvec = (int)(a.V / Row<T>::VN + 2);
+  const int room = (nvec + CL - 1) / CL + 1;
+  const size_t smem = (size_t)room * 16 * kGroups<WARPS>;
+  if (smem > kSliceMost) return TT_ERR_UNSUPPORTED;
+  if (smem > 48 * 1024 && !tc::smem_attr_set<policy_logits_kernel<T, WARPS>>(kSliceMost)) return TT_ERR_CUDA;
+  return launch(policy_logits_kernel<T, WARPS>, (a.N + kGroups<WARPS> - 1) / kGroups<WARPS> * CL,
+                32 * WARPS * kGroups<WARPS>, smem, CL, false, st, a, CL, room);
+}
+
+template <typename T>
+int launch_logits(const LogitsArgs& a, cudaStream_t st) {
+  const int64_t nvec = a.V / Row<T>::VN + 1, sms = sm_count();
+  if (nvec <= 512 && a.N >= 8 * sms) return launch_rows<T, 1>(a, 1, st);
+  if (nvec <= 1024 && a.N >= 8 * sms) return launch_rows<T, 2>(a, 1, st);
+  if (nvec <= 2048 && a.N >= 4 * sms) return launch_rows<T, 4>(a, 1, st);
+  int CL = 1;
+  while (CL < kCtasMost && (nvec > 2560 * (int64_t)CL || (2 * CL * a.N <= 4 * sms && nvec >= 2 * (int64_t)CL * 256))) CL *= 2;
+  return launch_rows<T, 8>(a, CL, st);
+}
+
+}  // namespace
+}  // namespace tt
+
+using namespace tt;
+
+TT_API size_t tt_policy_loss_workspace_bytes(int64_t N) {
+  return N <= kOneLaunch * kTokens ? 0 : (size_t)((N + kTokens - 1) / kTokens) * sizeof(Sums);
+}
+
+TT_API int tt_policy_loss(const float* logp, const float* entropy, const float* old_logp, const float* adv,
+                          const float* adv_neg, const float* ref_logp, const float* weights, int64_t N,
+                          const tt_policy* policy, float* sums, float* dlogp, float* dentropy, void* ws,
+                          size_t ws_bytes, tt_stream_t stream) {
+  Policy c;
+  const int rc = check_policy(policy, &c);
+  if (rc) return rc;
+  if (N < 0 || N > (int64_t)INT32_MAX || !sums || reinterpret_cast<uintptr_t>(sums) % 4) return TT_ERR_INVALID_ARG;
+  if (N && (!logp || !old_logp || !adv)) return TT_ERR_INVALID_ARG;
+  if (N && c.ent != 0.f && !entropy) return TT_ERR_INVALID_ARG;
+  const void* all[9] = {logp, entropy, old_logp, adv, adv_neg, ref_logp, weights, dlogp, dentropy};
+  uintptr_t bits = 0;
+  for (const void* p : all) bits |= reinterpret_cast<uintptr_t>(p);
+  if (bits % 4) return TT_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (N == 0) return cuda_status(cudaMemsetAsync(sums, 0, 4 * sizeof(float), st));
+  const int64_t blocks = (N + kTokens - 1) / kTokens;
+  LogpArgs a = {logp, entropy, {old_logp, adv, adv_neg, ref_logp, weights}, N, c, sums, dlogp, dentropy, nullptr};
+  auto kernel = bits % 16 ? policy_tokens_kernel<false> : policy_tokens_kernel<true>;
+  if (blocks <= kOneLaunch) {
+    int CL = 1;
+    while (CL < blocks) CL *= 2;
+    return launch(kernel, CL, kTokenThreads, 0, CL, false, st, a);
+  }
+  if (!ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
+  if (ws_bytes < tt_policy_loss_workspace_bytes(N)) return TT_ERR_WORKSPACE;
+  a.parts = static_cast<Sums*>(ws);
+  const int r = launch(kernel, blocks, kTokenThreads, 0, 1, false, st, a);
+  if (r) return r;
+  return launch(policy_sum_kernel<false>, 1, kSumThreads, 0, 1, true, st, (const void*)ws, blocks, c, sums);
+}
+
+TT_API size_t tt_policy_loss_logits_workspace_bytes(int64_t N) { return N < 1 ? 0 : (size_t)N * sizeof(float4); }
+
+TT_API int tt_policy_loss_logits(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* targets,
+                                 const float* old_logp, const float* adv, const float* adv_neg, const float* ref_logp,
+                                 const float* weights, const tt_policy* policy, float* sums, float* logp,
+                                 float* entropy, void* dlogits, void* ws, size_t ws_bytes, int32_t* err,
+                                 tt_stream_t stream) {
+  Policy c;
+  const int rc = check_policy(policy, &c);
+  if (rc) return rc;
+  if (dtype != TT_DT_BF16 && dtype != TT_DT_F16 && dtype != TT_DT_F32) return TT_ERR_INVALID_ARG;
+  const size_t es = dtype == TT_DT_F32 ? 4 : 2;
+  if (N < 0 || V < 1 || ld < V || N > INT32_MAX / 64 || V > INT32_MAX / 2) return TT_ERR_INVALID_ARG;
+  if (!sums || reinterpret_cast<uintptr_t>(sums) % 4) return TT_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (N == 0) return cuda_status(cudaMemsetAsync(sums, 0, 4 * sizeof(float), st));
+  if (!logits || !targets || !old_logp || !adv || !logp || !entropy || !err) return TT_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) % es) return TT_ERR_INVALID_ARG;
+  if (!ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
+  if (ws_bytes < tt_policy_loss_logits_workspace_bytes(N)) return TT_ERR_WORKSPACE;
+  const LogitsArgs a = {logits, dlogits, N, V, ld, targets, {old_logp, adv, adv_neg, ref_logp, weights}, c, logp, entropy,
+                        static_cast<float4*>(ws), err};
+  int r;
+  switch (dtype) {
+    case TT_DT_BF16: r = launch_logits<__nv_bfloat16>(a, st); break;
+    case TT_DT_F16: r = launch_logits<__half>(a, st); break;
+    default: r = launch_logits<float>(a, st);
+  }
+  if (r) return r;
+  return launch(policy_sum_kernel<true>, 1, kSumThreads, 0, 1, true, st, (const void*)ws, N, c, sums);
+}

@@ -23,9 +23,7 @@
 // of 32 + 8 fp32, half of each head turned: 81 us, 0.96. Dropped: the next
 // item loaded while one is turned (274 and 85 us: the registers cost more
 // warps than it hides), two and three items of a thread at once (345, 440).
-#include "common.cuh"
-
-#include <cuda_fp16.h>
+#include "rope.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -35,8 +33,6 @@ namespace tt {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxHalf = 128;  // rot <= 256
-constexpr int kMaxAxes = 4;
 constexpr int kMaxTokens = 32;  // tokens of a block
 
 struct RopeArgs {
@@ -54,40 +50,6 @@ struct RopeArgs {
   uint8_t axis[kMaxHalf];
 };
 
-// VEC consecutive elements of type T as floats.
-template <typename T, int VEC>
-struct Vec {
-  static __device__ __forceinline__ void load(const T* p, float (&f)[VEC]) {
-    if constexpr (VEC == 1) {
-      f[0] = static_cast<float>(*p);
-    } else {
-      static_assert(VEC * sizeof(T) == 16, "16-byte vectors");
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) f[i] = static_cast<float>(e[i]);
-    }
-  }
-  static __device__ __forceinline__ void store(T* p, const float (&f)[VEC]) {
-    if constexpr (VEC == 1) {
-      *p = static_cast<T>(f[0]);
-    } else {
-      uint4 u;
-      T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = static_cast<T>(f[i]);
-      *reinterpret_cast<uint4*>(p) = u;
-    }
-  }
-};
-
-// One pair turned; the order of the roundings is fixed, so that results do not depend on alignment.
-__device__ __forceinline__ void turn_pair(float& x1, float& x2, float c, float s) {
-  const float p = x1, q = x2;
-  x1 = __fmaf_rn(-q, s, __fmul_rn(p, c));
-  x2 = __fmaf_rn(p, s, __fmul_rn(q, c));
-}
-
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ float trig[];
@@ -100,7 +62,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int64_t pos = a.pos[a.axis[f] * a.pos_ld + t0 + t];
     const uint64_t turn = (uint64_t)pos * a.turn[f];
     float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+    trig_of(turn, s, c);
     cosines[i] = c;
     sines[i] = a.inverse ? -s : s;
   }
@@ -121,26 +83,40 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     float u[VEC], v[VEC];
     Vec<T, VEC>::load(x + o1, u);
     Vec<T, VEC>::load(x + o2, v);
-    if (rotated) {
-      const float* c = cosines + t * a.half + VEC * pv;
-      const float* s = sines + t * a.half + VEC * pv;
-      if (!a.adjacent) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) turn_pair(u[j], v[j], c[j], s[j]);
-      } else if constexpr (VEC == 1) {
-        turn_pair(u[0], v[0], c[0], s[0]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC / 2; ++j) {
-          turn_pair(u[2 * j], u[2 * j + 1], c[j], s[j]);
-          turn_pair(v[2 * j], v[2 * j + 1], c[VEC / 2 + j], s[VEC / 2 + j]);
-        }
-      }
-    }
+    if (rotated)
+      turn_vectors<VEC>(u, v, cosines + t * a.half + VEC * pv, sines + t * a.half + VEC * pv, a.adjacent);
     Vec<T, VEC>::store(y + o1, u);
     Vec<T, VEC>::store(y + o2, v);
   }
 }
+
+template <typename T>
+int launch_rope(RopeArgs& a, int rot, cudaStream_t st) {
+  constexpr int VEC = 16 / sizeof(T);
+  bool vec = rot % (2 * VEC) == 0 && a.d % (2 * VEC) == 0;
+  for (int w = 0; w < 2; ++w)
+    if (a.heads[w] > 0)
+      vec = vec && aligned16(a.x[w]) && aligned16(a.y[w]) && a.ld[w] % VEC == 0 && a.ldo[w] % VEC == 0;
+  const int step = vec ? VEC : 1;
+  a.npv = a.d / (2 * step);
+  a.nrot = rot / (2 * step);
+  // tokens of a block: six items to a thread (65,536 tokens of 48 bf16 heads: 3 items 250 us, 4 247, 6 242, 8 243;
+  // 12,669 of 40 fp32 heads: 79, 80, 81, 82), but four blocks to every SM first (64 tokens of 40 heads: one token a
+  // block 3.2 us, four 4.9)
+  const int64_t per_token = (int64_t)(a.heads[0] + a.heads[1]) * a.npv;
+  const int64_t by_items = (6 * kRopeThreads + per_token - 1) / per_token;
+  const int64_t by_blocks = a.N / (4 * (int64_t)sm_count());
+  a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({by_items, by_blocks, kMaxTokens}));
+  const unsigned grid = (unsigned)((a.N + a.tokens - 1) / a.tokens);
+  const size_t smem = 2 * sizeof(float) * a.tokens * a.half;
+  if (vec)
+    rope_kernel<T, VEC><<<grid, kRopeThreads, smem, st>>>(a);
+  else
+    rope_kernel<T, 1><<<grid, kRopeThreads, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+}  // namespace
 
 // |f|/2π modulo 1 in units of 2^-64, negated for f < 0, cut off below 2^-64 (then at position 2^31 the angle is off by
 // 2^-33 of a turn). As Payne and Hanek reduce large arguments: f = mant·2^s with a whole mant of 53 bits, and of the
@@ -172,33 +148,6 @@ uint64_t turns_of(double f) {
   return bits >> 63 ? 0 - t : t;
 }
 
-template <typename T>
-int launch_rope(RopeArgs& a, int rot, cudaStream_t st) {
-  constexpr int VEC = 16 / sizeof(T);
-  bool vec = rot % (2 * VEC) == 0 && a.d % (2 * VEC) == 0;
-  for (int w = 0; w < 2; ++w)
-    if (a.heads[w] > 0)
-      vec = vec && aligned16(a.x[w]) && aligned16(a.y[w]) && a.ld[w] % VEC == 0 && a.ldo[w] % VEC == 0;
-  const int step = vec ? VEC : 1;
-  a.npv = a.d / (2 * step);
-  a.nrot = rot / (2 * step);
-  // tokens of a block: six items to a thread (65,536 tokens of 48 bf16 heads: 3 items 250 us, 4 247, 6 242, 8 243;
-  // 12,669 of 40 fp32 heads: 79, 80, 81, 82), but four blocks to every SM first (64 tokens of 40 heads: one token a
-  // block 3.2 us, four 4.9)
-  const int64_t per_token = (int64_t)(a.heads[0] + a.heads[1]) * a.npv;
-  const int64_t by_items = (6 * kRopeThreads + per_token - 1) / per_token;
-  const int64_t by_blocks = a.N / (4 * (int64_t)sm_count());
-  a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({by_items, by_blocks, kMaxTokens}));
-  const unsigned grid = (unsigned)((a.N + a.tokens - 1) / a.tokens);
-  const size_t smem = 2 * sizeof(float) * a.tokens * a.half;
-  if (vec)
-    rope_kernel<T, VEC><<<grid, kRopeThreads, smem, st>>>(a);
-  else
-    rope_kernel<T, 1><<<grid, kRopeThreads, smem, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
-}
-
-}  // namespace
 }  // namespace tt
 
 using namespace tt;

@@ -327,7 +327,7 @@ def run(s):
                                                    eps=EPS, rot_dim=case["rot"], sections=_sections(case),
                                                    adjacent=case["adjacent"])
             return [dq, dwq, dk, dwk]
-        how = dict(adv_neg=s.get("adv_neg"), ref_logp=s.get("ref_logp"), weights=s["weights"],
+        how = dict(adv_neg=s.get("adv_neg"), ref_logp=s.get("ref_logp"), weights=s.get("weights"),
                    clip=(CLIP_LO, CLIP_HI), dual_clip=DUAL, kl_coef=KL)
         if op == "policy":
             sums, dlogp, dent = tt.policy_loss(s["logp"], s["old_logp"], s["adv"], entropy=s.get("entropy"),

@@ -230,6 +230,49 @@ TT_API int tt_tree_attn_bwd(const void* ws, const tt_bf16* Q, const tt_bf16* K, 
                             tt_bf16* dK, tt_bf16* dV, int64_t N, int Hq, int Hkv, int d, float scale,
                             void* bwd_ws, size_t bwd_ws_bytes, int32_t* err, tt_stream_t stream);
 
+/* ------------------------------------- the next token of running rollouts
+ * Attention of one new token of each of B running rollouts, which is what
+ * samples the rollouts of a tree: query b sees the keys of every segment that
+ * lists it (the prompt, common turns, its own rollout), each in full:
+ *   O_b = Σ_k softmax_k(scale·q_b·k)·v_k,  LSE_b in fp32 (natural log).
+ * The keys of a segment lie once in a pool and are read once for all of its
+ * queries. A segment s is the pool's rows [kv_begin[s], kv_begin[s] +
+ * kv_len[s]), seen by the queries q_begin[s] <= b < q_end[s]; with the
+ * rollouts in DFS order of the tree every segment's are consecutive. Segments
+ * may be given in any order, be empty (no keys or no queries), lie in one
+ * another's rows or be pieces (pages) of one; a key row that two segments of a
+ * query hold counts twice. A query that no key is listed for gets O = 0 and
+ * LSE = −inf.
+ * tt_tree_decode_plan reads the four device arrays int32 [S] and writes how
+ * the step's work is shared out into `plan` (tt_tree_decode_plan_bytes(S)
+ * bytes, 16-byte aligned): once for a step, for all layers' calls. rows: of
+ * the pool; pairs: at least Σ_s (q_end − q_begin) over the segments with keys
+ * (they bound the workspace). A segment outside [0, rows) or [0, B) sets
+ * `err` = TT_ERR_INVALID_ARG, pairs that are too few TT_ERR_WORKSPACE; attention
+ * calls given this plan set the same error and write nothing. In a captured
+ * graph the arrays are read again at every replay.
+ * Limits (TT_ERR_UNSUPPORTED): d 64 or 128, Hq % Hkv = 0, Hq <= 1024, B <= 2^20. */
+TT_API size_t tt_tree_decode_plan_bytes(int32_t S);
+TT_API int tt_tree_decode_plan(const int32_t* kv_begin, const int32_t* kv_len, const int32_t* q_begin,
+                               const int32_t* q_end, int32_t S, int32_t B, int64_t rows, int64_t pairs, int Hq, int Hkv,
+                               int d, void* plan, size_t plan_bytes, int32_t* err, tt_stream_t stream);
+/* plan: of the same S, B, rows, pairs, Hq, Hkv and d (else `err` =
+ * TT_ERR_INVALID_ARG and nothing is written), made on the same device. Q:
+ * [B][Hq][d] with queries q_ld elements apart; K, V: [rows][Hkv][d] with rows
+ * kv_ld elements apart (both strides multiples of 8; K and V may share one
+ * buffer); dtype TT_DT_BF16 or TT_DT_F16. O: [B][Hq][d] contiguous, of type
+ * dtype; LSE: fp32 [Hq][B]. ws: scratch of
+ * tt_tree_decode_attn_workspace_bytes(pairs, Hq, d) bytes, 16-byte aligned;
+ * calls that may overlap (other streams, graphs) need their own. Rows of the
+ * pool outside the listed segments may hold anything. The weights enter the
+ * second product in type dtype; everything else is fp32. Repeated calls agree
+ * bitwise. */
+TT_API size_t tt_tree_decode_attn_workspace_bytes(int64_t pairs, int Hq, int d);
+TT_API int tt_tree_decode_attn(const void* plan, const void* Q, int64_t q_ld, const void* K, const void* V, int64_t kv_ld,
+                               int dtype, int32_t S, int32_t B, int64_t rows, int64_t pairs, int Hq, int Hkv, int d,
+                               float scale, void* O, float* LSE, void* ws, size_t ws_bytes, int32_t* err,
+                               tt_stream_t stream);
+
 /* ------------------------------------------------------ chunk-vs-path mode
  * Path-at-a-time attention (AReaL-DTA, Key Contributions 1–2): a chunk of C
  * query rows sitting at path positions s0 .. s0+C−1 attends to the first

@@ -7,18 +7,19 @@ branch-fraction weighted log-prob loss, and that loss fused with the LM head; be
 front of the attention, and log-prob, entropy and top alternatives per token with their gradients. This package is
 its thin binding.
 """
-from ._native import (KERNEL_CLASSES, TTError, Tree, DTA_DEFAULT_SLOTS, DTA_ORDER_GREEDY, DTA_ORDER_INDEX, DtaPlan,
+from ._native import (KERNEL_CLASSES, TTError, Tree, DTA_DEFAULT_SLOTS, DTA_ORDER_GREEDY, DTA_ORDER_INDEX,
+                      DecodePlan, DtaPlan,
                       check_err, dta_leaf_order, dta_tree_attn, dta_workspace_bytes, exported_symbols, kernel_timing,
                       kernel_timing_read, lib, lmhead_logprob, lmhead_logprob_bwd, lmhead_token_logprob,
                       lmhead_token_logprob_bwd, new_err, policy_loss, policy_loss_logits, qk_norm_rope,
                       qk_norm_rope_bwd, rope, rope_bwd, token_logprob, token_logprob_bwd,
                       tree_attn_bwd, tree_attn_chunk_bwd, tree_attn_chunk_fwd, tree_attn_fwd, tree_build,
-                      tree_partition, tree_schedules, trie_build, weighted_logprob)  # noqa: F401
+                      tree_decode_attn, tree_decode_plan, tree_partition, tree_schedules, trie_build, weighted_logprob)  # noqa: F401
 
-__all__ = ["DTA_DEFAULT_SLOTS", "DTA_ORDER_GREEDY", "DTA_ORDER_INDEX", "DtaPlan", "KERNEL_CLASSES", "TTError", "Tree",
+__all__ = ["DTA_DEFAULT_SLOTS", "DTA_ORDER_GREEDY", "DTA_ORDER_INDEX", "DecodePlan", "DtaPlan", "KERNEL_CLASSES", "TTError", "Tree",
            "check_err", "dta_leaf_order", "dta_tree_attn", "dta_workspace_bytes", "exported_symbols", "kernel_timing",
            "kernel_timing_read", "lib", "lmhead_logprob", "lmhead_logprob_bwd", "lmhead_token_logprob",
            "lmhead_token_logprob_bwd", "new_err", "policy_loss", "policy_loss_logits", "qk_norm_rope",
            "qk_norm_rope_bwd", "rope", "rope_bwd", "token_logprob", "token_logprob_bwd",
            "tree_attn_bwd", "tree_attn_chunk_bwd", "tree_attn_chunk_fwd", "tree_attn_fwd", "tree_build",
-           "tree_partition", "tree_schedules", "trie_build", "weighted_logprob"]
+           "tree_decode_attn", "tree_decode_plan", "tree_partition", "tree_schedules", "trie_build", "weighted_logprob"]

@@ -82,6 +82,11 @@ _SIGS = {
     "tt_qk_norm_rope_bwd_workspace_bytes": (_sz, [_int]),
     "tt_qk_norm_rope_bwd": (_int, [_vp, _i64] * 6 + [_int, _i64, _int, _int, _int, _vp, _vp, _int, _f32, _int, _vp, _i64,
                                                      _int, _vp, _vp, _int, _vp, _vp, _vp, _sz, _vp]),
+    "tt_tree_decode_plan_bytes": (_sz, [_i32]),
+    "tt_tree_decode_plan": (_int, [_vp] * 4 + [_i32, _i32, _i64, _i64, _int, _int, _int, _vp, _sz, _vp, _vp]),
+    "tt_tree_decode_attn_workspace_bytes": (_sz, [_i64, _int, _int]),
+    "tt_tree_decode_attn": (_int, [_vp, _vp, _i64, _vp, _vp, _i64, _int, _i32, _i32, _i64, _i64, _int, _int, _int, _f32,
+                                   _vp, _vp, _vp, _sz, _vp, _vp]),
     "tt_policy_loss_workspace_bytes": (_sz, [_i64]),
     "tt_policy_loss": (_int, [_vp] * 7 + [_i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "tt_policy_loss_logits_workspace_bytes": (_sz, [_i64]),
@@ -568,6 +573,71 @@ def tree_attn_chunk_bwd(q, s0, k_path, v_path, o, lse, dO, dk_acc, dv_acc, lse_l
                                           _p(err), _stream(q.device))
     _check(rc, "tt_tree_attn_chunk_bwd")
     return dq
+
+
+@dataclass
+class DecodePlan:
+    """How the attention of one step of running rollouts is shared out (tt_tree_decode_plan), for all layers' calls."""
+    plan: torch.Tensor
+    S: int
+    B: int
+    rows: int
+    pairs: int
+    hq: int
+    hkv: int
+    d: int
+    ws_bytes: int
+    err: torch.Tensor
+
+    def check(self):
+        check_err(self.err, "tt_tree_decode_plan")
+        return self
+
+
+def tree_decode_plan(segments, B, rows, pairs, hq, hkv, d, err=None, out=None):
+    """The plan of one step of B running rollouts: segments int32 [4, S] on the device, its rows kv_begin, kv_len,
+    q_begin, q_end: the pool's rows [kv_begin, kv_begin + kv_len) are seen by the queries q_begin <= b < q_end. rows: of
+    the pool; pairs: at least the sum of q_end - q_begin. `out`: a plan's tensor to write into (of the same S)."""
+    _need(segments, torch.int32, "segments", 2)
+    if segments.shape[0] != 4:
+        raise ValueError("segments must be [4, S]: kv_begin, kv_len, q_begin, q_end")
+    S, L = segments.shape[1], lib()
+    nbytes = L.tt_tree_decode_plan_bytes(S)
+    plan = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=segments.device) if out is None else out
+    err = new_err(segments.device) if err is None else err
+    at, step = segments.data_ptr(), 4 * S
+    _call("tt_tree_decode_plan", _device_of(segments, plan, err), at, at + step, at + 2 * step, at + 3 * step, S, B, rows,
+          pairs, hq, hkv, d, plan.data_ptr(), plan.numel() * plan.element_size(), err.data_ptr())
+    return DecodePlan(plan, S, B, rows, pairs, hq, hkv, d, L.tt_tree_decode_attn_workspace_bytes(pairs, hq, d), err)
+
+
+def tree_decode_attn(plan: DecodePlan, q, k, v, scale=None, out=None, ws=None, err=None):
+    """O [B,Hq,d], LSE [Hq,B] fp32 of the queries q [B,Hq,d] over the pool's keys and values k, v [rows,Hkv,d] (bf16 or
+    fp16; rows of the pool any stride apart) that the plan lists for them (tt_tree_decode_attn). `ws`: plan.ws_bytes of
+    scratch, one for calls that may overlap."""
+    B, hq, d, q_ld = _rope_rows(q, "q")
+    rows, hkv, dk, k_ld = _rope_rows(k, "k")
+    _, _, _, v_ld = _rope_rows(v, "v")
+    if k.dtype != q.dtype or v.dtype != q.dtype or v.shape != k.shape or k_ld != v_ld or dk != d:
+        raise ValueError("q, k and v must share type and head dimension, k and v shape and strides")
+    if (B, rows, hq, hkv, d) != (plan.B, plan.rows, plan.hq, plan.hkv, plan.d):
+        raise ValueError("the plan is of other sizes")
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if out is None:
+        O = torch.empty_like(q, memory_format=torch.contiguous_format)
+        LSE = torch.empty((hq, B), dtype=torch.float32, device=q.device)
+    else:
+        O, LSE = out
+        if O.dtype != q.dtype or O.shape != q.shape or not O.is_contiguous():
+            raise ValueError("O must be contiguous, with the type and shape of q")
+        _per_row(LSE, torch.float32, "LSE", (hq, B), True)
+    if ws is None:
+        ws = torch.empty(plan.ws_bytes, dtype=torch.uint8, device=q.device)
+    err = plan.err if err is None else err
+    _call("tt_tree_decode_attn", _device_of(q, k, v, plan.plan, O, LSE, ws, err), plan.plan.data_ptr(), q.data_ptr(), q_ld,
+          k.data_ptr(), v.data_ptr(), k_ld, _DTYPES[q.dtype], plan.S, B, rows, plan.pairs, hq, hkv, d, scale, O.data_ptr(),
+          LSE.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr())
+    return O, LSE
 
 
 DTA_ORDER_INDEX, DTA_ORDER_GREEDY = 0, 1

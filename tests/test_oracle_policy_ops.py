@@ -3,6 +3,7 @@ and differences (CPU)."""
 import numpy as np
 import pytest
 
+from oracle import decode as D
 from oracle import norm_rope as NR
 from oracle import policy as P
 from oracle import rope as R
@@ -113,3 +114,27 @@ def test_planted_swap_of_the_clip_sides_is_caught():
     right = P.objective(lr, [0.0], [-2.0])[0][1]
     swapped = 2 * min(0.5, 1.2)  # a cost bounded above instead of below
     assert abs(right - 2 * 0.8) < 1e-14 and abs(swapped - right) > 0.1
+
+
+def test_decode_hand_derived():
+    k = np.array([[[1.0, 0.0]], [[0.0, 1.0]], [[9.0, 9.0]]])
+    v = np.array([[[1.0, 2.0]], [[3.0, 4.0]], [[9.0, 9.0]]])
+    q = np.array([[[np.log(3.0), 0.0]], [[5.0, 5.0]]])
+    O, LSE = D.attention(q, k, v, [(0, 1, 0, 1), (1, 1, 0, 1)], 1.0)  # weights 3/4 and 1/4, over two segments
+    np.testing.assert_allclose(O[0, 0], [0.75 * 1 + 0.25 * 3, 0.75 * 2 + 0.25 * 4], rtol=1e-14)
+    np.testing.assert_allclose(LSE[0, 0], np.log(4.0), rtol=1e-14)
+    assert (O[1] == 0).all() and LSE[0, 1] == -np.inf
+
+
+def test_decode_is_the_last_row_of_causal_attention_over_a_path():
+    from oracle import attention as A
+    from oracle import tree as T
+    rng = np.random.default_rng(5)
+    par, ln = np.array([-1, 0, 0], np.int32), np.array([5, 3, 4], np.int32)
+    tab = T.tables(par, ln)
+    Q, K, V, dO = (rng.standard_normal((12, h, 8)) for h in (4, 2, 2, 4))
+    O, LSE = A.tree_attention_branches(tab, Q, K, V, dO)[:2]
+    last = [7, 11]  # the leaves' last tokens
+    o, lse = D.attention(Q[last], K, V, [(0, 5, 0, 2), (5, 3, 0, 1), (8, 4, 1, 2)], 8 ** -0.5)
+    np.testing.assert_allclose(o, O[last], rtol=1e-12)
+    np.testing.assert_allclose(lse, LSE[:, last], rtol=1e-12)

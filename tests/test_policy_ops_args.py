@@ -132,3 +132,44 @@ def test_binding_refuses_cpu_tensors_and_mixed_arguments():
     from prefix_tree_gb300._native import _policy_of
     with pytest.raises(ValueError):
         _policy_of(0.2, 0.5, 0.0, 0.0, 1.0)
+
+
+def _plan(L, **over):
+    a = dict(kb=fake, kl=fake, qb=fake, qe=fake, S=3, B=4, rows=100, pairs=9, hq=4, hkv=2, d=64, plan=fake, n=big, err=fake,
+             st=None)
+    a.update(over)
+    return L.tt_tree_decode_plan(*a.values())
+
+
+DECODE_SIZES = [(dict(S=-1), BAD), (dict(B=-1), BAD), (dict(rows=-1), BAD), (dict(pairs=-1), BAD), (dict(hq=0), BAD),
+                (dict(hkv=0), BAD), (dict(rows=1 << 31), BAD), (dict(pairs=1 << 31), BAD), (dict(d=96), UNSUPPORTED),
+                (dict(hq=5), UNSUPPORTED), (dict(hq=1026), UNSUPPORTED), (dict(B=1 << 21), UNSUPPORTED),
+                (dict(plan=None), BAD), (dict(plan=ctypes.c_void_p(4104)), BAD), (dict(err=None), BAD)]
+
+
+@pytest.mark.parametrize("over,code", DECODE_SIZES + [(dict(kb=None), BAD), (dict(qe=None), BAD), (dict(n=64), WS)])
+def test_decode_plan_arguments(L, over, code):
+    assert _plan(L, **over) == code
+
+
+def _decode(L, **over):
+    a = dict(plan=fake, q=fake, q_ld=256, k=fake, v=fake, kv_ld=128, dt=0, S=3, B=4, rows=100, pairs=9, hq=4, hkv=2, d=64,
+             scale=0.125, o=fake, lse=fake, ws=fake, n=big, err=fake, st=None)
+    a.update(over)
+    return L.tt_tree_decode_attn(*a.values())
+
+
+@pytest.mark.parametrize("over,code", DECODE_SIZES + [
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(o=None), BAD), (dict(lse=None), BAD),
+    (dict(ws=None), BAD), (dict(n=64), WS), (dict(q=ctypes.c_void_p(4098)), BAD), (dict(k=ctypes.c_void_p(4104)), BAD),
+    (dict(q_ld=255), BAD), (dict(q_ld=260), BAD), (dict(kv_ld=120), BAD), (dict(kv_ld=132), BAD), (dict(dt=2), UNSUPPORTED),
+    (dict(dt=9), BAD), (dict(scale=float("nan")), BAD), (dict(B=0, q=None, o=None, lse=None, ws=None), OK)])
+def test_decode_attn_arguments(L, over, code):
+    assert _decode(L, **over) == code
+
+
+def test_decode_workspaces(L):
+    assert L.tt_tree_decode_plan_bytes(0) > 0 and L.tt_tree_decode_plan_bytes(-1) == 0
+    assert L.tt_tree_decode_plan_bytes(65) == L.tt_tree_decode_plan_bytes(0) + 65 * 32
+    f = L.tt_tree_decode_attn_workspace_bytes
+    assert f(-1, 4, 64) == f(1, 0, 64) == f(1, 4, 80) == 0 < f(0, 4, 64) < f(10, 4, 64) < f(10, 4, 128)

@@ -33,6 +33,12 @@ constexpr int64_t kPlanMagic = 0x7474646563706c31LL;  // "ttdecpl1"
 constexpr int kKeys = 128;       // keys of a block
 constexpr int kMostRows = 128;   // rows of a tile at most
 constexpr int kMostCtas = 1024;
+// A segment with more rows than this is taken by tiles of 128 rows on the tensor cores' asynchronous path, one with
+// fewer by tiles of 16 on the warps' own.
+#ifndef TT_WIDE
+#define TT_WIDE 32
+#endif
+constexpr int kWideFrom = TT_WIDE;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Plan: header, first segment of every CTA, and two int4 for each segment that has keys and queries:
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const PlanArg
         }
       }
       Count c = {0, 0, 0};
-      const int rows = (q1 - q0) * G, tile_rows = 16;
+      const int rows = (q1 - q0) * G, tile_rows = rows > kWideFrom ? kMostRows : 16;
       const int tiles = (rows + tile_rows - 1) / tile_rows;
       if (n > 0 && rows > 0) c = {(int64_t)((n + kKeys - 1) / kKeys) * tiles * a.Hkv, (int64_t)rows * a.Hkv, 1};
       Count total;
@@ -232,25 +238,42 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 constexpr int kWarps = 8;                  // that compute
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kStages = 3;                 // K tiles and V tiles in shared memory, each
+constexpr int kThreads = 32 * (kWarps + 2);  // and one that copies, one that issues the tensor-core products
+constexpr int kKStages = 3, kVStages = 2;  // K and V tiles in shared memory
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256, kColP = 384;  // S and P twice: 128 and 64 columns each
+// The running maximum of a row moves only when it grows by more than this (log2 units): weights stay below 2^8.
+constexpr float kRescale = 8.0f;
 
 template <int D>
 struct Smem {
   static constexpr uint32_t kBox = kKeys * 128;            // 64 columns of a block's keys, 128-byte swizzle
   static constexpr uint32_t kTile = (D / 64) * kBox;
-  static constexpr uint32_t k0 = 0;
-  static constexpr uint32_t v0 = kStages * kTile;
+  static constexpr uint32_t q = 0;                         // the 128 rows of a wide tile, laid out as a K tile
+  static constexpr uint32_t kQLd = D * 2 + 16;             // bytes of a row of Q of a narrow tile
+  static constexpr uint32_t k0 = q + kTile;
+  static constexpr uint32_t v0 = k0 + kKStages * kTile;
   static constexpr uint32_t kPLd = kKeys * 2 + 16;         // bytes of a row of weights: rows fall in different banks
-  static constexpr uint32_t p = v0 + kStages * kTile;
+  static constexpr uint32_t p = v0 + kVStages * kTile;     // narrow tiles: [16] rows of weights
   static constexpr uint32_t max = p + 16 * kPLd;           // [kWarps][16] f32
   static constexpr uint32_t sum = max + kWarps * 16 * 4;   // [kWarps][16] f32
   static constexpr uint32_t row_max = sum + kWarps * 16 * 4;  // [16] f32
-  static constexpr uint32_t bars = row_max + 16 * 4;
-  static constexpr uint32_t abort = bars + 4 * kStages * 8;
-  static constexpr uint32_t total = abort + 16 + 1024;     // + slack for the alignment to 1024 bytes
+  static constexpr uint32_t wide = row_max + 16 * 4;       // wide tiles: [2][128] f32 of the two halves of a row
+  static constexpr uint32_t bars = wide + 2 * 128 * 4;
+  static constexpr uint32_t misc = bars + 32 * 8;
+  static constexpr uint32_t total = misc + 16 + 1024;      // + slack for the alignment to 1024 bytes
 };
-constexpr int K_FULL = 0, V_FULL = kStages, K_EMPTY = 2 * kStages, V_EMPTY = 3 * kStages;
+// Barriers. EMPTY: the eight computing warps and the issuing one; a warp arrives for a block after it has seen the
+// block's FULL, so that it cannot be a phase ahead.
+constexpr int K_FULL = 0, V_FULL = K_FULL + kKStages, K_EMPTY = V_FULL + kVStages, V_EMPTY = K_EMPTY + kKStages,
+              Q_READY = V_EMPTY + kVStages, S_FULL = Q_READY + 1, S_FREE = S_FULL + 2, P_READY = S_FREE + 2,
+              P_FREE = P_READY + 2, FINAL = P_FREE + 2, NBAR = FINAL + 1;
+static_assert(NBAR <= 32, "barriers");
+
+// kind::f16 instruction descriptor for type T.
+template <typename T>
+constexpr uint32_t idesc_of(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16(M, N, a_mn, b_mn) & (std::is_same<T, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -259,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::bars);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::abort);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
   if (const int e = plan_error(a, D)) {
@@ -270,39 +294,112 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t w0 = (int64_t)c * hdr->quota, w1 = min((int64_t)hdr->blocks, w0 + hdr->quota);
   if (w0 >= w1) return;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kKStages; ++i) {
       mbar_init(&bar[K_FULL + i], 1);
-      mbar_init(&bar[V_FULL + i], 1);
-      mbar_init(&bar[K_EMPTY + i], kWarps);
-      mbar_init(&bar[V_EMPTY + i], kWarps);
+      mbar_init(&bar[K_EMPTY + i], kWarps + 1);
     }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&bar[V_FULL + i], 1);
+      mbar_init(&bar[V_EMPTY + i], kWarps + 1);
+    }
+    mbar_init(&bar[Q_READY], 32 * kWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar[S_FULL + i], 1);
+      mbar_init(&bar[S_FREE + i], 32 * kWarps);
+      mbar_init(&bar[P_READY + i], 32 * kWarps);
+      mbar_init(&bar[P_FREE + i], 1);
+    }
+    mbar_init(&bar[FINAL], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (warp == kWarps + 1) tmem_alloc(tmem_slot, kTmemCols);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
   const int n = (int)(w1 - w0), G = a.Hq / a.Hkv;
   const int4* segs = reinterpret_cast<const int4*>(static_cast<const char*>(a.plan) + kPlanSegs);
   Walk at(segs, a.Hkv, G, reinterpret_cast<const int32_t*>(static_cast<const char*>(a.plan) + kPlanCtas)[c], (int)w0);
 
   if (warp == kWarps) {
-    // ------------------------------------------------------------ producer: lane 0 the K tiles, lane 1 the V tiles
+    // ------------------------------------------------------------ copies: lane 0 the K tiles, lane 1 the V tiles
     if (lane < 2) {
       const CUtensorMap* map = lane ? &tmV : &tmK;
-      const int full = lane ? V_FULL : K_FULL, empty = lane ? V_EMPTY : K_EMPTY;
+      const int full = lane ? V_FULL : K_FULL, empty = lane ? V_EMPTY : K_EMPTY, stages = lane ? kVStages : kKStages;
       uint8_t* dst = sm + (lane ? L::v0 : L::k0);
       prefetch_tmap(map);
-      int i = 0;
+      int i = 0, st = 0, phase = 0;
       for (; i < n; ++i) {
-        const int st = i % kStages;
-        if (i >= kStages && !mbar_wait(&bar[empty + st], (i / kStages - 1) & 1, abort_flag, 50 + lane)) break;
+        if (i >= stages && !mbar_wait(&bar[empty + st], phase ^ 1, abort_flag, 50 + lane)) break;
         mbar_expect_tx(&bar[full + st], L::kTile);
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)
           tma_load_2d(dst + st * L::kTile + x * L::kBox, map, &bar[full + st], at.h * D + x * 64, at.kv + at.blk * kKeys);
         at.next(i + 1 < n);
+        if (++st == stages) st = 0, phase ^= 1;
       }
       // every copy issued has landed before the CTA may leave
-      for (int j = i - 1; j >= 0 && j >= i - kStages; --j) mbar_drain(&bar[full + j % kStages], (j / kStages) & 1, abort_flag);
+      for (int j = i - 1; j >= 0 && j >= i - stages; --j) mbar_drain(&bar[full + j % stages], (j / stages) & 1, abort_flag);
+    }
+  } else if (warp == kWarps + 1) {
+    // ------------------------------------------------------------ tensor-core products of the wide tiles
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_of<T>(128, 128, 0, 0), idPV = idesc_of<T>(128, D, 0, 1);
+      const uint64_t dq = smem_desc(smem_u32(sm + L::q), 16, 1024);
+      int j = 0, tiles = 0;              // wide blocks and wide tiles so far
+      int pv_st = -1, pv_phase = 0;      // the block whose second product is still to be issued: its V stage,
+      bool pv_first = false;             // and whether it is its tile's first
+      bool ok = true;
+      auto issue_pv = [&]() -> bool {    // of wide block j − 1
+        const int bb = (j - 1) & 1;
+        if (!mbar_wait(&bar[P_READY + bb], ((j - 1) >> 1) & 1, abort_flag, 54)) return false;
+        if (!mbar_wait(&bar[V_FULL + pv_st], pv_phase, abort_flag, 55)) return false;
+        tc_fence_after();
+        const uint64_t dv = smem_desc(smem_u32(sm + L::v0 + pv_st * L::kTile), L::kBox, 1024);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          umma_ts(tbase + kColO, tbase + kColP + bb * 64 + k * 8, desc_at(dv, k * 2048), idPV, !pv_first || k > 0);
+        umma_commit(&bar[P_FREE + bb]);
+        umma_commit(&bar[V_EMPTY + pv_st]);
+        pv_st = -1;
+        return true;
+      };
+      int kst = 0, kphase = 0, vst = 0, vphase = 0;
+      for (int i = 0; i < n; ++i) {
+        if (!mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 56)) { ok = false; break; }
+        if (at.tile_rows == kMostRows) {
+          const int bb = j & 1;
+          const bool first = i == 0 || at.blk == 0;
+          if (first && !mbar_wait(&bar[Q_READY], tiles++ & 1, abort_flag, 57)) { ok = false; break; }
+          if (j >= 2 && !mbar_wait(&bar[S_FREE + bb], ((j - 2) >> 1) & 1, abort_flag, 58)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t dk = smem_desc(smem_u32(sm + L::k0 + kst * L::kTile), 16, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * L::kBox + (k & 3) * 32;
+            umma_ss(tbase + kColS + bb * 128, desc_at(dq, off), desc_at(dk, off), idS, k > 0);
+          }
+          umma_commit(&bar[S_FULL + bb]);
+          umma_commit(&bar[K_EMPTY + kst]);
+          if (pv_st >= 0 && !issue_pv()) { ok = false; break; }
+          pv_st = vst, pv_phase = vphase, pv_first = first;
+          ++j;
+          // a tile's last block is finished here: the computing warps wait for it before they turn to the next tile
+          if ((i + 1 == n || at.blk + 1 == at.nb) && !issue_pv()) { ok = false; break; }
+        } else {  // the computing warps' alone
+          mbar_arrive(&bar[K_EMPTY + kst]);
+          if (!mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 59)) { ok = false; break; }
+          mbar_arrive(&bar[V_EMPTY + vst]);
+        }
+        at.next(i + 1 < n);
+        if (++kst == kKStages) kst = 0, kphase ^= 1;
+        if (++vst == kVStages) vst = 0, vphase ^= 1;
+      }
+      // completes after every product of this CTA, also after an abort: shared and tensor memory outlive them
+      (void)ok;
+      umma_commit(&bar[FINAL]);
+      mbar_drain(&bar[FINAL], 0, abort_flag);
     }
   } else {
     // ------------------------------------------------------------ 16 rows against the blocks, all warps on every block
@@ -310,26 +407,172 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kOut = kCols / 8;
     const int r0 = lane >> 2, cc = (lane & 3) * 2;
     const int mi = lane >> 3, mr = lane & 7;
-    uint32_t qa[D / 16][4];
     float o[kOut][4], m[2], l[2];
     float* smax = reinterpret_cast<float*>(sm + L::max);
     float* ssum = reinterpret_cast<float*>(sm + L::sum);
     float* srow = reinterpret_cast<float*>(sm + L::row_max);
     const uint32_t pbase = smem_u32(sm + L::p);
+    const uint32_t qbase = smem_u32(sm + L::q) + ((mi & 1) * 8 + mr) * L::kQLd + (mi >> 1) * 16;
+    float* half_of_row = reinterpret_cast<float*>(sm + L::wide);
+    int j = 0;                            // wide blocks so far
+    int kst = 0, kphase = 0, vst = 0, vphase = 0;
     for (int i = 0; i < n; ++i) {
-      const int st = i % kStages;
-      const uint32_t par = (i / kStages) & 1;
       const int tile_n = min(at.tile_rows, at.rows - at.tile * at.tile_rows);  // rows of this tile
-      if (i == 0 || at.blk == 0) {
+      const bool first = i == 0 || at.blk == 0, last = i + 1 == n || at.blk + 1 == at.nb;
+      const int valid = at.len - at.blk * kKeys;  // keys of the segment in this block, possibly more than there are
+      // rows behind the segment's end are another segment's, or not yet written: a weight of 0 times what lies there must
+      // be 0
+      auto clear_behind = [&]() {
+        if (valid >= kKeys) return;
+        for (int e = (int)threadIdx.x; e < (kKeys - valid) * (D / 8); e += 32 * kWarps) {
+          const int key = valid + e / (D / 8), u = e % (D / 8);
+          *reinterpret_cast<uint4*>(sm + L::v0 + vst * L::kTile + (u >> 3) * L::kBox + key * 128 + ((u & 7) << 4)) =
+              make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the products, and the next copy
+      };
+      if (at.tile_rows == kMostRows) {
+        // ---------------------------------------------------------- 128 rows: a thread one row and half of the keys
+        const int wq = warp & 3, hf = warp >> 2, r = wq * 32 + lane, bb = j & 1;
+        const uint32_t lanes = tbase + ((uint32_t)(wq * 32) << 16);
+        if (first) {
+          // the rows of Q into shared memory, in the swizzled layout that the products read
+          for (int e = (int)threadIdx.x; e < kMostRows * (D / 8); e += 32 * kWarps) {
+            const int row = e / (D / 8), u = e % (D / 8), rr = at.tile * kMostRows + row;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (row < tile_n)
+              x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(at.q0 + rr / G) * a.q_ld +
+                                                  (int64_t)(at.h * G + rr % G) * D + u * 8);
+            *reinterpret_cast<uint4*>(sm + L::q + (u >> 3) * L::kBox + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = x;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(&bar[Q_READY]);
+          m[0] = -INFINITY;
+          l[0] = 0.f;
+        }
+        mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 60);
+        mbar_wait(&bar[S_FULL + bb], (j >> 1) & 1, abort_flag, 61);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[K_EMPTY + kst]);
+        tc_fence_after();
+        uint32_t x[2][32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_ld32(lanes + kColS + bb * 128 + 64 * hf + q * 32, x[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_pin(x[q]);
+        tc_fence_before();
+        mbar_arrive(&bar[S_FREE + bb]);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const int seen = valid - 64 * hf;  // keys of this half that are there
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int col = q * 32 + 2 * e;
+            const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1])),
+                                        make_float2(a.scale_log2, a.scale_log2));
+            const float y0 = col < seen ? y.x : -INFINITY, y1 = col + 1 < seen ? y.y : -INFINITY;
+            x[q][2 * e] = __float_as_uint(y0);
+            x[q][2 * e + 1] = __float_as_uint(y1);
+            mx[e & 3] = fmax3f(mx[e & 3], y0, y1);
+          }
+        const float pm = fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+        half_of_row[hf * 128 + r] = pm;
+        named_barrier(2 + wq, 64);
+        const float top = fmaxf(pm, half_of_row[(hf ^ 1) * 128 + r]);
+        named_barrier(2 + wq, 64);  // (read before the next block writes)
+        bool moved = false;
+        float f = 1.f;
+        if (top > m[0] + kRescale) {
+          f = fast_exp2(m[0] - top);  // 0 at the tile's first keys
+          l[0] *= f;
+          moved = !first;
+          m[0] = top;
+        }
+        const float mu = m[0] == -INFINITY ? 0.f : m[0];
+        const float2 nm = make_float2(-mu, -mu);
+        float2 rs = make_float2(0.f, 0.f);
+        uint32_t pk[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 d = __fadd2_rn(make_float2(__uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1])), nm);
+            const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+            rs = __fadd2_rn(rs, w);
+            pk[q * 16 + e] = pack2<T>(w.x, w.y);
+          }
+        l[0] += rs.x + rs.y;
+        if (j >= 2) mbar_wait(&bar[P_FREE + bb], ((j - 2) >> 1) & 1, abort_flag, 62);
+        if (__any_sync(~0u, moved)) {
+          mbar_wait(&bar[P_FREE + (bb ^ 1)], ((j - 1) >> 1) & 1, abort_flag, 63);  // O of the block before
+          tc_fence_after();
+          const float g = moved ? f : 1.f;
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) {
+            const uint32_t col = lanes + kColO + (D / 2) * hf + q * 32;
+            uint32_t y[32];
+            tmem_ld32(col, y);
+            tmem_ld_wait();
+            tmem_pin(y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * g);
+            tmem_st32(col, y);
+          }
+        }
+        tmem_st32(lanes + kColP + bb * 64 + 32 * hf, pk);
+        tmem_st_wait();
+        mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 64);
+        clear_behind();
+        tc_fence_before();
+        mbar_arrive(&bar[P_READY + bb]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[V_EMPTY + vst]);
+        if (last) {
+          // the tile's part: the row's sums from tensor memory
+          half_of_row[hf * 128 + r] = l[0];
+          named_barrier(2 + wq, 64);
+          const float sum = l[0] + half_of_row[(hf ^ 1) * 128 + r];
+          named_barrier(2 + wq, 64);
+          mbar_wait(&bar[P_FREE + bb], (j >> 1) & 1, abort_flag, 65);
+          tc_fence_after();
+          const int64_t row = at.part_row(c) + r;
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t y[32];
+            tmem_ld32(lanes + kColO + (D / 2) * hf + q * 32, y);
+            tmem_ld_wait();
+            tmem_pin(y);
+            if (r < tile_n) {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + (D / 2) * hf + q * 32);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]),
+                                     __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
+            }
+          }
+          tc_fence_before();
+          if (hf == 0 && r < tile_n) a.part_ml[row] = make_float2(m[0], sum);
+        }
+        ++j;
+        at.next(i + 1 < n);
+        if (++kst == kKStages) kst = 0, kphase ^= 1;
+        if (++vst == kVStages) vst = 0, vphase ^= 1;
+        continue;
+      }
+      if (first) {
+        // the rows of Q into shared memory (where wide tiles keep theirs)
+        for (int e = (int)threadIdx.x; e < 16 * (D / 8); e += 32 * kWarps) {
+          const int row = e / (D / 8), u = e % (D / 8), rr = at.tile * 16 + row;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (row < tile_n)
+            x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(at.q0 + rr / G) * a.q_ld +
+                                                (int64_t)(at.h * G + rr % G) * D + u * 8);
+          *reinterpret_cast<uint4*>(sm + L::q + row * L::kQLd + u * 16) = x;
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int r = r0 + 8 * half, rr = at.tile * at.tile_rows + r;
-          const T* q = static_cast<const T*>(a.q) + (int64_t)(at.q0 + rr / G) * a.q_ld + (int64_t)(at.h * G + rr % G) * D + cc;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            qa[k][half] = r < tile_n ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
-            qa[k][half + 2] = r < tile_n ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
-          }
           m[half] = -INFINITY;
           l[half] = 0.f;
         }
@@ -337,25 +580,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < kOut; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+        named_barrier(1, 32 * kWarps);
       }
       // S of this warp's 16 keys
       float s[2][4] = {};
-      mbar_wait(&bar[K_FULL + st], par, abort_flag, 52);
+      mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 52);
       {
-        const uint32_t kt = smem_u32(sm + L::k0 + st * L::kTile);
+        const uint32_t kt = smem_u32(sm + L::k0 + kst * L::kTile);
         const int key = warp * 16 + (mi >> 1) * 8 + mr;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int unit = (k & 3) * 2 + (mi & 1);  // 16 bytes of the row within its box
-          uint32_t b[4];
+          uint32_t b[4], qa[4];
+          ldsm4(qa, qbase + k * 32);
           ldsm4(b, kt + (k >> 2) * L::kBox + key * 128 + ((unit ^ (key & 7)) << 4));
-          mma16816<T>(s[0], qa[k], b[0], b[1]);
-          mma16816<T>(s[1], qa[k], b[2], b[3]);
+          mma16816<T>(s[0], qa, b[0], b[1]);
+          mma16816<T>(s[1], qa, b[2], b[3]);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[K_EMPTY + st]);
-      const int valid = at.len - at.blk * kKeys;  // keys of the segment in this block, possibly more than there are
+      if (lane == 0) mbar_arrive(&bar[K_EMPTY + kst]);
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -399,20 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < kOut; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][e] *= f[e >> 1];
-      mbar_wait(&bar[V_FULL + st], par, abort_flag, 53);
-      if (valid < kKeys) {
-        // rows behind the segment's end are another segment's, or not yet written: a weight of 0 times what lies there
-        // must be 0
-        for (int e = (int)threadIdx.x; e < (kKeys - valid) * (D / 8); e += 32 * kWarps) {
-          const int key = valid + e / (D / 8), u = e % (D / 8);
-          *reinterpret_cast<uint4*>(sm + L::v0 + st * L::kTile + (u >> 3) * L::kBox + key * 128 + ((u & 7) << 4)) =
-              make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
-      }
+      mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 53);
+      clear_behind();
       named_barrier(1, 32 * kWarps);  // the weights are there
       {
-        const uint32_t vt = smem_u32(sm + L::v0 + st * L::kTile);
+        const uint32_t vt = smem_u32(sm + L::v0 + vst * L::kTile);
         const uint32_t pt = pbase + ((mi & 1) * 8 + mr) * L::kPLd + (mi >> 1) * 16;
         if constexpr (kOut == 2) {
 #pragma unroll
@@ -438,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[V_EMPTY + st]);
-      if (i + 1 == n || at.blk + 1 == at.nb) {
+      if (lane == 0) mbar_arrive(&bar[V_EMPTY + vst]);
+      if (last) {
         // the tile's part: every warp its columns of the sums, the first 16 threads maxima and sums of weights
         const int64_t row = at.part_row(c);
 #pragma unroll
@@ -465,9 +700,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       at.next(i + 1 < n);
+      if (++kst == kKStages) kst = 0, kphase ^= 1;
+      if (++vst == kVStages) vst = 0, vphase ^= 1;
     }
   }
+  tc_fence_before();
   __syncthreads();
+  if (warp == kWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
   if (*abort_flag && threadIdx.x == 0) set_err(a.err, TT_ERR_TIMEOUT);
 }
 

@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "logit_rows.cuh"
 
@@ -85,12 +86,9 @@ struct Policy {
 struct Inputs {  // per token, fp32 [N] each
   const float *old_logp, *adv, *adv_neg, *ref_logp, *weights;
 };
-struct Token {
-  float old_logp, gain, cost, ref_logp, w;
-};
-__device__ __forceinline__ void split(Token& t, float adv, bool two_sided, float adv_neg) {
-  t.gain = two_sided || !(adv < 0.f) ? adv : 0.f;
-  t.cost = two_sided ? adv_neg : adv < 0.f ? -adv : 0.f;
+__device__ __forceinline__ void split(float adv, bool two_sided, float adv_neg, float& gain, float& cost) {
+  gain = two_sided || !(adv < 0.f) ? adv : 0.f;
+  cost = two_sided ? adv_neg : adv < 0.f ? -adv : 0.f;
 }
 
 // e^x − 1 − x
@@ -199,10 +197,9 @@ __global__ void __launch_bounds__(kTokenThreads) policy_tokens_kernel(const Logp
     const float wt = u < a.N ? (a.in.weights ? w[i] : 1.f) : 0.f;
     dl[i] = dh[i] = 0.f;
     if (wt == 0.f) continue;  // a masked token, whatever its other inputs hold
-    Token k;
-    split(k, adv[i], a.in.adv_neg != nullptr, neg[i]);
-    float policy, kl, slope;
-    objective(a.c, k.gain, k.cost, lp[i] - old[i], a.in.ref_logp != nullptr, a.in.ref_logp ? ref[i] - lp[i] : 0.f,
+    float gain, cost, policy, kl, slope;
+    split(adv[i], a.in.adv_neg != nullptr, neg[i], gain, cost);
+    objective(a.c, gain, cost, lp[i] - old[i], a.in.ref_logp != nullptr, a.in.ref_logp ? ref[i] - lp[i] : 0.f,
               policy, kl, slope);
     add(s.v[0], wt * policy);
     add(s.v[1], wt * kl);
@@ -238,13 +235,21 @@ __global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const void* par
   __shared__ Sums room[kSumThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Sums s = {};
-  for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
-    if (ROWS) {
-      const float4 f = static_cast<const float4*>(parts)[i];
-      add(s.v[0], f.x);
-      add(s.v[1], f.y);
-      add(s.v[2], f.z);
-    } else {
+  constexpr int kLoads = 8;  // of a thread under way together
+  for (int64_t i = threadIdx.x; ROWS && i < n; i += kLoads * kSumThreads) {
+    float4 f[kLoads];
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      f[q] = i + q * kSumThreads < n ? static_cast<const float4*>(parts)[i + q * kSumThreads] : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      add(s.v[0], f[q].x);
+      add(s.v[1], f[q].y);
+      add(s.v[2], f[q].z);
+    }
+  }
+  if (!ROWS) {
+    for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
       const Sums p = static_cast<const Sums*>(parts)[i];
 #pragma unroll
       for (int q = 0; q < 3; ++q) s.v[q] = add(s.v[q], p.v[q]);
@@ -280,10 +285,18 @@ __device__ __forceinline__ F2 log_pair(float s) {
   return l;
 }
 
-// What the CTAs of a row tell each other: (m, s, u) of the slice and the target's logit, where it lies there.
-struct Slice {
-  Stat t;
-  float zy;
+// Stores v at the same place of CTA `rank` of the cluster; its barrier counts the bytes.
+__device__ __forceinline__ void send(float4* place, float4 v, uint64_t* bar, uint32_t rank) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   tc::dsmem_addr(smem_u32(place), rank)),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(tc::dsmem_addr(smem_u32(bar), rank))
+               : "memory");
+}
+// What every thread needs of its row.
+struct RowOf {
+  float m, log_s;
+  float gl, slope_t, at0;  // dlogp; and −dlogp − dH·(log p + H) as slope_t·(log2 p) + at0
+  int none, wide;          // no gradient; every difference to the maximum has to be bounded (see fold)
 };
 
 constexpr int kBatch = 4;   // vectors of a thread at once: one rescaling for all of them
@@ -292,133 +305,53 @@ constexpr int kCtasMost = 8;
 template <int WARPS>
 constexpr int kGroups = WARPS == 1 ? 4 : 1;  // groups of a block: each takes rows of its own
 
-// A row is taken by a group of WARPS warps of each of the CL CTAs of a cluster (WARPS < 8: CL = 1). `room`: vectors of a
-// group's slice in shared memory; a thread copies, sums and turns its own vectors, so that the copies need no barrier.
-template <typename T, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_kernel(const LogitsArgs a, int CL, int room) {
-  constexpr int VN = Row<T>::VN, kGroup = 32 * WARPS;
-  extern __shared__ __align__(16) uint4 slices[];
-  __shared__ Slice part[WARPS * kGroups<WARPS>];
-  __shared__ Slice of_ctas[kCtasMost];
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, group = threadIdx.x / kGroup;
-  const int tid = threadIdx.x % kGroup;
-  const int64_t row = kGroups<WARPS> > 1 ? (int64_t)blockIdx.x * kGroups<WARPS> + group : (int64_t)(blockIdx.x / CL);
-  const int rank = WARPS == 8 ? (int)(blockIdx.x % CL) : 0;
-  if (row >= a.N) return;  // (groups of one warp only)
-  if (WARPS == 8 && CL > 1) cg::this_cluster().barrier_arrive();  // waited for before the CTAs write to one another
-  const float w = a.in.weights ? a.in.weights[row] : 1.f;
-  const Row<T> z(static_cast<const T*>(a.z) + row * a.ld, a.V);
-  T* out = static_cast<T*>(a.dz) + row * a.ld;
-  const int lo = (int)((int64_t)z.nvec * rank / CL), hi = (int)((int64_t)z.nvec * (rank + 1) / CL);
-  const bool same = a.dz && (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(z.p) & 15);
-  const int wlo = z.whole_lo(), whi = z.whole_hi();
-  auto put = [&](int j, const uint4& u) {
-    if (same && j >= wlo && j < whi) {
-      *reinterpret_cast<uint4*>(out + z.first(j)) = u;
-    } else {
-      const int e = z.first(j);
-      const T* t = reinterpret_cast<const T*>(&u);
+// (m, s, u) of all lanes, the same bits in every one.
+__device__ __forceinline__ Stat sum_stats(Stat t) {
+  float M = t.m;
 #pragma unroll
-      for (int i = 0; i < VN; ++i)
-        if (e + i >= 0 && e + i < z.V) out[e + i] = t[i];
-    }
-  };
-  if (w == 0.f) {  // a masked row: its logits are not read
-    if (a.dz)
-      for (int j = lo + tid; j < hi; j += kGroup) put(j, make_uint4(0, 0, 0, 0));
-    if (rank == 0 && tid == 0) {
-      a.logp[row] = a.entropy[row] = 0.f;
-      a.rows[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    if (WARPS == 8 && CL > 1) cg::this_cluster().barrier_wait();
-    return;
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+  rescale(t, M);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    t.s += __shfl_xor_sync(kAll, t.s, o);
+    t.u += __shfl_xor_sync(kAll, t.u, o);
   }
-  uint4* buf = slices + group * room - lo;  // buf[j]: vector j
-  const int y = a.y[row];
-  const bool y_ok = y >= 0 && y < z.V;
-  auto fetch = [&](int at) {
-#pragma unroll
-    for (int v = 0; v < kBatch; ++v) {
-      const int j = at + v * kGroup;
-      if (j >= wlo && j < min(hi, whi))
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf + j)), "l"(z.p + z.first(j))
-                     : "memory");
-      else if (j < hi)
-        buf[j] = z.load(j);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int b = 0; b < kAhead; ++b) fetch(lo + tid + b * kBatch * kGroup);
-  Stat t = {-INFINITY, 0.f, 0.f};
-  const float2 l2 = make_float2(kLog2e, kLog2e);
-  uint4 masked;
-#pragma unroll
-  for (int i = 0; i < VN; ++i) reinterpret_cast<T*>(&masked)[i] = static_cast<T>(-INFINITY);
-  for (int j = lo + tid; j < hi; j += kBatch * kGroup) {
-    fetch(j + kAhead * kBatch * kGroup);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-    uint4 u[kBatch];
-#pragma unroll
-    for (int v = 0; v < kBatch; ++v) u[v] = j + v * kGroup < hi ? buf[j + v * kGroup] : masked;
-    static_assert(kBatch == 4, "four vectors");
-    rescale(t, fmaxf(t.m, Pairs<T>::max(u[0], u[1], u[2], u[3])));
-    const float mb = t.m == -INFINITY ? 0.f : t.m;
-    const float2 nm = make_float2(-mb, -mb);
-    float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int v = 0; v < kBatch; ++v) fold<T, false>(s, q, u[v], nm, l2);
-    t.s += s.x + s.y;
-    t.u += q.x + q.y;
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  t = join_warp(t, lane);
-  if (!plain_way_holds<T>(t.m)) {  // (see fold: extreme rows, again with every difference bounded)
-    t = {-INFINITY, 0.f, 0.f};
-    for (int j = lo + tid; j < hi; j += kGroup) {
-      const uint4 u = buf[j];
-      rescale(t, fmaxf(t.m, Pairs<T>::max(u)));
-      const float mb = t.m == -INFINITY ? 0.f : t.m;
-      float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
-      fold<T, true>(s, q, u, make_float2(-mb, -mb), l2);
-      t.s += s.x + s.y;
-      t.u += q.x + q.y;
-    }
-    t = join_warp(t, lane);
-  }
-  // the target's logit, by the thread that holds it
-  const int jy = y_ok ? (y + z.shift) / VN : -1;
-  const bool mine = jy >= lo && jy < hi && (jy - lo) % kGroup == tid;
-  float zy = -INFINITY;
-  if (mine) zy = static_cast<float>(reinterpret_cast<const T*>(buf + jy)[(y + z.shift) % VN]);
-  if constexpr (WARPS == 1) {
-    zy = __shfl_sync(kAll, zy, jy >= lo && jy < hi ? (jy - lo) % kGroup : 0);
-  } else {
-    Slice* p = part + group * WARPS;
-    zy = __shfl_sync(kAll, zy, jy >= lo && jy < hi ? (jy - lo) % 32 : 0);  // (its lane; the other warps' are unused)
-    if (lane == 0) p[warp] = {t, zy};
-    __syncthreads();
-    t = p[0].t;
-#pragma unroll
-    for (int q = 1; q < WARPS; ++q) merge(t, p[q].t);
-    zy = p[jy >= lo && jy < hi ? (jy - lo) % kGroup / 32 : 0].zy;
-  }
-  if constexpr (WARPS == 8) {
-    if (CL > 1) {
-      cg::cluster_group cluster = cg::this_cluster();
-      cluster.barrier_wait();  // every CTA has started
-      if (tid < CL) *cluster.map_shared_rank(&of_ctas[rank], tid) = {t, zy};
-      cluster.sync();
-      t = of_ctas[0].t;
-      int owner = 0;
-      for (int r = 0; r < CL; ++r) {
-        if (r) merge(t, of_ctas[r].t);
-        if ((int64_t)z.nvec * r / CL <= jy) owner = r;
-      }
-      zy = of_ctas[owner].zy;
-    }
-  }
-  // ---------------------------------------------------------------- the row
+  return t;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float2 g);
+template <>
+__device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float2 g) { return pack_bf16(g.x, g.y); }
+template <>
+__device__ __forceinline__ uint32_t pack_pair<__half>(float2 g) {
+  const __half2 h = __floats2half2_rn(g.x, g.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_twice_down(float x);  // x rounded towards -inf, twice
+template <>
+__device__ __forceinline__ uint32_t pack_twice_down<__nv_bfloat16>(float x) {
+  return 0x10001u * __bfloat16_as_ushort(__float2bfloat16_rd(x));
+}
+template <>
+__device__ __forceinline__ uint32_t pack_twice_down<__half>(float x) {
+  return 0x10001u * __half_as_ushort(__float2half_rd(x));
+}
+
+// A row's inputs as they are loaded, before its sums: nothing waits for them there.
+struct RowInputs {
+  float old_logp, adv, adv_neg, ref_logp, w;
+};
+__device__ __forceinline__ RowInputs inputs_of(const Inputs& in, int64_t row, float w) {
+  return {in.old_logp[row], in.adv[row], in.adv_neg ? in.adv_neg[row] : 0.f, in.ref_logp ? in.ref_logp[row] : 0.f, w};
+}
+
+// A row's terms, log-prob and entropy written (by `writer`), and what its gradient needs.
+template <typename T>
+__device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const RowInputs& in, const Stat& t, float zy, bool y_ok,
+                                        bool writer) {
+  const float w = in.w;
   const bool empty = t.m == -INFINITY && t.s == 0.f;  // every logit is -inf: no distribution
   const F2 ls = log_pair(t.s);
   const float log_s = ls.hi + ls.lo;
@@ -432,44 +365,240 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_ker
     const F2 b0 = two_sum(a0.hi, -other), b1 = two_sum(b0.hi, -ls.hi);
     return b1.hi + (a0.lo + b0.lo + b1.lo - ls.lo);
   };
-  Token k;
-  split(k, a.in.adv[row], a.in.adv_neg != nullptr, a.in.adv_neg ? a.in.adv_neg[row] : 0.f);
   float policy, kl, slope;
-  objective(a.c, k.gain, k.cost, from(a.in.old_logp[row]), a.in.ref_logp != nullptr,
-            a.in.ref_logp ? -from(a.in.ref_logp[row]) : 0.f, policy, kl, slope);
-  if (rank == 0 && tid == 0) {
+  float gain, cost;
+  split(in.adv, a.in.adv_neg != nullptr, in.adv_neg, gain, cost);
+  objective(a.c, gain, cost, from(in.old_logp), a.in.ref_logp != nullptr, a.in.ref_logp ? -from(in.ref_logp) : 0.f, policy,
+            kl, slope);
+  if (writer) {
     if (!y_ok) set_err(a.err, TT_ERR_INVALID_ARG);
     a.logp[row] = logp;
     a.entropy[row] = H;
     a.rows[row] = make_float4(w * policy, w * kl, w * H, 0.f);
   }
-  if (!a.dz) return;
-  const bool none = empty || !y_ok;  // no gradient
   const float gl = a.c.g * w * slope, gh = a.c.ent != 0.f ? -a.c.g * w * a.c.ent : 0.f;
-  const float b = fmaf(gh, H, gl);
-  const float2 nm = make_float2(-t.m, -t.m), ns = make_float2(-log_s, -log_s), nh = make_float2(-gh, -gh),
-               nb = make_float2(-b, -b);
-  auto grad = [&](float2 x) {
-    float2 lp = __fadd2_rn(__fadd2_rn(x, nm), ns);
-    lp = make_float2(max_nan(lp.x, kFloor), max_nan(lp.y, kFloor));
-    const float2 e = __fmul2_rn(lp, l2);
-    return __fmul2_rn(make_float2(fast_exp2(e.x), fast_exp2(e.y)), __ffma2_rn(nh, lp, nb));
-  };
-  for (int j = lo + tid; j < hi; j += kGroup) {
-    const uint4 u = buf[j];
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (!none) {
-      T* e = reinterpret_cast<T*>(&r);
+  constexpr float kLn2 = 0.6931471805599453f;
+  return {t.m, log_s, gl, -gh * kLn2, -fmaf(gh, H, gl), empty || !y_ok, !plain_way_holds<T>(t.m)};
+}
+
+// dz of vectors of a row.
+template <typename T>
+struct Turn {
+  float2 nm, nl, sl, b0;
+  uint32_t low;
+  __device__ __forceinline__ Turn(const RowOf& r)
+      : nm(make_float2(-r.m, -r.m)), nl(make_float2(-r.log_s * kLog2e, -r.log_s * kLog2e)),
+        sl(make_float2(r.slope_t, r.slope_t)), b0(make_float2(r.at0, r.at0)), low(0) {
+    // so far below the maximum that p is 0, and at least a step of the type below it
+    if constexpr (sizeof(T) == 2) low = pack_twice_down<T>(r.m - fmaxf(130.f, fabsf(r.m) * 0.015625f));
+  }
+  __device__ __forceinline__ float2 line(float2 d) const {  // d = z − m
+    const float2 lp = __ffma2_rn(d, make_float2(kLog2e, kLog2e), nl);  // log2 p
+    return __fmul2_rn(make_float2(fast_exp2(lp.x), fast_exp2(lp.y)), __ffma2_rn(sl, lp, b0));
+  }
+  // d bounded: a masked logit's p is 0, and 0 times the line has to be 0
+  __device__ __forceinline__ float2 bounded(float2 x) const {
+    const float2 d = __fadd2_rn(x, nm);
+    return make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
+  }
+  __device__ __forceinline__ uint4 wide(const uint4& u) const {
+    if constexpr (sizeof(T) == 4) {
+      const float2 x = line(bounded(Pairs<T>::get(u, 0))), y = line(bounded(Pairs<T>::get(u, 1)));
+      return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+    } else {
+      return make_uint4(pack_pair<T>(line(bounded(Pairs<T>::get(u, 0)))), pack_pair<T>(line(bounded(Pairs<T>::get(u, 1)))),
+                        pack_pair<T>(line(bounded(Pairs<T>::get(u, 2)))), pack_pair<T>(line(bounded(Pairs<T>::get(u, 3)))));
+    }
+  }
+  // 16-bit types, unless the row is a wide one: both elements of a pair bounded at once, before they are floats
+  __device__ __forceinline__ uint32_t pair(uint32_t w) const {
+    return pack_pair<T>(line(__fadd2_rn(Pairs<T>::floats(Pairs<T>::raise(w, low)), nm)));
+  }
+  __device__ __forceinline__ uint4 plain(const uint4& u) const {
+    if constexpr (sizeof(T) == 4)
+      return wide(u);
+    else
+      return make_uint4(pair(u.x), pair(u.y), pair(u.z), pair(u.w));
+  }
+  __device__ __forceinline__ T target(float zy, float gl) const {
+    return static_cast<T>(line(bounded(make_float2(zy, zy))).x + gl);
+  }
+};
+
+// Adds vectors to (m, s, u) with one rescaling.
+template <typename T, bool WIDE, int N>
+__device__ __forceinline__ void add_vectors(Stat& t, const uint4 (&u)[N]) {
+  float bm;
+  if constexpr (N == 4)
+    bm = Pairs<T>::max(u[0], u[1], u[2], u[3]);
+  else
+    bm = Pairs<T>::max(u[0]);
+  rescale(t, fmaxf(t.m, bm));
+  const float mb = t.m == -INFINITY ? 0.f : t.m;
+  const float2 nm = make_float2(-mb, -mb), l2 = make_float2(kLog2e, kLog2e);
+  float2 s = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < VN / 2; ++i) {
-        const float2 g = grad(Pairs<T>::get(u, i));
-        e[2 * i] = static_cast<T>(g.x);
-        e[2 * i + 1] = static_cast<T>(g.y);
+  for (int v = 0; v < N; ++v) fold<T, WIDE>(s, q, u[v], nm, l2);
+  t.s += s.x + s.y;
+  t.u += q.x + q.y;
+}
+
+// A row is taken by a group of WARPS warps of each of the CL CTAs of a cluster (CL a power of two; 1 for WARPS < 4).
+// `room`: vectors of a group's slice in shared memory; a thread copies, sums and turns its own vectors, so that the
+// copies need no barrier. The sums are joined and the row's scalars formed by one warp of every CTA.
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_kernel(const LogitsArgs a, int CL, int log_CL,
+                                                                                    int room) {
+  constexpr int VN = Row<T>::VN, kGroup = 32 * WARPS;
+  constexpr bool kCluster = WARPS >= 4;
+  extern __shared__ __align__(16) uint4 slices[];
+  __shared__ Stat part[WARPS];
+  __shared__ __align__(16) float4 of_ctas[kCtasMost];  // (m, s, u) of the slice, the target's logit where it lies there
+  __shared__ __align__(8) uint64_t arrived;
+  __shared__ int gave_up;
+  __shared__ float zy_shared;
+  __shared__ RowOf row_shared;
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : (int)threadIdx.x >> 5;
+  const int group = WARPS == 1 ? (int)threadIdx.x >> 5 : 0;
+  const int tid = WARPS == 1 ? lane : (int)threadIdx.x;
+  const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kGroups<WARPS> + group : (int64_t)(blockIdx.x >> log_CL);
+  const int rank = kCluster ? (int)blockIdx.x & (CL - 1) : 0;
+  if (row >= a.N) return;  // (groups of one warp only)
+  if (kCluster && CL > 1) {
+    if (tid == 0) {
+      tc::mbar_init(&arrived, 1);
+      gave_up = 0;
+      tc::fence_barrier_init();
+      tc::mbar_expect_tx(&arrived, (uint32_t)CL * 16);
+    }
+    cg::this_cluster().barrier_arrive();  // waited for before the CTAs write to one another
+  }
+  const float w = a.in.weights ? a.in.weights[row] : 1.f;
+  const Row<T> z(static_cast<const T*>(a.z) + row * a.ld, a.V);
+  T* out = static_cast<T*>(a.dz) + row * a.ld;
+  const int per = (z.nvec + CL - 1) >> log_CL, lo = rank * per, hi = min(z.nvec, lo + per);
+  const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(z.p) & 15);
+  const int wlo = z.whole_lo(), whi = min(hi, z.whole_hi());
+  auto put_ends = [&](int j, const uint4& u) {
+    const int e = z.first(j);
+    const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VN; ++i)
+      if (e + i >= 0 && e + i < z.V) out[e + i] = t[i];
+  };
+  auto put = [&](int j, const uint4& u) {
+    if (same && j >= wlo && j < whi)
+      *reinterpret_cast<uint4*>(out + z.first(j)) = u;
+    else
+      put_ends(j, u);
+  };
+  if (w == 0.f) {  // a masked row: its logits are not read
+    if (a.dz)
+      for (int j = lo + tid; j < hi; j += kGroup) put(j, make_uint4(0, 0, 0, 0));
+    if (rank == 0 && tid == 0) {
+      a.logp[row] = a.entropy[row] = 0.f;
+      a.rows[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (kCluster && CL > 1) cg::this_cluster().barrier_wait();
+    return;
+  }
+  uint4* buf = slices + group * room - lo;  // buf[j]: vector j
+  const int y = a.y[row];
+  const bool y_ok = y >= 0 && y < z.V;
+  const int jy = y_ok ? (y + z.shift) / VN : -1;
+  auto copy = [&](int j) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf + j)), "l"(z.p + z.first(j)) : "memory");
+  };
+  auto fetch = [&](int at) {
+    if (at >= wlo && at + (kBatch - 1) * kGroup < whi) {
+#pragma unroll
+      for (int v = 0; v < kBatch; ++v) copy(at + v * kGroup);
+    } else {
+#pragma unroll
+      for (int v = 0; v < kBatch; ++v) {
+        const int j = at + v * kGroup;
+        if (j >= wlo && j < whi)
+          copy(j);
+        else if (j < hi)
+          buf[j] = z.load(j);
       }
     }
-    put(j, r);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) fetch(lo + tid + b * kBatch * kGroup);
+  RowInputs in = {};
+  if (warp == 0) in = inputs_of(a.in, row, w);
+  Stat t = {-INFINITY, 0.f, 0.f};
+  int j = lo + tid;
+  for (; j + (kBatch - 1) * kGroup < hi; j += kBatch * kGroup) {
+    fetch(j + kAhead * kBatch * kGroup);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    uint4 u[kBatch];
+#pragma unroll
+    for (int v = 0; v < kBatch; ++v) u[v] = buf[j + v * kGroup];
+    add_vectors<T, false>(t, u);
   }
-  if (mine && !none) out[y] = static_cast<T>(grad(make_float2(zy, zy)).x + gl);  // behind this thread's own store
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  for (; j < hi; j += kGroup) {
+    const uint4 u[1] = {buf[j]};
+    add_vectors<T, false>(t, u);
+  }
+  t = sum_stats(t);
+  if (!plain_way_holds<T>(t.m)) {  // (see fold: extreme rows, again with every difference bounded)
+    t = {-INFINITY, 0.f, 0.f};
+    for (int i = lo + tid; i < hi; i += kGroup) {
+      const uint4 u[1] = {buf[i]};
+      add_vectors<T, true>(t, u);
+    }
+    t = sum_stats(t);
+  }
+  // the target's logit, by the thread that holds it
+  const bool here = jy >= lo && jy < hi, mine = here && ((jy - lo) & (kGroup - 1)) == tid;
+  float zy = -INFINITY;
+  if (mine) zy = static_cast<float>(reinterpret_cast<const T*>(buf + jy)[(y + z.shift) & (VN - 1)]);
+  RowOf r;
+  if constexpr (WARPS == 1) {
+    zy = __shfl_sync(kAll, zy, here ? (jy - lo) & 31 : 0);
+    r = row_of<T>(a, row, in, t, zy, y_ok, lane == 0);
+  } else {
+    if (lane == 0) part[warp] = t;
+    if (mine) zy_shared = zy;
+    __syncthreads();
+    if (warp == 0) {
+      t = lane < WARPS ? part[lane] : Stat{-INFINITY, 0.f, 0.f};
+      t = sum_stats(t);
+    }
+    if (kCluster && CL > 1) {
+      cg::this_cluster().barrier_wait();  // every CTA has started, its barrier is set up
+      if (warp == 0) {
+        // lane r tells CTA r; what the CTAs tell this one arrives with its barrier
+        if (lane < CL) send(&of_ctas[rank], make_float4(t.m, t.s, t.u, here ? zy_shared : 0.f), &arrived, lane);
+        if (!tc::mbar_wait(&arrived, 0, &gave_up, 70) && lane == 0) set_err(a.err, TT_ERR_TIMEOUT);
+        const float4 f = lane < CL ? of_ctas[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        t = sum_stats({f.x, f.y, f.z});
+      }
+    }
+    if (warp == 0) {
+      const float target = kCluster && CL > 1 ? of_ctas[y_ok ? jy / per : 0].w : zy_shared;
+      const RowOf mine_too = row_of<T>(a, row, in, t, target, y_ok, rank == 0 && lane == 0);
+      if (lane == 0) row_shared = mine_too;
+    }
+    __syncthreads();
+    r = row_shared;
+  }
+  if (!a.dz) return;
+  // ---------------------------------------------------------------- the gradient
+  const Turn<T> turn(r);
+  if (r.none) {
+    for (int i = lo + tid; i < hi; i += kGroup) put(i, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  if (sizeof(T) == 4 || r.wide)
+    for (int i = lo + tid; i < hi; i += kGroup) put(i, turn.wide(buf[i]));
+  else
+    for (int i = lo + tid; i < hi; i += kGroup) put(i, turn.plain(buf[i]));
+  if (mine) out[y] = turn.target(zy, r.gl);  // behind this thread's own store
 }
 
 int check_policy(const tt_policy* p, Policy* c) {
@@ -515,25 +644,33 @@ int launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, int CL, b
 constexpr int kSliceMost = 224 * 1024;
 
 template <typename T, int WARPS>
-int launch_rows(const LogitsArgs& a, int CL, cudaStream_t st) {
-  const int nvec = (int)(a.V / Row<T>::VN + 2);
-  const int room = (nvec + CL - 1) / CL + 1;
+int launch_rows(const LogitsArgs& a, int log_CL, cudaStream_t st) {
+  const int CL = 1 << log_CL, nvec = (int)(a.V / Row<T>::VN + 2);
+  const int room = (nvec + CL - 1) / CL;
   const size_t smem = (size_t)room * 16 * kGroups<WARPS>;
   if (smem > kSliceMost) return TT_ERR_UNSUPPORTED;
   if (smem > 48 * 1024 && !tc::smem_attr_set<policy_logits_kernel<T, WARPS>>(kSliceMost)) return TT_ERR_CUDA;
   return launch(policy_logits_kernel<T, WARPS>, (a.N + kGroups<WARPS> - 1) / kGroups<WARPS> * CL,
-                32 * WARPS * kGroups<WARPS>, smem, CL, false, st, a, CL, room);
+                32 * WARPS * kGroups<WARPS>, smem, CL, false, st, a, CL, log_CL, room);
 }
 
+#ifndef TT_PL_VEC
+#define TT_PL_VEC 5120
+#endif
+#ifndef TT_PL_W
+#define TT_PL_W 8
+#endif
 template <typename T>
 int launch_logits(const LogitsArgs& a, cudaStream_t st) {
   const int64_t nvec = a.V / Row<T>::VN + 1, sms = sm_count();
-  if (nvec <= 512 && a.N >= 8 * sms) return launch_rows<T, 1>(a, 1, st);
-  if (nvec <= 1024 && a.N >= 8 * sms) return launch_rows<T, 2>(a, 1, st);
-  if (nvec <= 2048 && a.N >= 4 * sms) return launch_rows<T, 4>(a, 1, st);
-  int CL = 1;
-  while (CL < kCtasMost && (nvec > 2560 * (int64_t)CL || (2 * CL * a.N <= 4 * sms && nvec >= 2 * (int64_t)CL * 256))) CL *= 2;
-  return launch_rows<T, 8>(a, CL, st);
+  if (nvec <= 512 && a.N >= 8 * sms) return launch_rows<T, 1>(a, 0, st);
+  if (nvec <= 1024 && a.N >= 8 * sms) return launch_rows<T, 2>(a, 0, st);
+  int log_CL = 0;
+  while (log_CL < 3 && (nvec > ((int64_t)TT_PL_VEC << log_CL) || (2 * a.N << log_CL) <= 4 * sms && nvec >= (int64_t)512 << log_CL))
+    ++log_CL;
+  if (TT_PL_W == 4 && (a.N << log_CL) >= 4 * sms) return launch_rows<T, 4>(a, log_CL, st);
+  if (TT_PL_W == 16) return launch_rows<T, 16>(a, log_CL, st);
+  return launch_rows<T, 8>(a, log_CL, st);
 }
 
 }  // namespace

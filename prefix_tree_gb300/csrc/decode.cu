@@ -31,14 +31,16 @@ using namespace tc;
 
 constexpr int64_t kPlanMagic = 0x7474646563706c31LL;  // "ttdecpl1"
 constexpr int kKeys = 128;       // keys of a block
-constexpr int kMostRows = 128;   // rows of a tile at most
+constexpr int kMostRows = 128;   // rows of a wide tile
+constexpr int kNarrow = 16;      // and of a narrow one
 constexpr int kMostCtas = 1024;
+constexpr int kPiece = 32;       // rows of a copy
+// Work is shared out by cost: of a block, and of a tile's start (its queries have to be fetched first and its sums
+// written last).
+constexpr int kBlockWide = 4, kBlockNarrow = 3, kStartWide = 12, kStartNarrow = 4;
 // A segment with more rows than this is taken by tiles of 128 rows on the tensor cores' asynchronous path, one with
 // fewer by tiles of 16 on the warps' own.
-#ifndef TT_WIDE
-#define TT_WIDE 32
-#endif
-constexpr int kWideFrom = TT_WIDE;
+constexpr int kWideFrom = 16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Plan: header, first segment of every CTA, and two int4 for each segment that has keys and queries:
@@ -48,10 +50,13 @@ struct PlanHeader {
   int64_t magic;
   int32_t S, B, Hq, Hkv, d, ctas, valid, code;  // code: the error where valid = 0
   int64_t rows, pairs;
-  int32_t blocks, quota, segments;
+  int32_t cost, quota, segments;
 };
 constexpr size_t kPlanCtas = 128, kPlanSegs = kPlanCtas + sizeof(int32_t) * kMostCtas;
 static_assert(sizeof(PlanHeader) <= kPlanCtas, "header");
+
+__host__ __device__ constexpr int block_cost(int tile_rows) { return tile_rows == kMostRows ? kBlockWide : kBlockNarrow; }
+__host__ __device__ constexpr int start_cost(int tile_rows) { return tile_rows == kMostRows ? kStartWide : kStartNarrow; }
 
 struct PlanArgs {
   const int32_t *kv_begin, *kv_len, *q_begin, *q_end;
@@ -63,83 +68,83 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 1024;
 
-struct Count {
-  int64_t blocks, rows;
-  int n;
-};
-__device__ __forceinline__ Count operator+(Count a, Count b) { return {a.blocks + b.blocks, a.rows + b.rows, a.n + b.n}; }
-
-// Exclusive sums over the block's threads, and the total.
-__device__ __forceinline__ Count scan_block(Count x, Count* room, Count& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Count in = x;
+// Exclusive sums of x and y over the block's threads, and the totals. `room`: one place per warp.
+__device__ __forceinline__ void scan_block(int64_t& x, int64_t& y, int64_t& all_x, int64_t& all_y, longlong2* room) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t x0 = x, y0 = y;
+  auto scan_warp = [&](int64_t& u, int64_t& v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Count y = {__shfl_up_sync(~0u, in.blocks, o), __shfl_up_sync(~0u, in.rows, o), __shfl_up_sync(~0u, in.n, o)};
-    if (lane >= o) in = in + y;
-  }
-  if (lane == 31) room[warp] = in;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t p = __shfl_up_sync(~0u, u, o), q = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) u += p, v += q;
+    }
+  };
+  scan_warp(x, y);
+  if (lane == 31) room[warp] = make_longlong2(x, y);
   __syncthreads();
-  Count before = {0, 0, 0};
-  total = {0, 0, 0};
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w == warp) before = total;
-    total = total + room[w];
-  }
-  __syncthreads();
-  return {before.blocks + in.blocks - x.blocks, before.rows + in.rows - x.rows, before.n + in.n - x.n};
+  int64_t u = lane < warps ? room[lane].x : 0, v = lane < warps ? room[lane].y : 0;
+  scan_warp(u, v);
+  all_x = __shfl_sync(~0u, u, 31);
+  all_y = __shfl_sync(~0u, v, 31);
+  const int64_t bx = __shfl_sync(~0u, u, (warp + 31) & 31), by = __shfl_sync(~0u, v, (warp + 31) & 31);
+  x += (warp ? bx : 0) - x0;
+  y += (warp ? by : 0) - y0;
 }
 
-// One CTA: two passes over the segments, the first for the totals.
+// One CTA; a thread takes consecutive segments.
 __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const PlanArgs a) {
-  __shared__ Count room[kPlanThreads / 32];
+  __shared__ longlong2 room[kPlanThreads / 32];
   __shared__ int code;
   PlanHeader* hdr = static_cast<PlanHeader*>(a.plan);
   int32_t* cta_seg = reinterpret_cast<int32_t*>(static_cast<char*>(a.plan) + kPlanCtas);
   int4* segs = reinterpret_cast<int4*>(static_cast<char*>(a.plan) + kPlanSegs);
   if (threadIdx.x == 0) code = 0;
   __syncthreads();
-  const int G = a.Hq / a.Hkv;
-  int quota = 1;
-  Count sum = {0, 0, 0};
-  for (int pass = 0; pass < 2; ++pass) {
-    sum = {0, 0, 0};
-    for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
-      const int s = s0 + (int)threadIdx.x;
-      int kb = 0, n = 0, q0 = 0, q1 = 0;
-      if (s < a.S) {
-        kb = a.kv_begin[s], n = a.kv_len[s], q0 = a.q_begin[s], q1 = a.q_end[s];
-        if (kb < 0 || n < 0 || (int64_t)kb + n > a.rows || q0 < 0 || q1 < q0 || q1 > a.B) {
-          atomicCAS(&code, 0, TT_ERR_INVALID_ARG);
-          n = 0;
-        }
-      }
-      Count c = {0, 0, 0};
-      const int rows = (q1 - q0) * G, tile_rows = rows > kWideFrom ? kMostRows : 16;
-      const int tiles = (rows + tile_rows - 1) / tile_rows;
-      if (n > 0 && rows > 0) c = {(int64_t)((n + kKeys - 1) / kKeys) * tiles * a.Hkv, (int64_t)rows * a.Hkv, 1};
-      Count total;
-      const Count at = sum + scan_block(c, room, total);
-      if (pass == 1 && c.n) {
-        segs[2 * at.n] = make_int4(kb, n, q0, q1 - q0);
-        segs[2 * at.n + 1] = make_int4((int)at.blocks, tiles, tile_rows, (int)at.rows);
-        // the CTAs whose run begins in it
-        for (int64_t r = (at.blocks + quota - 1) / quota; r * quota < at.blocks + c.blocks; ++r) cta_seg[r] = at.n;
-      }
-      sum = sum + total;
+  const int G = a.Hq / a.Hkv, each = (a.S + (int)blockDim.x - 1) / (int)blockDim.x;
+  const int s0 = min((int64_t)a.S, (int64_t)threadIdx.x * each), s1 = min(a.S, s0 + each);
+  // a segment's first row, keys, queries, and its cost, or 0 where it has no work
+  auto read = [&](int s, int4& x, int& tiles, int& tile_rows) -> int64_t {
+    const int q1 = a.q_end[s];
+    x = make_int4(a.kv_begin[s], a.kv_len[s], a.q_begin[s], 0);
+    if (x.x < 0 || x.y < 0 || (int64_t)x.x + x.y > a.rows || x.z < 0 || q1 < x.z || q1 > a.B) {
+      atomicCAS(&code, 0, TT_ERR_INVALID_ARG);
+      return 0;
     }
-    if (pass == 0) {
-      if (threadIdx.x == 0 && sum.rows > a.pairs * a.Hq) atomicCAS(&code, 0, TT_ERR_WORKSPACE);
-      if (threadIdx.x == 0 && sum.blocks > INT32_MAX / 2) atomicCAS(&code, 0, TT_ERR_UNSUPPORTED);
-      __syncthreads();
-      if (code) break;
-      quota = (int)((sum.blocks + a.ctas - 1) / a.ctas);
-      if (quota < 1) quota = 1;
-    }
-  }
+    x.w = q1 - x.z;
+    const int64_t rows = (int64_t)x.w * G;
+    if (!x.y || !rows) return 0;
+    tile_rows = rows > kWideFrom ? kMostRows : kNarrow;
+    tiles = (int)((rows + tile_rows - 1) / tile_rows);
+    return ((int64_t)((x.y + kKeys - 1) / kKeys) * block_cost(tile_rows) + start_cost(tile_rows)) * tiles * a.Hkv;
+  };
+  int64_t cost = 0, rows_n = 0;  // rows_n: partial rows << 24, and segments
+  int4 x;
+  int tiles, tile_rows;
+  for (int s = s0; s < s1; ++s)
+    if (const int64_t c = read(s, x, tiles, tile_rows)) cost += c, rows_n += ((int64_t)x.w * a.Hq << 24) + 1;
+  int64_t all_cost, all_rows_n;
+  scan_block(cost, rows_n, all_cost, all_rows_n, room);
+  if (threadIdx.x == 0 && (all_rows_n >> 24) > a.pairs * a.Hq) atomicCAS(&code, 0, TT_ERR_WORKSPACE);
+  if (threadIdx.x == 0 && all_cost > INT32_MAX / 2) atomicCAS(&code, 0, TT_ERR_UNSUPPORTED);
+  __syncthreads();
   if (threadIdx.x == 0) {
-    *hdr = {kPlanMagic, a.S, a.B, a.Hq, a.Hkv, a.d, a.ctas, code == 0, code, a.rows, a.pairs, (int)sum.blocks, quota, sum.n};
+    const int n = (int)(all_rows_n & 0xffffff);
+    const int64_t quota = max((all_cost + a.ctas - 1) / a.ctas, (int64_t)1);
+    *hdr = {kPlanMagic, a.S, a.B, a.Hq, a.Hkv, a.d, a.ctas, code == 0, code, a.rows, a.pairs, (int)all_cost, (int)quota, n};
     if (code) set_err(a.err, code);
+  }
+  if (code) return;
+  const int quota = (int)max((all_cost + a.ctas - 1) / a.ctas, (int64_t)1);
+  for (int s = s0; s < s1; ++s) {
+    const int64_t c = read(s, x, tiles, tile_rows);
+    if (!c) continue;
+    const int n = (int)(rows_n & 0xffffff);
+    segs[2 * n] = x;
+    segs[2 * n + 1] = make_int4((int)cost, tiles, tile_rows, (int)(rows_n >> 24));
+    // the CTAs whose run begins in it
+    for (int64_t r = (cost + quota - 1) / quota; r * quota < cost + c; ++r) cta_seg[r] = n;
+    cost += c;
+    rows_n += ((int64_t)x.w * a.Hq << 24) + 1;
   }
 }
 
@@ -166,36 +171,50 @@ __device__ __forceinline__ int plan_error(const DecodeArgs& a, int D) {
   return h->valid ? 0 : h->code;
 }
 
-// A run's way over its blocks: segment, head, tile, block.
+// A run's way over its blocks: segment, head, tile, block. Tiles follow one another on a line of costs, each its start
+// and then its blocks; a block belongs to the run [w, end) in which its place begins.
 struct Walk {
   const int4* segs;
-  int Hkv, G;
-  int seg, h, tile, blk;            // where it is
+  int Hkv, G, w, end;
+  int seg, h, tile, blk;            // where it is; w: the block's place
   int kv, len, q0, rows, nb;        // the segment's first key row, keys, first query, rows of a head, blocks of a tile
-  int tiles, tile_rows, row_base;
-  __device__ __forceinline__ void load() {
+  int tiles, tile_rows, row_base, cost, start;
+  __device__ __forceinline__ int load() {
     const int4 x = segs[2 * seg], y = segs[2 * seg + 1];
     kv = x.x, len = x.y, q0 = x.z, rows = x.w * G, nb = (len + kKeys - 1) / kKeys;
     tiles = y.y, tile_rows = y.z, row_base = y.w;
+    cost = block_cost(tile_rows), start = start_cost(tile_rows);
+    return y.x;
   }
-  __device__ __forceinline__ Walk(const int4* segs_, int Hkv_, int G_, int first_seg, int w) : segs(segs_), Hkv(Hkv_), G(G_) {
-    seg = first_seg;
-    load();
-    const int at = w - segs[2 * seg + 1].x, unit = at / nb;
-    blk = at - unit * nb;
+  __device__ __forceinline__ Walk(const int4* segs_, int Hkv_, int G_, int first_seg, int w_, int end_)
+      : segs(segs_), Hkv(Hkv_), G(G_), w(w_), end(end_), seg(first_seg) {
+    const int at = w - load(), whole = nb * cost + start, unit = at / whole, off = at - unit * whole - start;
+    blk = off <= 0 ? 0 : (off + cost - 1) / cost;
+    w += blk * cost - off;
     h = unit / tiles;
     tile = unit - h * tiles;
+    if (blk == nb) next_tile();
   }
-  // to the next block; `more`: there is one in this run
-  __device__ __forceinline__ void next(bool more) {
-    if (++blk < nb) return;
+  __device__ __forceinline__ bool done() const { return w >= end; }
+  // blocks of this tile in the run, from here on
+  __device__ __forceinline__ int stretch() const { return min(nb - blk, (end - w + cost - 1) / cost); }
+  // past n of them
+  __device__ __forceinline__ void pass(int n) {
+    w += n * cost;
+    blk += n;
+    if (blk == nb) next_tile();
+  }
+  __device__ __forceinline__ void next_tile() {
     blk = 0;
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++h < Hkv) return;
-    h = 0;
-    ++seg;
-    if (more) load();
+    if (++tile == tiles) {
+      tile = 0;
+      if (++h == Hkv) {
+        h = 0;
+        ++seg;
+        if (w < end) load();
+      }
+    }
+    w += start;
   }
   // place of row 0 of the current tile among the partial rows, for CTA c
   __device__ __forceinline__ int64_t part_row(int c) const {
@@ -238,9 +257,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 constexpr int kWarps = 8;                  // that compute
-constexpr int kThreads = 32 * (kWarps + 2);  // and one that copies, one that issues the tensor-core products
+// and four more: one copies the K tiles, one the V tiles (a thread suspended in a wait holds up the others of its warp), one
+// issues the tensor-core products.
+constexpr int kThreads = 32 * (kWarps + 4), kCopyK = kWarps, kCopyV = kWarps + 1, kIssue = kWarps + 2;
+// Twelve warps launch with 168 registers each; those four give some back for the computing ones:
+// 128·136 + 256·184 = 64,512 = 384·168 = 64,512 launched.
+constexpr uint32_t kRegsControl = 136, kRegsCompute = 184;
+static_assert(128 * kRegsControl + 256 * kRegsCompute <= kThreads * 168, "register split exceeds the launch's registers");
 constexpr int kKStages = 3, kVStages = 2;  // K and V tiles in shared memory
-constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256, kColP = 384;  // S and P twice: 128 and 64 columns each
+// Tensor memory: each of two groups of four warps has 128 columns for S, whose places its weights take, and up to 128
+// for O.
+constexpr uint32_t kTmemCols = 512, kGroupCols = 256, kColO = 128;
 // The running maximum of a row moves only when it grows by more than this (log2 units): weights stay below 2^8.
 constexpr float kRescale = 8.0f;
 
@@ -249,25 +276,32 @@ struct Smem {
   static constexpr uint32_t kBox = kKeys * 128;            // 64 columns of a block's keys, 128-byte swizzle
   static constexpr uint32_t kTile = (D / 64) * kBox;
   static constexpr uint32_t q = 0;                         // the 128 rows of a wide tile, laid out as a K tile
-  static constexpr uint32_t kQLd = D * 2 + 16;             // bytes of a row of Q of a narrow tile
   static constexpr uint32_t k0 = q + kTile;
   static constexpr uint32_t v0 = k0 + kKStages * kTile;
-  static constexpr uint32_t kPLd = kKeys * 2 + 16;         // bytes of a row of weights: rows fall in different banks
-  static constexpr uint32_t p = v0 + kVStages * kTile;     // narrow tiles: [16] rows of weights
-  static constexpr uint32_t max = p + 16 * kPLd;           // [kWarps][16] f32
-  static constexpr uint32_t sum = max + kWarps * 16 * 4;   // [kWarps][16] f32
-  static constexpr uint32_t row_max = sum + kWarps * 16 * 4;  // [16] f32
-  static constexpr uint32_t wide = row_max + 16 * 4;       // wide tiles: [2][128] f32 of the two halves of a row
-  static constexpr uint32_t bars = wide + 2 * 128 * 4;
+  // wide tiles: maximum and sum [2][2][128] f32 of the two groups' rows; narrow tiles: twice [kWarps][16] f32
+  static constexpr uint32_t rows = v0 + kVStages * kTile;
+  static constexpr uint32_t bars = rows + 4 * 128 * 4;
   static constexpr uint32_t misc = bars + 32 * 8;
-  static constexpr uint32_t total = misc + 16 + 1024;      // + slack for the alignment to 1024 bytes
+  static constexpr uint32_t total = misc + 16;             // with the start aligned to 1024 bytes
+  static_assert(kWarps * 8 * D * 4 <= kTile, "the joining rows exceed the place of Q");
 };
-// Barriers. EMPTY: the eight computing warps and the issuing one; a warp arrives for a block after it has seen the
-// block's FULL, so that it cannot be a phase ahead.
+// Barriers. EMPTY: one arrival of each computing warp after a narrow block; after a wide one all from the issuing thread,
+// the last of them when its products are done.
 constexpr int K_FULL = 0, V_FULL = K_FULL + kKStages, K_EMPTY = V_FULL + kVStages, V_EMPTY = K_EMPTY + kKStages,
-              Q_READY = V_EMPTY + kVStages, S_FULL = Q_READY + 1, S_FREE = S_FULL + 2, P_READY = S_FREE + 2,
-              P_FREE = P_READY + 2, FINAL = P_FREE + 2, NBAR = FINAL + 1;
+              Q_READY = V_EMPTY + kVStages, S_FULL = Q_READY + 1, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
+              FINAL = O_DONE + 1, NBAR = FINAL + 1;
 static_assert(NBAR <= 32, "barriers");
+
+__device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// A ring's stage and phase n blocks on.
+__device__ __forceinline__ void pass_stages(int n, int& stage, int& phase, int stages) {
+  stage += n;
+  phase ^= (stage / stages) & 1;
+  stage %= stages;
+}
 
 // kind::f16 instruction descriptor for type T.
 template <typename T>
@@ -279,434 +313,492 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecodeArgs a) {
   using L = Smem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
-  if (const int e = plan_error(a, D)) {
+  int e = plan_error(a, D);
+  if (smem_u32(sm) & 1023) e = TT_ERR_UNSUPPORTED;  // (the layout of the tiles rests on it)
+  if (e) {
     if (threadIdx.x == 0) set_err(a.err, e);
     return;
   }
   const int c = blockIdx.x;
-  const int64_t w0 = (int64_t)c * hdr->quota, w1 = min((int64_t)hdr->blocks, w0 + hdr->quota);
-  if (w0 >= w1) return;
+  const int64_t w0 = (int64_t)c * hdr->quota;
+  if (w0 >= hdr->cost) return;
+  const int w1 = (int)min((int64_t)hdr->cost, w0 + hdr->quota);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&bar[K_FULL + i], 1);
-      mbar_init(&bar[K_EMPTY + i], kWarps + 1);
+      mbar_init(&bar[K_EMPTY + i], kWarps);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&bar[V_FULL + i], 1);
-      mbar_init(&bar[V_EMPTY + i], kWarps + 1);
+      mbar_init(&bar[V_EMPTY + i], kWarps);
     }
     mbar_init(&bar[Q_READY], 32 * kWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar[S_FULL + i], 1);
-      mbar_init(&bar[S_FREE + i], 32 * kWarps);
-      mbar_init(&bar[P_READY + i], 32 * kWarps);
-      mbar_init(&bar[P_FREE + i], 1);
+      mbar_init(&bar[P_READY + i], 128);
     }
+    mbar_init(&bar[O_DONE], 1);
     mbar_init(&bar[FINAL], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kWarps + 1) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == kIssue) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const int n = (int)(w1 - w0), G = a.Hq / a.Hkv;
+  const int G = a.Hq / a.Hkv;
   const int4* segs = reinterpret_cast<const int4*>(static_cast<const char*>(a.plan) + kPlanSegs);
-  Walk at(segs, a.Hkv, G, reinterpret_cast<const int32_t*>(static_cast<const char*>(a.plan) + kPlanCtas)[c], (int)w0);
+  Walk at(segs, a.Hkv, G, reinterpret_cast<const int32_t*>(static_cast<const char*>(a.plan) + kPlanCtas)[c], (int)w0, w1);
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ copies: lane 0 the K tiles, lane 1 the V tiles
-    if (lane < 2) {
-      const CUtensorMap* map = lane ? &tmV : &tmK;
-      const int full = lane ? V_FULL : K_FULL, empty = lane ? V_EMPTY : K_EMPTY, stages = lane ? kVStages : kKStages;
-      uint8_t* dst = sm + (lane ? L::v0 : L::k0);
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if ((warp == kCopyK || warp == kCopyV) && lane == 0) {
+      // ---------------------------------------------------------- copies
+      const bool v = warp == kCopyV;
+      const CUtensorMap* map = v ? &tmV : &tmK;
+      const int full = v ? V_FULL : K_FULL, empty = v ? V_EMPTY : K_EMPTY, stages = v ? kVStages : kKStages;
+      uint8_t* dst = sm + (v ? L::v0 : L::k0);
       prefetch_tmap(map);
       int i = 0, st = 0, phase = 0;
-      for (; i < n; ++i) {
-        if (i >= stages && !mbar_wait(&bar[empty + st], phase ^ 1, abort_flag, 50 + lane)) break;
-        mbar_expect_tx(&bar[full + st], L::kTile);
+      for (bool ok = true; ok && !at.done();) {
+        const int n = at.stretch();
+        int y0 = at.kv + at.blk * kKeys, left = at.len - at.blk * kKeys;
+        for (int t = 0; t < n; ++t, ++i, y0 += kKeys, left -= kKeys) {
+          if (i >= stages && !mbar_wait(&bar[empty + st], phase ^ 1, abort_flag, 50)) {
+            ok = false;
+            break;
+          }
+          // the pieces that hold keys of the segment
+          const int pieces = (min(kKeys, left) + kPiece - 1) / kPiece;
+          mbar_expect_tx(&bar[full + st], pieces * kPiece * D * 2);
+          for (int y = 0; y < pieces; ++y)
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_2d(dst + st * L::kTile + x * L::kBox, map, &bar[full + st], at.h * D + x * 64, at.kv + at.blk * kKeys);
-        at.next(i + 1 < n);
-        if (++st == stages) st = 0, phase ^= 1;
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_2d(dst + st * L::kTile + x * L::kBox + y * kPiece * 128, map, &bar[full + st], at.h * D + x * 64,
+                          y0 + y * kPiece);
+          if (++st == stages) st = 0, phase ^= 1;
+        }
+        at.pass(n);
       }
       // every copy issued has landed before the CTA may leave
       for (int j = i - 1; j >= 0 && j >= i - stages; --j) mbar_drain(&bar[full + j % stages], (j / stages) & 1, abort_flag);
-    }
-  } else if (warp == kWarps + 1) {
-    // ------------------------------------------------------------ tensor-core products of the wide tiles
-    if (lane == 0) {
+    } else if (warp == kIssue && lane == 0) {
+      // ---------------------------------------------------------- tensor-core products of the wide tiles
       constexpr uint32_t idS = idesc_of<T>(128, 128, 0, 0), idPV = idesc_of<T>(128, D, 0, 1);
       const uint64_t dq = smem_desc(smem_u32(sm + L::q), 16, 1024);
-      int j = 0, tiles = 0;              // wide blocks and wide tiles so far
-      int pv_st = -1, pv_phase = 0;      // the block whose second product is still to be issued: its V stage,
-      bool pv_first = false;             // and whether it is its tile's first
-      bool ok = true;
-      auto issue_pv = [&]() -> bool {    // of wide block j − 1
-        const int bb = (j - 1) & 1;
-        if (!mbar_wait(&bar[P_READY + bb], ((j - 1) >> 1) & 1, abort_flag, 54)) return false;
+      int tiles = 0, blocks[2] = {0, 0};  // wide tiles so far, and blocks of each group
+      int kst = 0, kphase = 0, vst = 0, vphase = 0;
+      // the block whose second product is still to be issued: its V stage and group, and whether it is the group's first
+      int pv_st = -1, pv_phase = 0, pv_group = 0;
+      bool pv_first = false, ok = true;
+      auto issue_pv = [&]() -> bool {
+        if (!mbar_wait(&bar[P_READY + pv_group], (blocks[pv_group] - 1) & 1, abort_flag, 54)) return false;
         if (!mbar_wait(&bar[V_FULL + pv_st], pv_phase, abort_flag, 55)) return false;
         tc_fence_after();
         const uint64_t dv = smem_desc(smem_u32(sm + L::v0 + pv_st * L::kTile), L::kBox, 1024);
+        const uint32_t cols = tbase + pv_group * kGroupCols;
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          umma_ts(tbase + kColO, tbase + kColP + bb * 64 + k * 8, desc_at(dv, k * 2048), idPV, !pv_first || k > 0);
-        umma_commit(&bar[P_FREE + bb]);
+          umma_ts(cols + kColO, cols + k * 8, desc_at(dv, k * 2048), idPV, !pv_first || k > 0);
+        arrive_n(&bar[V_EMPTY + pv_st], kWarps - 1);
         umma_commit(&bar[V_EMPTY + pv_st]);
         pv_st = -1;
         return true;
       };
-      int kst = 0, kphase = 0, vst = 0, vphase = 0;
-      for (int i = 0; i < n; ++i) {
-        if (!mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 56)) { ok = false; break; }
+      while (ok && !at.done()) {
+        const int n = at.stretch();
         if (at.tile_rows == kMostRows) {
-          const int bb = j & 1;
-          const bool first = i == 0 || at.blk == 0;
-          if (first && !mbar_wait(&bar[Q_READY], tiles++ & 1, abort_flag, 57)) { ok = false; break; }
-          if (j >= 2 && !mbar_wait(&bar[S_FREE + bb], ((j - 2) >> 1) & 1, abort_flag, 58)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t dk = smem_desc(smem_u32(sm + L::k0 + kst * L::kTile), 16, 1024);
+          ok = mbar_wait(&bar[Q_READY], tiles++ & 1, abort_flag, 57);
+          for (int t = 0; ok && t < n; ++t) {  // the groups take the blocks in turn
+            const int g = t & 1;
+            if (!mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 56)) { ok = false; break; }
+            // (S of this group's block before was read before its weights were ready, and those were used by the product
+            // issued before this one)
+            tc_fence_after();
+            const uint64_t dk = smem_desc(smem_u32(sm + L::k0 + kst * L::kTile), 16, 1024);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * L::kBox + (k & 3) * 32;
-            umma_ss(tbase + kColS + bb * 128, desc_at(dq, off), desc_at(dk, off), idS, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * L::kBox + (k & 3) * 32;
+              umma_ss(tbase + g * kGroupCols, desc_at(dq, off), desc_at(dk, off), idS, k > 0);
+            }
+            umma_commit(&bar[S_FULL + g]);
+            arrive_n(&bar[K_EMPTY + kst], kWarps - 1);
+            umma_commit(&bar[K_EMPTY + kst]);
+            if (pv_st >= 0) ok = issue_pv();
+            ++blocks[g];
+            pv_st = vst, pv_phase = vphase, pv_group = g, pv_first = t < 2;
+            if (++kst == kKStages) kst = 0, kphase ^= 1;
+            if (++vst == kVStages) vst = 0, vphase ^= 1;
           }
-          umma_commit(&bar[S_FULL + bb]);
-          umma_commit(&bar[K_EMPTY + kst]);
-          if (pv_st >= 0 && !issue_pv()) { ok = false; break; }
-          pv_st = vst, pv_phase = vphase, pv_first = first;
-          ++j;
-          // a tile's last block is finished here: the computing warps wait for it before they turn to the next tile
-          if ((i + 1 == n || at.blk + 1 == at.nb) && !issue_pv()) { ok = false; break; }
-        } else {  // the computing warps' alone
-          mbar_arrive(&bar[K_EMPTY + kst]);
-          if (!mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 59)) { ok = false; break; }
-          mbar_arrive(&bar[V_EMPTY + vst]);
+          ok = ok && issue_pv();
+          umma_commit(&bar[O_DONE]);
+        } else {
+          pass_stages(n, kst, kphase, kKStages);
+          pass_stages(n, vst, vphase, kVStages);
         }
-        at.next(i + 1 < n);
-        if (++kst == kKStages) kst = 0, kphase ^= 1;
-        if (++vst == kVStages) vst = 0, vphase ^= 1;
+        at.pass(n);
       }
       // completes after every product of this CTA, also after an abort: shared and tensor memory outlive them
-      (void)ok;
       umma_commit(&bar[FINAL]);
       mbar_drain(&bar[FINAL], 0, abort_flag);
     }
   } else {
-    // ------------------------------------------------------------ 16 rows against the blocks, all warps on every block
-    constexpr int kCols = D / kWarps;     // columns of O of a warp
-    constexpr int kOut = kCols / 8;
-    const int r0 = lane >> 2, cc = (lane & 3) * 2;
-    const int mi = lane >> 3, mr = lane & 7;
-    float o[kOut][4], m[2], l[2];
-    float* smax = reinterpret_cast<float*>(sm + L::max);
-    float* ssum = reinterpret_cast<float*>(sm + L::sum);
-    float* srow = reinterpret_cast<float*>(sm + L::row_max);
-    const uint32_t pbase = smem_u32(sm + L::p);
-    const uint32_t qbase = smem_u32(sm + L::q) + ((mi & 1) * 8 + mr) * L::kQLd + (mi >> 1) * 16;
-    float* half_of_row = reinterpret_cast<float*>(sm + L::wide);
-    int j = 0;                            // wide blocks so far
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+    // ------------------------------------------------------------ the computing warps, tile by tile
+    // Rows behind the segment's end are another segment's, or not yet written: a weight of 0 times what lies there must be
+    // 0. Zeroes rows [lo, hi) of a V tile, by `threads` threads.
+    auto clear_rows = [](uint8_t* tile, int lo, int hi, int thread, int threads) {
+      for (int e = thread; e < (hi - lo) * (D / 8); e += threads) {
+        const int key = lo + e / (D / 8), u = e % (D / 8);
+        *reinterpret_cast<uint4*>(tile + (u >> 3) * L::kBox + key * 128 + ((u & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the products, and the next copy
+    };
+    float* shared_rows = reinterpret_cast<float*>(sm + L::rows);
+    int j = 0, wide_tiles = 0;            // blocks of this warp's group and wide tiles so far
     int kst = 0, kphase = 0, vst = 0, vphase = 0;
-    for (int i = 0; i < n; ++i) {
+    while (!at.done()) {
       const int tile_n = min(at.tile_rows, at.rows - at.tile * at.tile_rows);  // rows of this tile
-      const bool first = i == 0 || at.blk == 0, last = i + 1 == n || at.blk + 1 == at.nb;
-      const int valid = at.len - at.blk * kKeys;  // keys of the segment in this block, possibly more than there are
-      // rows behind the segment's end are another segment's, or not yet written: a weight of 0 times what lies there must
-      // be 0
-      auto clear_behind = [&]() {
-        if (valid >= kKeys) return;
-        for (int e = (int)threadIdx.x; e < (kKeys - valid) * (D / 8); e += 32 * kWarps) {
-          const int key = valid + e / (D / 8), u = e % (D / 8);
-          *reinterpret_cast<uint4*>(sm + L::v0 + vst * L::kTile + (u >> 3) * L::kBox + key * 128 + ((u & 7) << 4)) =
-              make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the products, and the next copy
-      };
+      const int64_t part = at.part_row(c);
+      const int n = at.stretch();
+      int left = at.len - at.blk * kKeys;  // keys of the segment from this block on
       if (at.tile_rows == kMostRows) {
-        // ---------------------------------------------------------- 128 rows: a thread one row and half of the keys
-        const int wq = warp & 3, hf = warp >> 2, r = wq * 32 + lane, bb = j & 1;
-        const uint32_t lanes = tbase + ((uint32_t)(wq * 32) << 16);
-        if (first) {
-          // the rows of Q into shared memory, in the swizzled layout that the products read
-          for (int e = (int)threadIdx.x; e < kMostRows * (D / 8); e += 32 * kWarps) {
-            const int row = e / (D / 8), u = e % (D / 8), rr = at.tile * kMostRows + row;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (row < tile_n)
-              x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(at.q0 + rr / G) * a.q_ld +
-                                                  (int64_t)(at.h * G + rr % G) * D + u * 8);
-            *reinterpret_cast<uint4*>(sm + L::q + (u >> 3) * L::kBox + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = x;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          mbar_arrive(&bar[Q_READY]);
-          m[0] = -INFINITY;
-          l[0] = 0.f;
+        // ---------------------------------------------------------- 128 rows: two groups of four warps take the blocks
+        // in turn, a thread one row; while one group is at its exponentials the other's products run
+        const int wq = warp & 3, g = warp >> 2, r = wq * 32 + lane;
+        const uint32_t lanes = tbase + ((uint32_t)(wq * 32) << 16), cols = lanes + g * kGroupCols;
+        // the rows of Q into shared memory, in the swizzled layout that the products read
+        constexpr int kUnits = kMostRows * (D / 8) / (32 * kWarps);  // 16-byte pieces of a thread, all under way at once
+        uint4 piece[kUnits];
+#pragma unroll
+        for (int e = 0; e < kUnits; ++e) {
+          const int at_e = (int)threadIdx.x + e * 32 * kWarps, row = at_e / (D / 8), u = at_e % (D / 8);
+          const int rr = at.tile * kMostRows + row;
+          piece[e] = make_uint4(0, 0, 0, 0);
+          if (row < tile_n)
+            piece[e] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(at.q0 + rr / G) * a.q_ld +
+                                                       (int64_t)(at.h * G + rr % G) * D + u * 8);
         }
-        mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 60);
-        mbar_wait(&bar[S_FULL + bb], (j >> 1) & 1, abort_flag, 61);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[K_EMPTY + kst]);
+#pragma unroll
+        for (int e = 0; e < kUnits; ++e) {
+          const int at_e = (int)threadIdx.x + e * 32 * kWarps, row = at_e / (D / 8), u = at_e % (D / 8);
+          *reinterpret_cast<uint4*>(sm + L::q + (u >> 3) * L::kBox + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = piece[e];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&bar[Q_READY]);
+        float m = -INFINITY, l = 0.f;
+        const float size = fabsf(a.scale_log2);
+        for (int t = 0; t < n; ++t, left -= kKeys) {
+          if ((t & 1) == g) {
+            const int valid = left;  // possibly more than a block's
+            mbar_wait(&bar[S_FULL + g], j & 1, abort_flag, 61);
+            tc_fence_after();
+            // 32 scores of the row; a negative scale turns them round, so that the maximum is the largest weight's; keys
+            // that are not there become -inf
+            auto scores = [&](int q, uint32_t (&x)[32]) {
+              if (a.scale_log2 < 0.f) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] ^= 0x80000000u;
+              }
+              if (valid < kKeys) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (q * 32 + e >= valid) x[e] = 0xff800000u;
+              }
+            };
+            // (loaded again for the weights: a thread has no registers for a whole row)
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint32_t x[2][32];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) tmem_ld32(cols + half * 64 + q * 32, x[q]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                tmem_pin(x[q]);
+                scores(2 * half + q, x[q]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  mx[e & 3] = fmax3f(mx[e & 3], __uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1]));
+              }
+            }
+            const float top = fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * size;
+            bool moved = false;
+            float f = 1.f;
+            if (top > m + kRescale) {
+              f = fast_exp2(m - top);  // 0 at the group's first keys
+              l *= f;
+              moved = t >= 2;
+              m = top;
+            }
+            if (__any_sync(~0u, moved)) {  // (the products into O that were issued before this S are done, as it is)
+              const float by = moved ? f : 1.f;
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t y[32];
+                tmem_ld32(cols + kColO + q * 32, y);
+                tmem_ld_wait();
+                tmem_pin(y);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * by);
+                tmem_st32(cols + kColO + q * 32, y);
+              }
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            const float2 nm = make_float2(-mu, -mu), by = make_float2(size, size);
+            float2 rs = make_float2(0.f, 0.f);
+            // the weights of 32 scores take half of the columns of those: never ones that are still to be read
+            auto weigh = [&](int q, const uint32_t (&y)[32]) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 d = __ffma2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), by, nm);
+                const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                rs = __fadd2_rn(rs, w);
+                pk[e] = pack2<T>(w.x, w.y);
+              }
+              tmem_st16(cols + q * 16, pk);
+            };
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint32_t x[2][32];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) tmem_ld32(cols + half * 64 + q * 32, x[q]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                tmem_pin(x[q]);
+                scores(2 * half + q, x[q]);
+                weigh(2 * half + q, x[q]);
+              }
+            }
+            l += rs.x + rs.y;
+            tmem_st_wait();
+            if (valid < kKeys) {
+              mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 64);
+              clear_rows(sm + L::v0 + vst * L::kTile, valid, kKeys, threadIdx.x & 127, 128);
+            }
+            tc_fence_before();
+            mbar_arrive(&bar[P_READY + g]);
+            ++j;
+          }
+          if (++vst == kVStages) vst = 0, vphase ^= 1;
+        }
+        pass_stages(n, kst, kphase, kKStages);
+        // the tile's part: both groups' sums of a row from tensor memory, each thread half of the columns
+        shared_rows[(g * 2) * 128 + r] = m;
+        shared_rows[(g * 2 + 1) * 128 + r] = l;
+        mbar_wait(&bar[O_DONE], wide_tiles++ & 1, abort_flag, 65);
         tc_fence_after();
-        uint32_t x[2][32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_ld32(lanes + kColS + bb * 128 + 64 * hf + q * 32, x[q]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_pin(x[q]);
-        tc_fence_before();
-        mbar_arrive(&bar[S_FREE + bb]);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        const int seen = valid - 64 * hf;  // keys of this half that are there
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int col = q * 32 + 2 * e;
-            const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1])),
-                                        make_float2(a.scale_log2, a.scale_log2));
-            const float y0 = col < seen ? y.x : -INFINITY, y1 = col + 1 < seen ? y.y : -INFINITY;
-            x[q][2 * e] = __float_as_uint(y0);
-            x[q][2 * e + 1] = __float_as_uint(y1);
-            mx[e & 3] = fmax3f(mx[e & 3], y0, y1);
-          }
-        const float pm = fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-        half_of_row[hf * 128 + r] = pm;
         named_barrier(2 + wq, 64);
-        const float top = fmaxf(pm, half_of_row[(hf ^ 1) * 128 + r]);
-        named_barrier(2 + wq, 64);  // (read before the next block writes)
-        bool moved = false;
-        float f = 1.f;
-        if (top > m[0] + kRescale) {
-          f = fast_exp2(m[0] - top);  // 0 at the tile's first keys
-          l[0] *= f;
-          moved = !first;
-          m[0] = top;
-        }
-        const float mu = m[0] == -INFINITY ? 0.f : m[0];
-        const float2 nm = make_float2(-mu, -mu);
-        float2 rs = make_float2(0.f, 0.f);
-        uint32_t pk[32];
+        const float m0 = shared_rows[r], m1 = shared_rows[256 + r], l0 = shared_rows[128 + r], l1 = shared_rows[384 + r];
+        const float top = fmaxf(m0, m1), mu = top == -INFINITY ? 0.f : top;
+        const float f0 = fast_exp2(m0 - mu), f1 = fast_exp2(m1 - mu);
+        const int64_t row = part + r;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < D / 64; ++q) {
+          const int col = (D / 2) * g + q * 32;
+          uint32_t y[32], z[32];
+          tmem_ld32(lanes + kColO + col, y);
+          if (n > 1) tmem_ld32(lanes + kGroupCols + kColO + col, z);  // (a single block was the first group's)
+          tmem_ld_wait();
+          tmem_pin(y);
+          tmem_pin(z);
+          if (r < tile_n) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + col);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 d = __fadd2_rn(make_float2(__uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1])), nm);
-            const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-            rs = __fadd2_rn(rs, w);
-            pk[q * 16 + e] = pack2<T>(w.x, w.y);
-          }
-        l[0] += rs.x + rs.y;
-        if (j >= 2) mbar_wait(&bar[P_FREE + bb], ((j - 2) >> 1) & 1, abort_flag, 62);
-        if (__any_sync(~0u, moved)) {
-          mbar_wait(&bar[P_FREE + (bb ^ 1)], ((j - 1) >> 1) & 1, abort_flag, 63);  // O of the block before
-          tc_fence_after();
-          const float g = moved ? f : 1.f;
+            for (int e = 0; e < 8; ++e) {
+              float v[4];
 #pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            const uint32_t col = lanes + kColO + (D / 2) * hf + q * 32;
-            uint32_t y[32];
-            tmem_ld32(col, y);
-            tmem_ld_wait();
-            tmem_pin(y);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * g);
-            tmem_st32(col, y);
-          }
-        }
-        tmem_st32(lanes + kColP + bb * 64 + 32 * hf, pk);
-        tmem_st_wait();
-        mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 64);
-        clear_behind();
-        tc_fence_before();
-        mbar_arrive(&bar[P_READY + bb]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[V_EMPTY + vst]);
-        if (last) {
-          // the tile's part: the row's sums from tensor memory
-          half_of_row[hf * 128 + r] = l[0];
-          named_barrier(2 + wq, 64);
-          const float sum = l[0] + half_of_row[(hf ^ 1) * 128 + r];
-          named_barrier(2 + wq, 64);
-          mbar_wait(&bar[P_FREE + bb], (j >> 1) & 1, abort_flag, 65);
-          tc_fence_after();
-          const int64_t row = at.part_row(c) + r;
-#pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            uint32_t y[32];
-            tmem_ld32(lanes + kColO + (D / 2) * hf + q * 32, y);
-            tmem_ld_wait();
-            tmem_pin(y);
-            if (r < tile_n) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + (D / 2) * hf + q * 32);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]),
-                                     __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
+              for (int i = 0; i < 4; ++i) {
+                v[i] = __uint_as_float(y[4 * e + i]) * f0;
+                if (n > 1) v[i] = fmaf(__uint_as_float(z[4 * e + i]), f1, v[i]);
+              }
+              dst[e] = make_float4(v[0], v[1], v[2], v[3]);
             }
           }
-          tc_fence_before();
-          if (hf == 0 && r < tile_n) a.part_ml[row] = make_float2(m[0], sum);
         }
-        ++j;
-        at.next(i + 1 < n);
-        if (++kst == kKStages) kst = 0, kphase ^= 1;
-        if (++vst == kVStages) vst = 0, vphase ^= 1;
-        continue;
-      }
-      if (first) {
-        // the rows of Q into shared memory (where wide tiles keep theirs)
-        for (int e = (int)threadIdx.x; e < 16 * (D / 8); e += 32 * kWarps) {
-          const int row = e / (D / 8), u = e % (D / 8), rr = at.tile * 16 + row;
+        tc_fence_before();
+        if (g == 0 && r < tile_n) a.part_ml[row] = make_float2(top, l0 * f0 + l1 * f1);
+        named_barrier(2 + wq, 64);  // (read before the next tile's are written, or O again)
+      } else {
+        // ---------------------------------------------------------- 16 rows: a warp 16 keys of every block, by itself
+        named_barrier(1, 32 * kWarps);  // a wide tile before it is done with the shared rows
+        const int r0 = lane >> 2, cc = (lane & 3) * 2, mi = lane >> 3, mr = lane & 7;
+        // the rows of Q into shared memory (where wide tiles keep theirs): held in registers they would cost 32
+        constexpr int kQLd = D * 2 + 16;  // bytes of a row: rows fall in different banks
+        for (int e = (int)threadIdx.x; e < kNarrow * (D / 8); e += 32 * kWarps) {
+          const int row = e / (D / 8), u = e % (D / 8), rr = at.tile * kNarrow + row;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (row < tile_n)
             x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(at.q0 + rr / G) * a.q_ld +
                                                 (int64_t)(at.h * G + rr % G) * D + u * 8);
-          *reinterpret_cast<uint4*>(sm + L::q + row * L::kQLd + u * 16) = x;
+          *reinterpret_cast<uint4*>(sm + L::q + row * kQLd + u * 16) = x;
         }
+        const uint32_t qbase = smem_u32(sm + L::q) + ((mi & 1) * 8 + mr) * kQLd + (mi >> 1) * 16;
+        float o[D / 8][4], m[2], l[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           m[half] = -INFINITY;
           l[half] = 0.f;
         }
 #pragma unroll
-        for (int t = 0; t < kOut; ++t)
+        for (int t = 0; t < D / 8; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
         named_barrier(1, 32 * kWarps);
-      }
-      // S of this warp's 16 keys
-      float s[2][4] = {};
-      mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 52);
-      {
-        const uint32_t kt = smem_u32(sm + L::k0 + kst * L::kTile);
-        const int key = warp * 16 + (mi >> 1) * 8 + mr;
+        const int key0 = warp * 16;
+        for (int t = 0; t < n; ++t, left -= kKeys) {
+          const int seen = left - key0;  // keys of the segment from this warp's first on
+          float s[2][4] = {};
+          mbar_wait(&bar[K_FULL + kst], kphase, abort_flag, 52);
+          if (seen > 0) {
+            const uint32_t kt = smem_u32(sm + L::k0 + kst * L::kTile);
+            const int key = key0 + (mi >> 1) * 8 + mr;
+            float s2[2][4] = {};  // a second chain of products
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int unit = (k & 3) * 2 + (mi & 1);  // 16 bytes of the row within its box
-          uint32_t b[4], qa[4];
-          ldsm4(qa, qbase + k * 32);
-          ldsm4(b, kt + (k >> 2) * L::kBox + key * 128 + ((unit ^ (key & 7)) << 4));
-          mma16816<T>(s[0], qa, b[0], b[1]);
-          mma16816<T>(s[1], qa, b[2], b[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[K_EMPTY + kst]);
-      float mx[2] = {-INFINITY, -INFINITY};
+            for (int k0 = 0; k0 < D / 16; k0 += 2) {
+              uint32_t qa[2][4], b[2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+              for (int k = 0; k < 2; ++k) {
+                ldsm4(qa[k], qbase + (k0 + k) * 32);
+                ldsm4(b[k], kt + ((k0 + k) >> 2) * L::kBox + key * 128 + (((((k0 + k) & 3) * 2 + (mi & 1)) ^ (key & 7)) << 4));
+              }
+              mma16816<T>(s[0], qa[0], b[0][0], b[0][1]);
+              mma16816<T>(s[1], qa[0], b[0][2], b[0][3]);
+              mma16816<T>(s2[0], qa[1], b[1][0], b[1][1]);
+              mma16816<T>(s2[1], qa[1], b[1][2], b[1][3]);
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = warp * 16 + t * 8 + cc + (e & 1);
-          s[t][e] = key < valid ? s[t][e] * a.scale_log2 : -INFINITY;
-          mx[e >> 1] = fmaxf(mx[e >> 1], s[t][e]);
-        }
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        mx[half] = fmaxf(mx[half], __shfl_xor_sync(~0u, mx[half], 1));
-        mx[half] = fmaxf(mx[half], __shfl_xor_sync(~0u, mx[half], 2));
-        if ((lane & 3) == 0) smax[warp * 16 + r0 + 8 * half] = mx[half];
-      }
-      named_barrier(1, 32 * kWarps);  // the maxima are there; the weights of the block before are used
-      float f[2], mu[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x = m[half];
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) x = fmaxf(x, smax[w * 16 + r0 + 8 * half]);
-        mu[half] = x == -INFINITY ? 0.f : x;
-        f[half] = fast_exp2(m[half] - mu[half]);
-        m[half] = x;
-        l[half] *= f[half];
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[t][e] = fast_exp2(s[t][e] - mu[e >> 1]);
-          l[e >> 1] += s[t][e];
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          *reinterpret_cast<uint32_t*>(sm + L::p + (r0 + 8 * half) * L::kPLd + (warp * 16 + t * 8 + cc) * 2) =
-              pack2<T>(s[t][2 * half], s[t][2 * half + 1]);
-      }
-#pragma unroll
-      for (int t = 0; t < kOut; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] *= f[e >> 1];
-      mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 53);
-      clear_behind();
-      named_barrier(1, 32 * kWarps);  // the weights are there
-      {
-        const uint32_t vt = smem_u32(sm + L::v0 + vst * L::kTile);
-        const uint32_t pt = pbase + ((mi & 1) * 8 + mr) * L::kPLd + (mi >> 1) * 16;
-        if constexpr (kOut == 2) {
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k) {
-            const int key = k * 16 + (mi & 1) * 8 + mr, unit = warp * 2 + (mi >> 1);  // 8 columns
-            uint32_t pa[4], b[4];
-            ldsm4(pa, pt + k * 32);
-            ldsm4t(b, vt + (unit >> 3) * L::kBox + key * 128 + (((unit & 7) ^ (key & 7)) << 4));
-            mma16816<T>(o[0], pa, b[0], b[1]);
-            mma16816<T>(o[1], pa, b[2], b[3]);
+              for (int e = 0; e < 4; ++e) s[t][e] = (s[t][e] + s2[t][e]) * a.scale_log2;
           }
-        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[K_EMPTY + kst]);
+          uint32_t pa[4];
+          if (seen > 0) {
+            if (seen < 16) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 32; ++k) {
-            const int key = k * 32 + mi * 8 + mr;
-            uint32_t pa[4], pb[4], b[4];
-            ldsm4(pa, pt + k * 64);
-            ldsm4(pb, pt + k * 64 + 32);
-            ldsm4t(b, vt + key * 128 + ((warp ^ (key & 7)) << 4));
-            mma16816<T>(o[0], pa, b[0], b[1]);
-            mma16816<T>(o[0], pb, b[2], b[3]);
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (t * 8 + cc + (e & 1) >= seen) s[t][e] = -INFINITY;
+            }
+            float f[2] = {1.f, 1.f};
+            bool moved = false;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (half * 8 >= tile_n) break;  // (rows that are not there: their scores are 0 or were cleared)
+              float x = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+              if (x > m[half] + kRescale) {
+                f[half] = fast_exp2(m[half] - x);  // 0 at the first keys
+                l[half] *= f[half];
+                m[half] = x;
+                moved = true;
+              }
+              const float mu = m[half] == -INFINITY ? 0.f : m[half];
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  s[t][2 * half + e] = fast_exp2(s[t][2 * half + e] - mu);
+                  l[half] += s[t][2 * half + e];
+                }
+            }
+            if (__any_sync(~0u, moved)) {
+#pragma unroll
+              for (int t = 0; t < D / 8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][e] *= f[e >> 1];
+            }
+            pa[0] = pack2<T>(s[0][0], s[0][1]);
+            pa[1] = pack2<T>(s[0][2], s[0][3]);
+            pa[2] = pack2<T>(s[1][0], s[1][1]);
+            pa[3] = pack2<T>(s[1][2], s[1][3]);
           }
+          mbar_wait(&bar[V_FULL + vst], vphase, abort_flag, 53);
+          if (seen > 0) {
+            if (seen < 16) clear_rows(sm + L::v0 + vst * L::kTile, key0 + seen, key0 + 16, lane, 32);
+            __syncwarp();
+            const uint32_t vt = smem_u32(sm + L::v0 + vst * L::kTile);
+            const int key = key0 + (mi & 1) * 8 + mr;
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) {
+              const int unit = 2 * u + (mi >> 1);  // 8 columns
+              uint32_t b[4];
+              ldsm4t(b, vt + (unit >> 3) * L::kBox + key * 128 + (((unit & 7) ^ (key & 7)) << 4));
+              mma16816<T>(o[2 * u], pa, b[0], b[1]);
+              mma16816<T>(o[2 * u + 1], pa, b[2], b[3]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[V_EMPTY + vst]);
+          if (++kst == kKStages) kst = 0, kphase ^= 1;
+          if (++vst == kVStages) vst = 0, vphase ^= 1;
         }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[V_EMPTY + vst]);
-      if (last) {
-        // the tile's part: every warp its columns of the sums, the first 16 threads maxima and sums of weights
-        const int64_t row = at.part_row(c);
+        // The tile's part: the warps' sums are joined, eight rows at a time, in shared memory (where wide tiles keep their
+        // Q), with the columns of a row turned so that rows fall in different banks.
+        float* stage = reinterpret_cast<float*>(sm + L::q);          // [kWarps][8][D]
+        float* max_of = reinterpret_cast<float*>(sm + L::rows);      // [kWarps][16]
+        float* sum_of = max_of + kWarps * 16;
+        named_barrier(1, 32 * kWarps);  // no warp reads Q any more
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int r = r0 + 8 * half;
+          if (half * 8 >= tile_n) break;
           l[half] += __shfl_xor_sync(~0u, l[half], 1);
           l[half] += __shfl_xor_sync(~0u, l[half], 2);
           if ((lane & 3) == 0) {
-            ssum[warp * 16 + r] = l[half];
-            if (warp == 0) srow[r] = m[half];
+            max_of[warp * 16 + r0 + 8 * half] = m[half];
+            sum_of[warp * 16 + r0 + 8 * half] = l[half];
           }
-          if (r < tile_n)
 #pragma unroll
-            for (int t = 0; t < kOut; ++t)
-              *reinterpret_cast<float2*>(a.part_o + (row + r) * D + warp * kCols + t * 8 + cc) =
-                  make_float2(o[t][2 * half], o[t][2 * half + 1]);
-        }
-        named_barrier(1, 32 * kWarps);
-        if (threadIdx.x < 16 && (int)threadIdx.x < tile_n) {
-          float x = 0.f;
-          for (int w = 0; w < kWarps; ++w) x += ssum[w * 16 + threadIdx.x];
-          a.part_ml[row + threadIdx.x] = make_float2(srow[threadIdx.x], x);
+          for (int t = 0; t < D / 8; ++t)
+            *reinterpret_cast<float2*>(stage + (warp * 8 + r0) * D + ((t * 8 + cc) ^ (r0 * 8))) =
+                make_float2(o[t][2 * half], o[t][2 * half + 1]);
+          named_barrier(1, 32 * kWarps);
+          const int r = half * 8 + warp;  // this warp's row
+          if (r < tile_n) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, max_of[w * 16 + r]);
+            const float mu = top == -INFINITY ? 0.f : top;
+            constexpr int kE = D / 32;  // columns of a lane
+            float acc[kE] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float g = fast_exp2(max_of[w * 16 + r] - mu);
+              sum = fmaf(g, sum_of[w * 16 + r], sum);
+              const float* src = stage + (w * 8 + warp) * D + ((lane * kE) ^ (warp * 8));
+#pragma unroll
+              for (int e = 0; e < kE; ++e) acc[e] = fmaf(g, src[e], acc[e]);
+            }
+            float* dst = a.part_o + (part + r) * D + lane * kE;
+            if constexpr (kE == 4)
+              *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            else
+              *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+            if (lane == 0) a.part_ml[part + r] = make_float2(top, sum);
+          }
+          named_barrier(1, 32 * kWarps);  // read before it is written again
         }
       }
-      at.next(i + 1 < n);
-      if (++kst == kKStages) kst = 0, kphase ^= 1;
-      if (++vst == kVStages) vst = 0, vphase ^= 1;
+      at.pass(n);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarps + 1) {
+  if (warp == kIssue) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmemCols);
   }
@@ -794,15 +886,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
       for (int e = 0; e < found; ++e) {
         const int4 x = segs[2 * list[e]], y = segs[2 * list[e] + 1];
         const int nb = (x.y + kKeys - 1) / kKeys, r = (b - x.z) * G + (hq - h * G), tile = r / y.z;
-        const int first = y.x + (h * y.y + tile) * nb;  // the tile's first block
-        const int c0 = first / quota, c1 = (first + nb - 1) / quota;
+        const int cost = block_cost(y.z), start = start_cost(y.z);
+        const int first = y.x + (h * y.y + tile) * (nb * cost + start) + start;  // place of the tile's first block
+        const int c0 = first / quota, c1 = (first + (nb - 1) * cost) / quota;
         for (int c = c0; c <= c1; c += 32) {
           if (kept + 32 > kJoinParts) {
             take(kept);
             kept = 0;
           }
-          if (c + lane <= c1) rows[warp][kept + lane] = y.w + h * x.w * G + r + (c + lane) * kMostRows;
-          kept += min(32, c1 - c + 1);
+          // whether a block's place begins in the run of CTA c + lane
+          const int64_t run = (int64_t)(c + lane) * quota;
+          const int64_t blk = run <= first ? 0 : (run - first + cost - 1) / cost;
+          const bool has = c + lane <= c1 && blk < nb && first + blk * cost < run + quota;
+          const uint32_t with = __ballot_sync(~0u, has);
+          if (has) rows[warp][kept + __popc(with & ((1u << lane) - 1))] = y.w + h * x.w * G + r + (c + lane) * kMostRows;
+          kept += __popc(with);
         }
       }
     __syncthreads();
@@ -830,8 +928,8 @@ template <typename T, int D>
 int launch_decode(const DecodeArgs& a, const void* k, const void* v, int64_t kv_ld, cudaStream_t st) {
   const uint64_t rows = std::max<int64_t>(a.rows, 1);
   CUtensorMap mk, mv;
-  if (!make_tmap_bf16_ld(&mk, k, (uint64_t)a.Hkv * D, rows, kv_ld, kKeys) ||
-      !make_tmap_bf16_ld(&mv, v, (uint64_t)a.Hkv * D, rows, kv_ld, kKeys))
+  if (!make_tmap_bf16_ld(&mk, k, (uint64_t)a.Hkv * D, rows, kv_ld, kPiece) ||
+      !make_tmap_bf16_ld(&mv, v, (uint64_t)a.Hkv * D, rows, kv_ld, kPiece))
     return TT_ERR_CUDA;
   const int smem = (int)Smem<D>::total;
   if (!smem_attr_set<decode_kernel<T, D>>(smem)) return TT_ERR_CUDA;
@@ -866,7 +964,7 @@ TT_API int tt_tree_decode_plan(const int32_t* kv_begin, const int32_t* kv_len, c
   if ((S && (!kv_begin || !kv_len || !q_begin || !q_end)) || !plan || !aligned16(plan) || !err) return TT_ERR_INVALID_ARG;
   if (plan_bytes < tt_tree_decode_plan_bytes(S)) return TT_ERR_WORKSPACE;
   const PlanArgs a = {kv_begin, kv_len, q_begin, q_end, S, B, Hq, Hkv, d, ctas(), rows, pairs, plan, err};
-  decode_plan_kernel<<<1, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  decode_plan_kernel<<<1, S <= 256 ? 256 : kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
@@ -890,7 +988,9 @@ TT_API int tt_tree_decode_attn(const void* plan, const void* Q, int64_t q_ld, co
     return TT_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
   if (ws_bytes < tt_tree_decode_attn_workspace_bytes(pairs, Hq, d)) return TT_ERR_WORKSPACE;
-  DecodeArgs a = {plan, Q, q_ld, B, Hq, Hkv, S, ctas(), rows, pairs, scale * kLog2e, nullptr, nullptr, O, LSE, err};
+  // (a scale of 0 times a masked score of -inf would not be -inf; one of 1e-30 makes equal weights as well)
+  const float scale_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;
+  DecodeArgs a = {plan, Q, q_ld, B, Hq, Hkv, S, ctas(), rows, pairs, scale_log2, nullptr, nullptr, O, LSE, err};
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(pairs, Hq) * d);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

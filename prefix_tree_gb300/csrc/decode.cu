@@ -318,17 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
-  int e = plan_error(a, D);
-  if (smem_u32(sm) & 1023) e = TT_ERR_UNSUPPORTED;  // (the layout of the tiles rests on it)
-  if (e) {
-    if (threadIdx.x == 0) set_err(a.err, e);
-    return;
-  }
-  const int c = blockIdx.x;
-  const int64_t w0 = (int64_t)c * hdr->quota;
-  if (w0 >= hdr->cost) return;
-  const int w1 = (int)min((int64_t)hdr->cost, w0 + hdr->quota);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&bar[K_FULL + i], 1);
@@ -348,11 +337,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  wait_prerequisites();  // the kernels before this one: the plan, Q, K and V, and tensor memory that they may hold
+  launch_dependents();   // the joining kernel may be placed as CTAs finish
   if (warp == kIssue) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
+  int e = plan_error(a, D);
+  if (smem_u32(sm) & 1023) e = TT_ERR_UNSUPPORTED;  // (the layout of the tiles rests on it)
+  if (e && threadIdx.x == 0) set_err(a.err, e);
+  const int c = blockIdx.x;
+  const int64_t w0 = e ? 0 : (int64_t)c * hdr->quota, cost = e ? 0 : hdr->cost;
+  if (w0 >= cost) {  // nothing for this CTA
+    __syncthreads();
+    if (warp == kIssue) tmem_dealloc(tbase, kTmemCols);
+    return;
+  }
+  const int w1 = (int)min(cost, w0 + hdr->quota);
   const int G = a.Hq / a.Hkv;
   const int4* segs = reinterpret_cast<const int4*>(static_cast<const char*>(a.plan) + kPlanSegs);
   Walk at(segs, a.Hkv, G, reinterpret_cast<const int32_t*>(static_cast<const char*>(a.plan) + kPlanCtas)[c], (int)w0, w1);
@@ -814,7 +817,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   __shared__ int rows[kJoinWarps][kJoinParts];
   __shared__ float weights[kJoinWarps][kJoinParts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  launch_dependents();  // the next layer's kernel may set itself up; it waits for this one
+  wait_prerequisites();
   if (plan_error(a, D)) return;
   const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
   const int4* segs = reinterpret_cast<const int4*>(static_cast<const char*>(a.plan) + kPlanSegs);
@@ -933,18 +937,28 @@ int launch_decode(const DecodeArgs& a, const void* k, const void* v, int64_t kv_
     return TT_ERR_CUDA;
   const int smem = (int)Smem<D>::total;
   if (!smem_attr_set<decode_kernel<T, D>>(smem)) return TT_ERR_CUDA;
-  decode_kernel<T, D><<<a.ctas, kThreads, smem, st>>>(mk, mv, a);
-  if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.B, (a.Hq + kJoinWarps - 1) / kJoinWarps);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = st;
+  // Both as programmatic dependents: the first sets itself up while the kernel before it in the stream ends, the second
+  // while the first's last CTAs work; each waits for its predecessors before it reads anything that they write.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D>, a));
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  if (cudaLaunchKernelEx(&cfg, decode_kernel<T, D>, mk, mv, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return TT_ERR_CUDA;
+  }
+  cfg.gridDim = dim3(a.B, (a.Hq + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D>, a);
+  (void)cudaGetLastError();
+  return cuda_status(err);
 }
 
 }  // namespace

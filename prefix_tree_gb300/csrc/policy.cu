@@ -155,6 +155,7 @@ template <bool VEC>
 __global__ void __launch_bounds__(kTokenThreads) policy_tokens_kernel(const LogpArgs a) {
   __shared__ Sums room[kTokenThreads / 32];
   __shared__ Sums of_ctas[kOneLaunch];
+  launch_dependents();
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
   Sums s = {};
   auto get = [&](const float* p, float (&v)[kPerThread], int64_t t, bool whole) {
@@ -233,7 +234,7 @@ constexpr int kSumThreads = 1024;
 template <bool ROWS>
 __global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const void* parts, int64_t n, const Policy c, float* sums) {
   __shared__ Sums room[kSumThreads / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_prerequisites();
   Sums s = {};
   constexpr int kLoads = 8;  // of a thread under way together
   for (int64_t i = threadIdx.x; ROWS && i < n; i += kLoads * kSumThreads) {
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_ker
   const int tid = WARPS == 1 ? lane : (int)threadIdx.x;
   const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kGroups<WARPS> + group : (int64_t)(blockIdx.x >> log_CL);
   const int rank = kCluster ? (int)blockIdx.x & (CL - 1) : 0;
+  launch_dependents();
   if (row >= a.N) return;  // (groups of one warp only)
   if (kCluster && CL > 1) {
     if (tid == 0) {

@@ -286,13 +286,6 @@ __device__ __forceinline__ F2 log_pair(float s) {
   return l;
 }
 
-// Stores v at the same place of CTA `rank` of the cluster; its barrier counts the bytes.
-__device__ __forceinline__ void send(float4* place, float4 v, uint64_t* bar, uint32_t rank) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                   tc::dsmem_addr(smem_u32(place), rank)),
-               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(tc::dsmem_addr(smem_u32(bar), rank))
-               : "memory");
-}
 // What every thread needs of its row.
 struct RowOf {
   float m, log_s;
@@ -301,7 +294,7 @@ struct RowOf {
 };
 
 constexpr int kBatch = 4;   // vectors of a thread at once: one rescaling for all of them
-constexpr int kAhead = 4;   // batches on their way beside the one in use
+constexpr int kAhead = 2;   // batches on their way beside the one in use
 constexpr int kCtasMost = 8;
 template <int WARPS>
 constexpr int kGroups = WARPS == 1 ? 4 : 1;  // groups of a block: each takes rows of its own
@@ -444,37 +437,30 @@ __device__ __forceinline__ void add_vectors(Stat& t, const uint4 (&u)[N]) {
   t.u += q.x + q.y;
 }
 
-// A row is taken by a group of WARPS warps of each of the CL CTAs of a cluster (CL a power of two; 1 for WARPS < 4).
+// Blocks to an SM that the registers are held to: left alone the compiler takes 90 (a tree's rows 1200 -> 1470 us).
+template <int WARPS, bool CLUSTER>
+constexpr int kMinBlocks = WARPS == 8 ? (CLUSTER ? 4 : 6) : WARPS == 2 ? 20 : 10;
+
+// A row is taken by a group of WARPS warps, or (CLUSTER) of eight warps of each of the CL CTAs of a cluster, CL a power of two.
 // `room`: vectors of a group's slice in shared memory; a thread copies, sums and turns its own vectors, so that the
 // copies need no barrier. The sums are joined and the row's scalars formed by one warp of every CTA.
-template <typename T, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_kernel(const LogitsArgs a, int CL, int log_CL,
-                                                                                    int room) {
+template <typename T, int WARPS, bool CLUSTER>
+__global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>, kMinBlocks<WARPS, CLUSTER>)
+    policy_logits_kernel(const LogitsArgs a, int CL, int log_CL, int room) {
   constexpr int VN = Row<T>::VN, kGroup = 32 * WARPS;
-  constexpr bool kCluster = WARPS >= 4;
   extern __shared__ __align__(16) uint4 slices[];
   __shared__ Stat part[WARPS];
   __shared__ __align__(16) float4 of_ctas[kCtasMost];  // (m, s, u) of the slice, the target's logit where it lies there
-  __shared__ __align__(8) uint64_t arrived;
-  __shared__ int gave_up;
   __shared__ float zy_shared;
   __shared__ RowOf row_shared;
   const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : (int)threadIdx.x >> 5;
   const int group = WARPS == 1 ? (int)threadIdx.x >> 5 : 0;
   const int tid = WARPS == 1 ? lane : (int)threadIdx.x;
   const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kGroups<WARPS> + group : (int64_t)(blockIdx.x >> log_CL);
-  const int rank = kCluster ? (int)blockIdx.x & (CL - 1) : 0;
+  const int rank = CLUSTER ? (int)blockIdx.x & (CL - 1) : 0;
   launch_dependents();
   if (row >= a.N) return;  // (groups of one warp only)
-  if (kCluster && CL > 1) {
-    if (tid == 0) {
-      tc::mbar_init(&arrived, 1);
-      gave_up = 0;
-      tc::fence_barrier_init();
-      tc::mbar_expect_tx(&arrived, (uint32_t)CL * 16);
-    }
-    cg::this_cluster().barrier_arrive();  // waited for before the CTAs write to one another
-  }
+  if (CLUSTER) cg::this_cluster().barrier_arrive();  // waited for before the CTAs write to one another
   const float w = a.in.weights ? a.in.weights[row] : 1.f;
   const Row<T> z(static_cast<const T*>(a.z) + row * a.ld, a.V);
   T* out = static_cast<T*>(a.dz) + row * a.ld;
@@ -494,16 +480,6 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_ker
     else
       put_ends(j, u);
   };
-  if (w == 0.f) {  // a masked row: its logits are not read
-    if (a.dz)
-      for (int j = lo + tid; j < hi; j += kGroup) put(j, make_uint4(0, 0, 0, 0));
-    if (rank == 0 && tid == 0) {
-      a.logp[row] = a.entropy[row] = 0.f;
-      a.rows[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    if (kCluster && CL > 1) cg::this_cluster().barrier_wait();
-    return;
-  }
   uint4* buf = slices + group * room - lo;  // buf[j]: vector j
   const int y = a.y[row];
   const bool y_ok = y >= 0 && y < z.V;
@@ -529,6 +505,17 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_ker
   };
 #pragma unroll
   for (int b = 0; b < kAhead; ++b) fetch(lo + tid + b * kBatch * kGroup);
+  if (w == 0.f) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // a masked row: its logits are not read
+    if (a.dz)
+      for (int j = lo + tid; j < hi; j += kGroup) put(j, make_uint4(0, 0, 0, 0));
+    if (rank == 0 && tid == 0) {
+      a.logp[row] = a.entropy[row] = 0.f;
+      a.rows[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (CLUSTER) cg::this_cluster().barrier_wait();
+    return;
+  }
   RowInputs in = {};
   if (warp == 0) in = inputs_of(a.in, row, w);
   Stat t = {-INFINITY, 0.f, 0.f};
@@ -571,18 +558,19 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>) policy_logits_ker
       t = lane < WARPS ? part[lane] : Stat{-INFINITY, 0.f, 0.f};
       t = sum_stats(t);
     }
-    if (kCluster && CL > 1) {
-      cg::this_cluster().barrier_wait();  // every CTA has started, its barrier is set up
+    if (CLUSTER) {
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.barrier_wait();  // every CTA has started
+      if (warp == 0 && lane < CL)
+        *cluster.map_shared_rank(&of_ctas[rank], lane) = make_float4(t.m, t.s, t.u, here ? zy_shared : 0.f);
+      cluster.sync();
       if (warp == 0) {
-        // lane r tells CTA r; what the CTAs tell this one arrives with its barrier
-        if (lane < CL) send(&of_ctas[rank], make_float4(t.m, t.s, t.u, here ? zy_shared : 0.f), &arrived, lane);
-        if (!tc::mbar_wait(&arrived, 0, &gave_up, 70) && lane == 0) set_err(a.err, TT_ERR_TIMEOUT);
         const float4 f = lane < CL ? of_ctas[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         t = sum_stats({f.x, f.y, f.z});
       }
     }
     if (warp == 0) {
-      const float target = kCluster && CL > 1 ? of_ctas[y_ok ? jy / per : 0].w : zy_shared;
+      const float target = CLUSTER ? of_ctas[y_ok ? jy / per : 0].w : zy_shared;
       const RowOf mine_too = row_of<T>(a, row, in, t, target, y_ok, rank == 0 && lane == 0);
       if (lane == 0) row_shared = mine_too;
     }
@@ -645,34 +633,34 @@ int launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, int CL, b
 // Most shared memory of a CTA for its slice: what is left of 227 KB beside the static part.
 constexpr int kSliceMost = 224 * 1024;
 
-template <typename T, int WARPS>
+template <typename T, int WARPS, bool CLUSTER>
 int launch_rows(const LogitsArgs& a, int log_CL, cudaStream_t st) {
   const int CL = 1 << log_CL, nvec = (int)(a.V / Row<T>::VN + 2);
   const int room = (nvec + CL - 1) / CL;
   const size_t smem = (size_t)room * 16 * kGroups<WARPS>;
   if (smem > kSliceMost) return TT_ERR_UNSUPPORTED;
-  if (smem > 48 * 1024 && !tc::smem_attr_set<policy_logits_kernel<T, WARPS>>(kSliceMost)) return TT_ERR_CUDA;
-  return launch(policy_logits_kernel<T, WARPS>, (a.N + kGroups<WARPS> - 1) / kGroups<WARPS> * CL,
+  if (smem > 48 * 1024 && !tc::smem_attr_set<policy_logits_kernel<T, WARPS, CLUSTER>>(kSliceMost)) return TT_ERR_CUDA;
+  return launch(policy_logits_kernel<T, WARPS, CLUSTER>, (a.N + kGroups<WARPS> - 1) / kGroups<WARPS> * CL,
                 32 * WARPS * kGroups<WARPS>, smem, CL, false, st, a, CL, log_CL, room);
 }
 
-#ifndef TT_PL_VEC
-#define TT_PL_VEC 5120
-#endif
-#ifndef TT_PL_W
-#define TT_PL_W 8
-#endif
+// How rows are taken: by a warp or two each while they are short and many, by a CTA of eight warps, or by 2, 4 or 8 CTAs. A
+// slice of up to 80 KB leaves two CTAs and more to an SM, one's copies under way during another's joins. Few rows are cut
+// further while every slice finds an SM of its own. Measured, us for the choice and the next one (bf16):
+//   20,000 x 1000: warp 29, two warps 41;        20,000 x 8000: two warps 108, four 156;
+//   20,000 x 16,000: one CTA 201, two 245;       12,669 x 151,936 (16 % masked): 4 CTAs 1200, 8 CTAs 1348, 1 persistent CTA
+//   to an SM with part of the row read again 1440, persistent clusters that copy the next row ahead 1590.
+constexpr int64_t kSliceVectors = 5120;
 template <typename T>
 int launch_logits(const LogitsArgs& a, cudaStream_t st) {
   const int64_t nvec = a.V / Row<T>::VN + 1, sms = sm_count();
-  if (nvec <= 512 && a.N >= 8 * sms) return launch_rows<T, 1>(a, 0, st);
-  if (nvec <= 1024 && a.N >= 8 * sms) return launch_rows<T, 2>(a, 0, st);
+  if (nvec <= 512 && a.N >= 8 * sms) return launch_rows<T, 1, false>(a, 0, st);
+  if (nvec <= 1024 && a.N >= 8 * sms) return launch_rows<T, 2, false>(a, 0, st);
   int log_CL = 0;
-  while (log_CL < 3 && (nvec > ((int64_t)TT_PL_VEC << log_CL) || (2 * a.N << log_CL) <= 4 * sms && nvec >= (int64_t)512 << log_CL))
+  while (log_CL < 3 &&
+         (nvec > kSliceVectors << log_CL || ((2 * a.N << log_CL) <= 4 * sms && nvec >= (int64_t)512 << log_CL)))
     ++log_CL;
-  if (TT_PL_W == 4 && (a.N << log_CL) >= 4 * sms) return launch_rows<T, 4>(a, log_CL, st);
-  if (TT_PL_W == 16) return launch_rows<T, 16>(a, log_CL, st);
-  return launch_rows<T, 8>(a, log_CL, st);
+  return log_CL ? launch_rows<T, 8, true>(a, log_CL, st) : launch_rows<T, 8, false>(a, 0, st);
 }
 
 }  // namespace

@@ -111,9 +111,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Lets a kernel that was launched as a programmatic dependent of this one be placed once every CTA of this grid has come
-// here: its launch and prologue overlap with this grid's work. It waits (wait_prerequisites) before it reads results.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Until the grids that this one depends on have finished and their writes are visible (returns at once otherwise).
 __device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

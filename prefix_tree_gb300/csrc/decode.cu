@@ -338,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   wait_prerequisites();  // the kernels before this one: the plan, Q, K and V, and tensor memory that they may hold
-  launch_dependents();   // the joining kernel may be placed as CTAs finish
   if (warp == kIssue) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -813,15 +812,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinWarps = 8, kJoinChunk = 32 * kJoinWarps, kJoinParts = 64;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const DecodeArgs a) {
-  __shared__ int list[kJoinChunk], counts[kJoinWarps];
+  __shared__ int4 list[kJoinChunk][2];
+  __shared__ int counts[kJoinWarps];
   __shared__ int rows[kJoinWarps][kJoinParts];
   __shared__ float weights[kJoinWarps][kJoinParts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  launch_dependents();  // the next layer's kernel may set itself up; it waits for this one
   wait_prerequisites();
-  if (plan_error(a, D)) return;
   const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
   const int4* segs = reinterpret_cast<const int4*>(static_cast<const char*>(a.plan) + kPlanSegs);
+  // (the first segments together with the header that says how many there are: the plan has room for all S)
+  int4 x = make_int4(0, 0, 0, 0), y = x;
+  if ((int)threadIdx.x < a.S) x = segs[2 * threadIdx.x], y = segs[2 * threadIdx.x + 1];
+  if (plan_error(a, D)) return;
   const int b = blockIdx.x, hq = blockIdx.y * kJoinWarps + warp, G = a.Hq / a.Hkv, h = hq / G, quota = hdr->quota;
   constexpr int kE = D / 32;  // columns of a lane
   float M = -INFINITY, Ls = 0.f, acc[kE] = {};
@@ -871,11 +873,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   for (int s0 = 0; s0 < hdr->segments; s0 += kJoinChunk) {
     // the chunk's segments with this query, in order
     const int s = s0 + (int)threadIdx.x;
-    bool on = false;
-    if (s < hdr->segments) {
-      const int4 x = segs[2 * s];
-      on = b >= x.z && b < x.z + x.w;
-    }
+    if (s0 && s < hdr->segments) x = segs[2 * s], y = segs[2 * s + 1];
+    const bool on = s < hdr->segments && b >= x.z && b < x.z + x.w;
     const uint32_t ballot = __ballot_sync(~0u, on);
     if (lane == 0) counts[warp] = __popc(ballot);
     __syncthreads();
@@ -884,11 +883,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
       if (w == warp) before = found;
       found += counts[w];
     }
-    if (on) list[before + __popc(ballot & ((1u << lane) - 1))] = s;
+    if (on) {
+      const int at = before + __popc(ballot & ((1u << lane) - 1));
+      list[at][0] = x;
+      list[at][1] = y;
+    }
     __syncthreads();
     if (hq < a.Hq)
       for (int e = 0; e < found; ++e) {
-        const int4 x = segs[2 * list[e]], y = segs[2 * list[e] + 1];
+        const int4 x = list[e][0], y = list[e][1];
         const int nb = (x.y + kKeys - 1) / kKeys, r = (b - x.z) * G + (hq - h * G), tile = r / y.z;
         const int cost = block_cost(y.z), start = start_cost(y.z);
         const int first = y.x + (h * y.y + tile) * (nb * cost + start) + start;  // place of the tile's first block
@@ -937,8 +940,9 @@ int launch_decode(const DecodeArgs& a, const void* k, const void* v, int64_t kv_
     return TT_ERR_CUDA;
   const int smem = (int)Smem<D>::total;
   if (!smem_attr_set<decode_kernel<T, D>>(smem)) return TT_ERR_CUDA;
-  // Both as programmatic dependents: the first sets itself up while the kernel before it in the stream ends, the second
-  // while the first's last CTAs work; each waits for its predecessors before it reads anything that they write.
+  // Both as programmatic dependents: their launches are prepared while the kernel before runs, and each waits for its
+  // predecessors before it reads anything. (Neither lets its own dependents be placed early: CTAs of the joining kernel that
+  // wait on SMs took 3 % longer.)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

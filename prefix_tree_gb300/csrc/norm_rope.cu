@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? (BWD ? 2 : 3) : 1)
       o2[i] = here[i] ? o1[i] + VEC : 0;
     }
   }
-  if (BWD) launch_dependents();
   load_weights<T>(a, weights);
   float2 acc[NV][2][P];
 #pragma unroll
@@ -392,7 +391,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
     o1[i] = !rotated ? 2 * p : a.adjacent ? 2 * p : p;
     o2[i] = !rotated ? 2 * p + 1 : a.adjacent ? 2 * p + 1 : p + a.half;
   }
-  if (BWD) launch_dependents();
   load_weights<T>(a, weights);
   float acc[NV][2] = {};
   for (int64_t t0 = (int64_t)role.block * tokens; t0 < a.N; t0 += (int64_t)role.blocks * tokens) {

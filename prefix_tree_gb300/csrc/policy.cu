@@ -155,7 +155,6 @@ template <bool VEC>
 __global__ void __launch_bounds__(kTokenThreads) policy_tokens_kernel(const LogpArgs a) {
   __shared__ Sums room[kTokenThreads / 32];
   __shared__ Sums of_ctas[kOneLaunch];
-  launch_dependents();
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
   Sums s = {};
   auto get = [&](const float* p, float (&v)[kPerThread], int64_t t, bool whole) {
@@ -458,7 +457,6 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>, kMinBlocks<WARPS,
   const int tid = WARPS == 1 ? lane : (int)threadIdx.x;
   const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kGroups<WARPS> + group : (int64_t)(blockIdx.x >> log_CL);
   const int rank = CLUSTER ? (int)blockIdx.x & (CL - 1) : 0;
-  launch_dependents();
   if (row >= a.N) return;  // (groups of one warp only)
   if (CLUSTER) cg::this_cluster().barrier_arrive();  // waited for before the CTAs write to one another
   const float w = a.in.weights ? a.in.weights[row] : 1.f;

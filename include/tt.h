@@ -155,8 +155,8 @@ TT_API int tt_rope(const void* q, void* q_out, int64_t q_ld, int64_t q_out_ld, c
  * q, k, their outputs and strides, pos, axes, tables and adjacent as in
  * tt_rope; rot = 0: the norm alone (pos and the tables may be NULL). An
  * output may be its own input (same stride), not another tensor's.
- * Sums are fp32: a head's sum of squares has to stay below 3e38. A head of
- * zeros gives zeros with eps > 0 (NaN with eps = 0).
+ * Sums are fp32: a head's mean of squares, and eps with it, has to lie between
+ * 1e-37 and 1e38/d. A head of zeros gives zeros with eps > 0 (NaN with 0).
  * Limits (TT_ERR_UNSUPPORTED): d and rot even, d <= 512, rot <= 256, at most 4
  * axes and 1024 heads each. N = 0 does nothing. 16-byte accesses under the
  * rule of tt_rope; results of both kinds of access agree to fp32 rounding of
@@ -251,7 +251,10 @@ TT_API int tt_tree_attn_bwd(const void* ws, const tt_bf16* Q, const tt_bf16* K, 
  * `err` = TT_ERR_INVALID_ARG, pairs that are too few TT_ERR_WORKSPACE; attention
  * calls given this plan set the same error and write nothing. In a captured
  * graph the arrays are read again at every replay.
- * Limits (TT_ERR_UNSUPPORTED): d 64 or 128, Hq % Hkv = 0, Hq <= 1024, B <= 2^20. */
+ * Limits (TT_ERR_UNSUPPORTED): d 64 or 128, Hq % Hkv = 0, Hq <= 1024, B <=
+ * 2^20; (TT_ERR_INVALID_ARG): S < 2^24, rows < 2^30; and, found on the device
+ * (`err` = TT_ERR_UNSUPPORTED), about 2^30 units of work: 4 for every 128 keys
+ * of a segment, key head and 128 rows of its queries, 12 for the 128 rows. */
 TT_API size_t tt_tree_decode_plan_bytes(int32_t S);
 TT_API int tt_tree_decode_plan(const int32_t* kv_begin, const int32_t* kv_len, const int32_t* q_begin,
                                const int32_t* q_end, int32_t S, int32_t B, int64_t rows, int64_t pairs, int Hq, int Hkv,
@@ -591,8 +594,8 @@ TT_API int tt_policy_loss(const float* logp, const float* entropy, const float* 
  *   dz_v = p_v·(−dlogp − dentropy·(log p_v + entropy)) + dlogp·[v = y].
  * logp, entropy: fp32 [N], written. dlogits: type and ld of logits, NULL = not
  * wanted; it may be logits itself; columns from V on are left as they are.
- * A masked row (weight 0) is not read: its logp and entropy are 0 and its
- * dlogits zeros. A target outside [0, V) (of a row that is not masked) sets
+ * A masked row (weight 0) is not regarded, whatever its logits and target
+ * hold: its logp and entropy are 0 and its dlogits zeros. A target outside [0, V) (of a row that is not masked) sets
  * `err` = TT_ERR_INVALID_ARG, the row's logp (hence the loss) is NaN and its
  * dlogits zeros. Masked logits (−inf), rows with nothing but −inf (logp = −inf,
  * entropy 0, dlogits zeros) and rows with a NaN or +inf (NaN) as in

@@ -989,8 +989,8 @@ def policy_loss_logits(logits, targets, old_logp, adv, adv_neg=None, ref_logp=No
                        err=None):
     """Clipped policy objective from logits [N,V] (bf16, fp16 or fp32; rows may be padded) with the gradient with respect
     to them, in one read (tt_policy_loss_logits): (sums, logp, entropy, dlogits). Arguments as in policy_loss; `out` =
-    (sums, logp, entropy, dlogits), whose dlogits may be logits itself. A masked row (weight 0) is not read: its logp,
-    entropy and dlogits are 0."""
+    (sums, logp, entropy, dlogits), whose dlogits may be logits itself. A masked row (weight 0) is not regarded: its
+    logp, entropy and dlogits are 0."""
     N, V, ld = _logit_rows(logits, "logits")
     rows, dev = (N,), logits.device
     _per_row(targets, torch.int32, "targets", rows, True)

@@ -34,6 +34,7 @@ constexpr int kKeys = 128;       // keys of a block
 constexpr int kMostRows = 128;   // rows of a wide tile
 constexpr int kNarrow = 16;      // and of a narrow one
 constexpr int kMostCtas = 1024;
+constexpr int kMostSegs = (1 << 24) - 1;
 constexpr int kPiece = 32;       // rows of a copy
 // Work is shared out by cost: of a block, and of a tile's start (its queries have to be fetched first and its sums
 // written last).
@@ -120,12 +121,17 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const PlanArg
   int64_t cost = 0, rows_n = 0;  // rows_n: partial rows << 24, and segments
   int4 x;
   int tiles, tile_rows;
+  // (a thread's sum is cut off where it is too large already, so that the block's cannot wrap; a partial row costs an eighth
+  // and more, so that the rows of a step that is not too large cannot either)
   for (int s = s0; s < s1; ++s)
-    if (const int64_t c = read(s, x, tiles, tile_rows)) cost += c, rows_n += ((int64_t)x.w * a.Hq << 24) + 1;
+    if (const int64_t c = read(s, x, tiles, tile_rows)) {
+      cost = min(cost + c, (int64_t)INT32_MAX);
+      rows_n += ((int64_t)x.w * a.Hq << 24) + 1;
+    }
   int64_t all_cost, all_rows_n;
   scan_block(cost, rows_n, all_cost, all_rows_n, room);
-  if (threadIdx.x == 0 && (all_rows_n >> 24) > a.pairs * a.Hq) atomicCAS(&code, 0, TT_ERR_WORKSPACE);
   if (threadIdx.x == 0 && all_cost > INT32_MAX / 2) atomicCAS(&code, 0, TT_ERR_UNSUPPORTED);
+  if (threadIdx.x == 0 && (all_rows_n >> 24) > a.pairs * a.Hq) atomicCAS(&code, 0, TT_ERR_WORKSPACE);
   __syncthreads();
   if (threadIdx.x == 0) {
     const int n = (int)(all_rows_n & 0xffffff);
@@ -914,16 +920,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   }
   if (hq >= a.Hq) return;
   take(kept);
-  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  const float inv = Ls != 0.f ? 1.f / Ls : 0.f;  // (a NaN stays one)
   T* o = static_cast<T*>(a.o) + ((int64_t)b * a.Hq + hq) * D + lane * kE;
 #pragma unroll
   for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) a.lse[(int64_t)hq * a.B + b] = Ls > 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[(int64_t)hq * a.B + b] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
 }
 
 int check_sizes(int32_t S, int32_t B, int64_t rows, int64_t pairs, int Hq, int Hkv, int d) {
   if (S < 0 || B < 0 || rows < 0 || pairs < 0 || Hq < 1 || Hkv < 1) return TT_ERR_INVALID_ARG;
-  if (rows > INT32_MAX / 2 || S > (1 << 24)) return TT_ERR_INVALID_ARG;
+  if (rows > INT32_MAX / 2 || S > kMostSegs) return TT_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || Hq % Hkv || Hq > 1024 || B > (1 << 20)) return TT_ERR_UNSUPPORTED;
   if (pairs > (INT32_MAX / 2) / Hq) return TT_ERR_INVALID_ARG;
   return TT_OK;
@@ -971,7 +977,7 @@ int launch_decode(const DecodeArgs& a, const void* k, const void* v, int64_t kv_
 using namespace tt;
 
 TT_API size_t tt_tree_decode_plan_bytes(int32_t S) {
-  return S < 0 || S > (1 << 24) ? 0 : kPlanSegs + (size_t)S * 2 * sizeof(int4);
+  return S < 0 || S > kMostSegs ? 0 : kPlanSegs + (size_t)S * 2 * sizeof(int4);
 }
 
 TT_API int tt_tree_decode_plan(const int32_t* kv_begin, const int32_t* kv_len, const int32_t* q_begin,
@@ -980,6 +986,9 @@ TT_API int tt_tree_decode_plan(const int32_t* kv_begin, const int32_t* kv_len, c
   const int rc = check_sizes(S, B, rows, pairs, Hq, Hkv, d);
   if (rc) return rc;
   if ((S && (!kv_begin || !kv_len || !q_begin || !q_end)) || !plan || !aligned16(plan) || !err) return TT_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(kv_begin) | reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(q_begin) |
+       reinterpret_cast<uintptr_t>(q_end)) % 4)
+    return TT_ERR_INVALID_ARG;
   if (plan_bytes < tt_tree_decode_plan_bytes(S)) return TT_ERR_WORKSPACE;
   const PlanArgs a = {kv_begin, kv_len, q_begin, q_end, S, B, Hq, Hkv, d, ctas(), rows, pairs, plan, err};
   decode_plan_kernel<<<1, S <= 256 ? 256 : kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
@@ -999,9 +1008,9 @@ TT_API int tt_tree_decode_attn(const void* plan, const void* Q, int64_t q_ld, co
   if (rc) return rc;
   if (dtype == TT_DT_F32) return TT_ERR_UNSUPPORTED;
   if (dtype != TT_DT_BF16 && dtype != TT_DT_F16) return TT_ERR_INVALID_ARG;
-  if (!plan || !aligned16(plan) || !err || !std::isfinite(scale)) return TT_ERR_INVALID_ARG;
+  if (!plan || !aligned16(plan) || !err || !std::isfinite(scale * kLog2e)) return TT_ERR_INVALID_ARG;
   if (B == 0) return TT_OK;
-  if (!Q || !aligned16(Q) || !O || !aligned16(O) || !LSE || q_ld < (int64_t)Hq * d || q_ld % 8) return TT_ERR_INVALID_ARG;
+  if (!Q || !aligned16(Q) || !O || !aligned16(O) || !LSE || reinterpret_cast<uintptr_t>(LSE) % 4 || q_ld < (int64_t)Hq * d || q_ld % 8) return TT_ERR_INVALID_ARG;
   if (rows && (!K || !V || !aligned16(K) || !aligned16(V) || kv_ld < (int64_t)Hkv * d || kv_ld % 8))
     return TT_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;

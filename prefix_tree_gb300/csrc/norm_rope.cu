@@ -62,6 +62,9 @@ __device__ __forceinline__ float sum_group(float x) {
   return x;
 }
 
+// r³·mean: r³ alone leaves fp32's range from heads of 1e-13 on, r·mean does not.
+__device__ __forceinline__ float cubed(float r, float mean) { return r * (r * (r * mean)); }
+
 __device__ __forceinline__ void copy16(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? (BWD ? 2 : 3) : 1)
         const float2 r2 = make_float2(r, r);
         float2 back = r2;
         if constexpr (BWD) {
-          const float shift = -(r * r * r * sum_group<LANES>(sp.x + sp.y) * a.inv_d);
+          const float shift = -cubed(r, sum_group<LANES>(sp.x + sp.y) * a.inv_d);
           back = make_float2(shift, shift);
         }
 #pragma unroll
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
           }
         }
         const float r = rsqrtf(fmaf(sum_group<32>(ss), a.inv_d, a.eps));
-        const float shift = BWD ? r * r * r * sum_group<32>(sp) * a.inv_d : 0.f;
+        const float shift = BWD ? cubed(r, sum_group<32>(sp) * a.inv_d) : 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int p = lane + 32 * i;
@@ -599,6 +602,7 @@ int check(NormArgs& a, int dtype, int64_t N, int d, int w_dtype, float eps, int 
     if (a.y[0] == a.y[1] || a.y[0] == a.x[1] || a.y[1] == a.x[0]) return TT_ERR_INVALID_ARG;
     if (bwd && (a.y[0] == a.dy[1] || a.y[1] == a.dy[0])) return TT_ERR_INVALID_ARG;
   }
+  if (reinterpret_cast<uintptr_t>(pos) % 4) return TT_ERR_INVALID_ARG;
   if (rot && (!pos || (axes > 1 && pos_ld != 0 && pos_ld < N))) return TT_ERR_INVALID_ARG;
   return TT_OK;
 }

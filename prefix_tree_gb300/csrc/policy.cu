@@ -46,6 +46,7 @@ __device__ __forceinline__ F2 two_sum(float a, float b) {
 }
 __device__ __forceinline__ F2 add(F2 x, F2 y) {
   F2 s = two_sum(x.hi, y.hi);
+  if (!(fabsf(s.hi) < INFINITY)) return {s.hi, 0.f};  // (there the rounding errors are NaN)
   s.lo += x.lo + y.lo;
   return two_sum(s.hi, s.lo);
 }
@@ -354,7 +355,7 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
   const float logp = empty ? -INFINITY : !y_ok ? __int_as_float(0x7fc00000)
                                                : zy == -INFINITY ? zy - log_s : a1.hi + (a0.lo + a1.lo - ls.lo);
   auto from = [&](float other) {  // logp − other
-    if (!(fabsf(logp) < INFINITY)) return logp - other;
+    if (!(fabsf(logp) < INFINITY && fabsf(other) < INFINITY)) return logp - other;
     const F2 b0 = two_sum(a0.hi, -other), b1 = two_sum(b0.hi, -ls.hi);
     return b1.hi + (a0.lo + b0.lo + b1.lo - ls.lo);
   };
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(32 * WARPS * kGroups<WARPS>, kMinBlocks<WARPS,
 #pragma unroll
   for (int b = 0; b < kAhead; ++b) fetch(lo + tid + b * kBatch * kGroup);
   if (w == 0.f) {
-    asm volatile("cp.async.wait_all;" ::: "memory");  // a masked row: its logits are not read
+    asm volatile("cp.async.wait_all;" ::: "memory");  // a masked row, whatever the logits that came hold
     if (a.dz)
       for (int j = lo + tid; j < hi; j += kGroup) put(j, make_uint4(0, 0, 0, 0));
     if (rank == 0 && tid == 0) {
@@ -720,6 +721,9 @@ TT_API int tt_policy_loss_logits(const void* logits, int dtype, int64_t N, int64
   if (N == 0) return cuda_status(cudaMemsetAsync(sums, 0, 4 * sizeof(float), st));
   if (!logits || !targets || !old_logp || !adv || !logp || !entropy || !err) return TT_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) % es) return TT_ERR_INVALID_ARG;
+  const void* words[9] = {targets, old_logp, adv, adv_neg, ref_logp, weights, logp, entropy, err};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) % 4) return TT_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;
   if (ws_bytes < tt_policy_loss_logits_workspace_bytes(N)) return TT_ERR_WORKSPACE;
   const LogitsArgs a = {logits, dlogits, N, V, ld, targets, {old_logp, adv, adv_neg, ref_logp, weights}, c, logp, entropy,

@@ -302,6 +302,26 @@ __device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
+// A copy whose lines the L2 cache keeps as `policy` says.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], [%2], "
+      "%5;" ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+// The keys of a segment whose rows take several tiles are read again for each, by CTAs at different times; those of the others
+// once, and they are not to drive the first ones out of the L2 cache. Four layers of a deep tree (16,001 shared rows, 600 of
+// their queries' heads to a key head; 120 rollouts of 1500 rows): no policy 703 us, this one 635 to 648; with the first ones marked to
+// be evicted last 632, but these would stay in the way of the kernels that follow.
+__device__ __forceinline__ uint64_t cache_policy(bool again) {
+  uint64_t p;
+  if (again)
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // A ring's stage and phase n blocks on.
 __device__ __forceinline__ void pass_stages(int n, int& stage, int& phase, int stages) {
   stage += n;
@@ -374,10 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int full = v ? V_FULL : K_FULL, empty = v ? V_EMPTY : K_EMPTY, stages = v ? kVStages : kKStages;
       uint8_t* dst = sm + (v ? L::v0 : L::k0);
       prefetch_tmap(map);
+      const uint64_t once = cache_policy(false), again = cache_policy(true);
       int i = 0, st = 0, phase = 0;
       for (bool ok = true; ok && !at.done();) {
         const int n = at.stretch();
         int y0 = at.kv + at.blk * kKeys, left = at.len - at.blk * kKeys;
+        const uint64_t policy = at.tiles > 1 ? again : once;
         for (int t = 0; t < n; ++t, ++i, y0 += kKeys, left -= kKeys) {
           if (i >= stages && !mbar_wait(&bar[empty + st], phase ^ 1, abort_flag, 50)) {
             ok = false;
@@ -390,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < D / 64; ++x)
               tma_load_2d(dst + st * L::kTile + x * L::kBox + y * kPiece * 128, map, &bar[full + st], at.h * D + x * 64,
-                          y0 + y * kPiece);
+                          y0 + y * kPiece, policy);
           if (++st == stages) st = 0, phase ^= 1;
         }
         at.pass(n);

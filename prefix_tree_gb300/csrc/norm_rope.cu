@@ -117,15 +117,20 @@ __device__ __forceinline__ void load_weights(const NormArgs& a, float* weights) 
     weights[i] = v;
   }
 }
-// Cosines and sines [nt][half] of the tokens t0 .. t0 + nt − 1.
+// Cosines and sines [nt][half] of the tokens t0 .. t0 + nt − 1. A thread keeps to one frequency: in a table among the parameters
+// the lanes of a warp look up their 32 places one after another (a lookup for every angle: the backward of 12,669 tokens 61 us,
+// one for a thread's: 50).
 __device__ __forceinline__ void load_trig(const NormArgs& a, int64_t t0, int nt, bool back, float* cosines, float* sines) {
-  for (int i = threadIdx.x; i < nt * a.half; i += kThreads) {
-    const int t = i / a.half, f = i - t * a.half;
-    const int64_t pos = a.pos[a.axis[f] * a.pos_ld + t0 + t];
+  if (!a.half) return;
+  const int step = kThreads / a.half, first = (int)threadIdx.x / a.half, f = (int)threadIdx.x - first * a.half;
+  if (first >= step) return;
+  const uint64_t turn = a.turn[f];
+  const int32_t* pos = a.pos + a.axis[f] * a.pos_ld + t0;
+  for (int t = first; t < nt; t += step) {
     float s, c;
-    trig_of((uint64_t)pos * a.turn[f], s, c);
-    cosines[i] = c;
-    sines[i] = back ? -s : s;
+    trig_of((uint64_t)(int64_t)pos[t] * turn, s, c);
+    cosines[t * a.half + f] = c;
+    sines[t * a.half + f] = back ? -s : s;
   }
 }
 // The tensor and the blocks that a block of the backward belongs to: the first ones take q, the others k, in proportion to
@@ -190,19 +195,8 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? (BWD ? 2 : 3) : 1)
     for (int j = 0; j < P; ++j) acc[i][0][j] = acc[i][1][j] = make_float2(0.f, 0.f);
   for (int64_t t0 = (int64_t)role.block * tokens; t0 < a.N; t0 += (int64_t)role.blocks * tokens) {
     const int nt = (int)min((int64_t)tokens, a.N - t0);
-    if (BWD) __syncthreads();  // the previous tokens' cosines are no longer read
-    load_trig(a, t0, nt, BWD, cosines, sines);
-    __syncthreads();
     for (int w = role.first; w <= role.last; ++w) {
       const int H = a.heads[w], split = a.split[w], units = nt * split, rounds = (H + split - 1) / split;
-      float2 w1[NV][P], w2[NV][P];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          w1[i][j] = reinterpret_cast<const float2*>(weights + w * a.d + o1[i])[j];
-          w2[i][j] = reinterpret_cast<const float2*>(weights + w * a.d + o2[i])[j];
-        }
       // A group takes a token's heads `split` apart, then those of another token. Whole warps go round together: their lanes
       // meet in the shuffles.
       const int n = (units + kGroups - 1) / kGroups * rounds, step = split * a.d;
@@ -240,6 +234,19 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? (BWD ? 2 : 3) : 1)
       };
       enter();
       for (int k = 0; k < kDepth - 1; ++k) copy(k);
+      if (w == role.first) {  // while they come
+        if (BWD) __syncthreads();  // the previous tokens' cosines are no longer read
+        load_trig(a, t0, nt, BWD, cosines, sines);
+        __syncthreads();
+      }
+      float2 w1[NV][P], w2[NV][P];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          w1[i][j] = reinterpret_cast<const float2*>(weights + w * a.d + o1[i])[j];
+          w2[i][j] = reinterpret_cast<const float2*>(weights + w * a.d + o2[i])[j];
+        }
       // Non-adjacent pairs: the cosines, sines and negated sines of two pairs each; adjacent ones: both of a pair.
       float2 c[NV][ADJ ? 2 * P : P], s1[NV][ADJ ? 2 * P : P], s2[NV][ADJ ? 1 : P];
       T* y = nullptr;

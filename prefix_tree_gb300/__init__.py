@@ -4,8 +4,9 @@ The CUDA library libtt (C ABI in include/tt.h) computes every token's
 log-probability of a DFS-serialised rollout tree exactly once: tree tables,
 tree attention forward/backward (whole tree or path-at-a-time chunks), the
 branch-fraction weighted log-prob loss, and that loss fused with the LM head; beside them the rotary positions in
-front of the attention, and log-prob, entropy and top alternatives per token with their gradients. This package is
-its thin binding.
+front of the attention, also behind a norm of the heads, log-prob, entropy and top alternatives per token with their
+gradients, the clipped policy objective on log-probs or logits, and the attention of running rollouts' next tokens.
+This package is its thin binding.
 """
 from ._native import (KERNEL_CLASSES, TTError, Tree, DTA_DEFAULT_SLOTS, DTA_ORDER_GREEDY, DTA_ORDER_INDEX,
                       DecodePlan, DtaPlan,

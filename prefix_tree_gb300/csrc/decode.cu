@@ -16,6 +16,14 @@
 // a fixed order. With row_base(tile) + 128·CTA as the place of a part, the
 // parts of different tiles and CTAs cannot meet: along the runs one of the two
 // grows at every step, by at least the rows that the part before takes.
+//
+// Bound by memory where most keys are the rollouts' own: 480 of them with 384
+// keys each (1.07 GB) take 157 us, 6.85 TB/s. Where a long prompt has many rows
+// its products and exponentials bound it: a wide block whose keys lie in the
+// L2 cache takes 1.35 us, a narrow one 0.9. A group of 64 rollouts of 8192
+// shared and about 1150 own keys, 8 key heads of 128: 54 + 6 us for 325 MB; a
+// deep tree of 16,001 shared keys, six common turns and 120 rollouts of 1500:
+// 143 to 153 + 9 us for 842 MB.
 #include "tc_common.cuh"
 
 #include <cuda_fp16.h>
@@ -37,10 +45,11 @@ constexpr int kMostCtas = 1024;
 constexpr int kMostSegs = (1 << 24) - 1;
 constexpr int kPiece = 32;       // rows of a copy
 // Work is shared out by cost: of a block, and of a tile's start (its queries have to be fetched first and its sums
-// written last).
+// written last). A narrow block at 2.5 or 3.5 in place of 3: the group of 64 rollouts 5 and 13 % slower, the deep tree 1 % and
+// 18 %.
 constexpr int kBlockWide = 4, kBlockNarrow = 3, kStartWide = 12, kStartNarrow = 4;
 // A segment with more rows than this is taken by tiles of 128 rows on the tensor cores' asynchronous path, one with
-// fewer by tiles of 16 on the warps' own.
+// fewer by tiles of 16 on the warps' own: 24 rows to a segment take 18.8 us by one wide tile and 23.3 by two narrow ones.
 constexpr int kWideFrom = 16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -311,8 +320,8 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
 }
 // The keys of a segment whose rows take several tiles are read again for each, by CTAs at different times; those of the others
 // once, and they are not to drive the first ones out of the L2 cache. Four layers of a deep tree (16,001 shared rows, 600 of
-// their queries' heads to a key head; 120 rollouts of 1500 rows): no policy 703 us, this one 635 to 648; with the first ones marked to
-// be evicted last 632, but these would stay in the way of the kernels that follow.
+// their queries' heads to a key head; 120 rollouts of 1500 rows): no policy 703 to 722 us, this one 634 to 648; with the first
+// ones marked to be evicted last 632, but these would stay in the way of the kernels that follow.
 __device__ __forceinline__ uint64_t cache_policy(bool again) {
   uint64_t p;
   if (again)
@@ -1032,7 +1041,8 @@ TT_API int tt_tree_decode_attn(const void* plan, const void* Q, int64_t q_ld, co
   if (dtype != TT_DT_BF16 && dtype != TT_DT_F16) return TT_ERR_INVALID_ARG;
   if (!plan || !aligned16(plan) || !err || !std::isfinite(scale * kLog2e)) return TT_ERR_INVALID_ARG;
   if (B == 0) return TT_OK;
-  if (!Q || !aligned16(Q) || !O || !aligned16(O) || !LSE || reinterpret_cast<uintptr_t>(LSE) % 4 || q_ld < (int64_t)Hq * d || q_ld % 8) return TT_ERR_INVALID_ARG;
+  if (!Q || !aligned16(Q) || !O || !aligned16(O) || !LSE || reinterpret_cast<uintptr_t>(LSE) % 4) return TT_ERR_INVALID_ARG;
+  if (q_ld < (int64_t)Hq * d || q_ld % 8) return TT_ERR_INVALID_ARG;
   if (rows && (!K || !V || !aligned16(K) || !aligned16(V) || kv_ld < (int64_t)Hkv * d || kv_ld % 8))
     return TT_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return TT_ERR_INVALID_ARG;

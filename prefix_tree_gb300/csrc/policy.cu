@@ -26,7 +26,9 @@
 // old by exact two-sums, with log S as a pair, since rounding logp (about 12)
 // to fp32 first would leave 5e-7 in the ratio; e^x − 1 − x by its series
 // below 1/2, where the difference cancels. The sums over tokens are carried as
-// pairs of floats (about 48 bits), in a fixed order.
+// pairs of floats (about 48 bits), in a fixed order; from log-probs every
+// token's ratio and policy term too, since terms of both signs cancel (524,288
+// tokens 11 us, with ratios as single floats 8.7).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -59,6 +61,35 @@ __device__ __forceinline__ void add(F2& x, float y) {
   x.hi = s.hi;
   x.lo += s.lo;
 }
+// a·x
+__device__ __forceinline__ F2 scaled(float a, F2 x) {
+  const float p = a * x.hi;
+  return {p, fmaf(a, x.lo, fmaf(a, x.hi, -p))};
+}
+// e^x to about 2^-35: x = k·ln 2 + f (Cody and Waite's reduction: ln 2 is split so that k times its first part is exact), e^(f/8)
+// − 1 by its series with the first two terms as pairs, then squared three times.
+__device__ __forceinline__ F2 exp_pair(F2 x) {
+  if (!(fabsf(x.hi) < 80.f)) return {expf(x.hi), 0.f};
+  constexpr float kHi = 0.693145751953125f, kLo = 1.42860682e-6f;  // ln 2 to 15 bits, and the rest
+  const float k = rintf(x.hi * 1.44269504f), p = k * kLo;
+  const F2 f = two_sum(fmaf(-k, kHi, x.hi), -p);
+  const float g = 0.125f * f.hi, gl = 0.125f * (f.lo - fmaf(k, kLo, -p) + x.lo);
+  const float g2 = g * g, g2l = fmaf(2.f * g, gl, fmaf(g, g, -g2));
+  const float rest = g * g2 * fmaf(g, fmaf(g, fmaf(g, 1.f / 720, 1.f / 120), 1.f / 24), 1.f / 6);
+  F2 u = two_sum(g, 0.5f * g2);
+  u.lo += gl + 0.5f * g2l + rest;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {  // (1 + u)² − 1
+    const float q = u.hi * u.hi, ql = fmaf(2.f * u.hi, u.lo, fmaf(u.hi, u.hi, -q));
+    const F2 v = two_sum(2.f * u.hi, q);
+    u = two_sum(v.hi, v.lo + fmaf(2.f, u.lo, ql));
+  }
+  F2 e = two_sum(1.f, u.hi);
+  e.lo += u.lo;
+  const float scale = __int_as_float(((int)k + 127) << 23);
+  return {e.hi * scale, e.lo * scale};
+}
+
 // Policy, KL and entropy terms.
 struct Sums {
   F2 v[3];
@@ -87,6 +118,7 @@ __device__ __forceinline__ void sum_block(Sums& s, Sums* room) {
 // ------------------------------------------------------------------ the objective of one token
 struct Policy {
   float lo, hi, dual, kl, ent, g;  // 1 − ε_lo, 1 + ε_hi, c, β, γ, g
+  float lo_rest, hi_rest;          // of the first two to more than fp32
 };
 struct Inputs {  // per token, fp32 [N] each
   const float *old_logp, *adv, *adv_neg, *ref_logp, *weights;
@@ -110,24 +142,27 @@ __device__ __forceinline__ float exp_rest(float x, float em1) {
   return p * x * x;
 }
 
-// move = logp − old, x = ref − logp (has_ref). Terms without the weight; slope = dL/dlogp without g and w. Comparisons
-// are such that a NaN stays one.
-__device__ __forceinline__ void objective(const Policy& c, float gain, float cost, float move, bool has_ref, float x,
-                                          float& policy, float& kl, float& slope) {
-  const float r = expf(move);
-  policy = -gain * (r > c.hi ? c.hi : r);
-  slope = r > c.hi ? 0.f : -gain * r;
-  if (cost != 0.f) {
-    const float b = r < c.lo ? c.lo : r;
-    policy = fmaf(cost, b > c.dual ? c.dual : b, policy);
-    if (!(r < c.lo) && !(r > c.dual)) slope = fmaf(cost, r, slope);
-  }
-  kl = 0.f;
-  if (has_ref) {
-    const float em1 = expm1f(x);
-    kl = exp_rest(x, em1);
-    if (c.kl != 0.f) slope = fmaf(-c.kl, em1, slope);
-  }
+// The slope of the policy term with respect to logp, r = e^(logp − old): r times one factor, so that gain and cost may cancel.
+// Comparisons are such that a NaN stays one.
+__device__ __forceinline__ float policy_slope(const Policy& c, float gain, float cost, float r) {
+  const float by = (!(r < c.lo) && !(r > c.dual) ? cost : 0.f) - (r > c.hi ? 0.f : gain);
+  return by != 0.f || !(r > c.hi) ? r * by : 0.f;
+}
+// The term itself; and as a pair: over many tokens the terms of both signs cancel, and their roundings do not.
+__device__ __forceinline__ float policy_term(const Policy& c, float gain, float cost, float r) {
+  const float term = -gain * (r > c.hi ? c.hi : r), b = r < c.lo ? c.lo : r;
+  return cost != 0.f ? fmaf(cost, b > c.dual ? c.dual : b, term) : term;
+}
+__device__ __forceinline__ F2 policy_term(const Policy& c, float gain, float cost, F2 r) {
+  const F2 term = scaled(-gain, r.hi > c.hi ? F2{c.hi, c.hi_rest} : r);
+  if (cost == 0.f) return term;
+  return add(term, scaled(cost, r.hi > c.dual ? F2{c.dual, 0.f} : r.hi < c.lo ? F2{c.lo, c.lo_rest} : r));
+}
+// The KL term and its part of the slope, x = ref − logp.
+__device__ __forceinline__ float kl_term(const Policy& c, float x, float& slope) {
+  const float em1 = expm1f(x);
+  if (c.kl != 0.f) slope = fmaf(-c.kl, em1, slope);
+  return exp_rest(x, em1);
 }
 
 // sums[4] = loss, policy, KL, entropy
@@ -202,12 +237,12 @@ __global__ void __launch_bounds__(kTokenThreads) policy_tokens_kernel(const Logp
     const float wt = u < a.N ? (a.in.weights ? w[i] : 1.f) : 0.f;
     dl[i] = dh[i] = 0.f;
     if (wt == 0.f) continue;  // a masked token, whatever its other inputs hold
-    float gain, cost, policy, kl, slope;
+    float gain, cost;
     split(adv[i], a.in.adv_neg != nullptr, neg[i], gain, cost);
-    objective(a.c, gain, cost, lp[i] - old[i], a.in.ref_logp != nullptr, a.in.ref_logp ? ref[i] - lp[i] : 0.f,
-              policy, kl, slope);
-    add(s.v[0], wt * policy);
-    add(s.v[1], wt * kl);
+    const F2 r = exp_pair(two_sum(lp[i], -old[i]));
+    float slope = policy_slope(a.c, gain, cost, r.hi);
+    s.v[0] = add(s.v[0], scaled(wt, policy_term(a.c, gain, cost, r)));
+    if (a.in.ref_logp) add(s.v[1], wt * kl_term(a.c, ref[i] - lp[i], slope));
     if (a.entropy) add(s.v[2], wt * h[i]);
     dl[i] = a.c.g * wt * slope;
     dh[i] = a.c.ent != 0.f ? -a.c.g * wt * a.c.ent : 0.f;
@@ -277,8 +312,8 @@ struct LogitsArgs {
   int32_t* err;
 };
 
-// log s for s >= 1 (or 0, inf, NaN) as a pair: s = 2^k·f with f in [1/√2, √2), log s = k·ln 2 + log f. ln 2 is split so
-// that k times its first part is exact.
+// log s for s >= 1 (or 0, inf, NaN) as a pair: s = 2^k·f with f in [1/√2, √2), log s = k·ln 2 + log f (Cody and
+// Waite's reduction): ln 2 is split so that k times its first part is exact.
 __device__ __forceinline__ F2 log_pair(float s) {
   const uint32_t b = __float_as_uint(s);
   if (!(s > 0.f) || s == INFINITY) return {logf(s), 0.f};
@@ -292,7 +327,7 @@ __device__ __forceinline__ F2 log_pair(float s) {
 
 // What every thread needs of its row.
 struct RowOf {
-  float m, log_s;
+  float m, nl;             // nl: −log2 S
   float gl, slope_t, at0;  // dlogp; and −dlogp − dH·(log p + H) as slope_t·(log2 p) + at0
   int none, wide;          // no gradient; every difference to the maximum has to be bounded (see fold)
 };
@@ -353,7 +388,7 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
   const bool empty = t.m == -INFINITY && t.s == 0.f;  // every logit is -inf: no distribution
   const F2 ls = log_pair(t.s);
   const float log_s = ls.hi + ls.lo;
-  const float h = empty ? 0.f : log_s - t.u / t.s, H = h < 0.f ? 0.f : h;
+  const float h = empty ? 0.f : ls.hi - t.u / t.s + ls.lo, H = h < 0.f ? 0.f : h;
   // log-prob, and its difference to another one, by exact sums
   const F2 a0 = two_sum(zy, -t.m), a1 = two_sum(a0.hi, -ls.hi);
   const float logp = empty ? -INFINITY : !y_ok ? __int_as_float(0x7fc00000)
@@ -363,11 +398,11 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
     const F2 b0 = two_sum(a0.hi, -other), b1 = two_sum(b0.hi, -ls.hi);
     return b1.hi + (a0.lo + b0.lo + b1.lo - ls.lo);
   };
-  float policy, kl, slope;
   float gain, cost;
   split(in.adv, a.in.adv_neg != nullptr, in.adv_neg, gain, cost);
-  objective(a.c, gain, cost, from(in.old_logp), a.in.ref_logp != nullptr, a.in.ref_logp ? -from(in.ref_logp) : 0.f, policy,
-            kl, slope);
+  const float r = expf(from(in.old_logp)), policy = policy_term(a.c, gain, cost, r);
+  float slope = policy_slope(a.c, gain, cost, r);
+  const float kl = a.in.ref_logp ? kl_term(a.c, -from(in.ref_logp), slope) : 0.f;
   if (writer) {
     if (!y_ok) set_err(a.err, TT_ERR_INVALID_ARG);
     a.logp[row] = logp;
@@ -376,7 +411,10 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
   }
   const float gl = a.c.g * w * slope, gh = a.c.ent != 0.f ? -a.c.g * w * a.c.ent : 0.f;
   constexpr float kLn2 = 0.6931471805599453f;
-  return {t.m, log_s, gl, -gh * kLn2, -fmaf(gh, H, gl), empty || !y_ok, !plain_way_holds<T>(t.m)};
+  // −log2 S rounded (about 16: to 1e-6); the rest of it goes into the line, and as a factor of p into both of its numbers
+  const float nl = -ls.hi * kLog2e, rest = -fmaf(ls.hi, kLog2e, nl) - ls.lo * kLog2e, more = fmaf(rest, kLn2, 1.f);
+  const float by = -gh * kLn2;
+  return {t.m, nl, gl, by * more, fmaf(by, rest, -fmaf(gh, H, gl)) * more, empty || !y_ok, !plain_way_holds<T>(t.m)};
 }
 
 // dz of vectors of a row.
@@ -385,7 +423,7 @@ struct Turn {
   float2 nm, nl, sl, b0;
   uint32_t low;
   __device__ __forceinline__ Turn(const RowOf& r)
-      : nm(make_float2(-r.m, -r.m)), nl(make_float2(-r.log_s * kLog2e, -r.log_s * kLog2e)),
+      : nm(make_float2(-r.m, -r.m)), nl(make_float2(r.nl, r.nl)),
         sl(make_float2(r.slope_t, r.slope_t)), b0(make_float2(r.at0, r.at0)), low(0) {
     // so far below the maximum that p is 0, and at least a step of the type below it
     if constexpr (sizeof(T) == 2) low = pack_twice_down<T>(r.m - fmaxf(130.f, fabsf(r.m) * 0.015625f));
@@ -606,8 +644,9 @@ int check_policy(const tt_policy* p, Policy* c) {
     if (!std::isfinite(f)) return TT_ERR_INVALID_ARG;
   if (p->clip_lo < 0.f || p->clip_lo > 1.f || p->clip_hi < 0.f) return TT_ERR_INVALID_ARG;
   if (p->dual_clip != 0.f && !(p->dual_clip >= 1.f)) return TT_ERR_INVALID_ARG;
-  *c = {1.f - p->clip_lo, 1.f + p->clip_hi, p->dual_clip == 0.f ? INFINITY : p->dual_clip, p->kl_coef, p->entropy_coef,
-        p->g};
+  const double lo = 1.0 - p->clip_lo, hi = 1.0 + p->clip_hi;
+  *c = {(float)lo, (float)hi, p->dual_clip == 0.f ? INFINITY : p->dual_clip, p->kl_coef, p->entropy_coef, p->g,
+        (float)(lo - (float)lo), (float)(hi - (float)hi)};
   return TT_OK;
 }
 

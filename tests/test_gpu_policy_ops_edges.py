@@ -72,3 +72,34 @@ def test_nan_keys_reach_the_queries_that_see_them(tt):
     hit = torch.arange(20, device="cuda") == 3
     assert torch.isnan(o[hit]).all() and torch.isnan(lse[:, hit]).all()
     assert torch.isfinite(o[~hit]).all() and torch.isfinite(lse[:, ~hit]).all()
+
+
+@pytest.mark.parametrize("N", [3000, 100_000])
+def test_terms_of_both_signs_cancel_and_their_roundings_do_not(tt, N):
+    """The policy term's sum over advantages that add up to nearly nothing: ratios, products and sums are pairs of floats (a
+    ratio to 2^-34, with twice that for the rest), so that what is left of the sum is rounded once."""
+    rng = np.random.default_rng(N)
+    lp = (-rng.exponential(2.0, N)).astype(np.float32)
+    old = (lp + 0.2 * rng.standard_normal(N)).astype(np.float32)
+    adv = rng.standard_normal(N).astype(np.float32)
+    w = np.ones(N, np.float32)
+    whole = P.objective(lp, old, adv, None, None, None, w, lo=float(np.float32(0.2)), hi=float(np.float32(0.2)))[0][1]
+    r = np.exp(lp.astype(np.float64) - old)
+    adv[0] = np.float32(adv[0] + whole / max(1.0, min(r[0], 1.2)))  # nearly nothing is left
+    ref = P.objective(lp, old, adv, None, None, None, w, lo=float(np.float32(0.2)), hi=float(np.float32(0.2)))[0][1]
+    dev = lambda a: torch.tensor(a, device="cuda")
+    sums, _, _ = tt.policy_loss(dev(lp), dev(old), dev(adv), weights=dev(w), clip=0.2)
+    size = (np.abs(adv.astype(np.float64)) * np.maximum(r, 0.8)).sum()
+    assert abs(float(sums[1]) - ref) <= 2.0 ** -24 * abs(ref) + 2.0 ** -32 * size
+    assert abs(ref) < 0.05 * size
+
+
+@pytest.mark.parametrize("move", [-100.0, -79.5, -20.3, -1.1, -0.3466, -1e-3, 0.0, 3e-5, 0.3466, 0.7, 15.9, 79.9])
+def test_ratios_of_all_sizes(tt, move):
+    """One token with an unbounded advantage: the term is the ratio itself, or 1 − clip below; from |move| = 80 on its
+    exponential is fp32's (2^-22)."""
+    lp, old = torch.full((1,), -3.0, device="cuda"), torch.full((1,), -3.0 - move, device="cuda")
+    sums, dlogp, _ = tt.policy_loss(lp, old, torch.full((1,), -1.0, device="cuda"), clip=(1.0, 0.2))
+    r = np.exp(-3.0 - old.double().item())
+    assert abs(float(sums[1]) - r) <= 2.0 ** (-22 if abs(move) >= 79 else -24) * r * 1.001 + (2.0 ** -148 if r < 2.0 ** -126 else 0)
+    assert abs(float(dlogp[0]) - r) <= 2.0 ** -22 * r + (2.0 ** -148 if r < 2.0 ** -126 else 0)

@@ -857,10 +857,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   wait_prerequisites();
   const PlanHeader* hdr = static_cast<const PlanHeader*>(a.plan);
   const int4* segs = reinterpret_cast<const int4*>(static_cast<const char*>(a.plan) + kPlanSegs);
-  // (the first segments together with the header that says how many there are: the plan has room for all S)
+  if (plan_error(a, D)) return;  // (before any segment is read: the bytes may hold a plan of fewer of them, or none)
   int4 x = make_int4(0, 0, 0, 0), y = x;
-  if ((int)threadIdx.x < a.S) x = segs[2 * threadIdx.x], y = segs[2 * threadIdx.x + 1];
-  if (plan_error(a, D)) return;
+  if ((int)threadIdx.x < hdr->segments) x = segs[2 * threadIdx.x], y = segs[2 * threadIdx.x + 1];
   const int b = blockIdx.x, hq = blockIdx.y * kJoinWarps + warp, G = a.Hq / a.Hkv, h = hq / G, quota = hdr->quota;
   constexpr int kE = D / 32;  // columns of a lane
   float M = -INFINITY, Ls = 0.f, acc[kE] = {};

@@ -480,9 +480,9 @@ __device__ __forceinline__ void add_vectors(Stat& t, const uint4 (&u)[N]) {
 }
 
 // That a CTA has started says nothing about memory: with the release that the cluster barrier has by default 12,669 rows of
-// 151,936 took 1211 us, not 1179.
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// 151,936 took 1211 us, not 1179. Not the aligned forms: a masked row's lanes come out of their last stores one by one.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Blocks to an SM that the registers are held to: left alone the compiler takes 90 (a tree's rows 1200 -> 1470 us).
 template <int WARPS, bool CLUSTER>

@@ -329,7 +329,7 @@ __device__ __forceinline__ F2 log_pair(float s) {
 struct RowOf {
   float m, nl;             // nl: −log2 S
   float gl, slope_t, at0;  // dlogp; and −dlogp − dH·(log p + H) as slope_t·(log2 p) + at0
-  int none, wide;          // no gradient; every difference to the maximum has to be bounded (see fold)
+  int none, wide;          // no gradient; every difference to the maximum has to be bounded (see turns_plainly)
 };
 
 constexpr int kBatch = 4;   // vectors of a thread at once: one rescaling for all of them
@@ -380,6 +380,17 @@ __device__ __forceinline__ RowInputs inputs_of(const Inputs& in, int64_t row, fl
   return {in.old_logp[row], in.adv[row], in.adv_neg ? in.adv_neg[row] : 0.f, in.ref_logp ? in.ref_logp[row] : 0.f, w};
 }
 
+// Whether a row of 16-bit logits with maximum m can be turned with its elements raised to Turn::low. That bound, about
+// m − |m|/64, has to be finite in the type (fp16: from m = −64,496 down it is −inf; the sums hold on to −65,000, since they
+// raise to the lowest value itself), and p = 0 times the line there has to be 0: the line's slope times 2^-6·|m| below fp32's
+// largest value.
+template <typename T>
+__device__ __forceinline__ bool turns_plainly(float m) {
+  if constexpr (sizeof(T) == 4) return true;
+  else if constexpr (std::is_same<T, __half>::value) return m > -64000.f && m < INFINITY;
+  else return fabsf(m) < 1e30f;
+}
+
 // A row's terms, log-prob and entropy written (by `writer`), and what its gradient needs.
 template <typename T>
 __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const RowInputs& in, const Stat& t, float zy, bool y_ok,
@@ -414,7 +425,7 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
   // −log2 S rounded (about 16: to 1e-6); the rest of it goes into the line, and as a factor of p into both of its numbers
   const float nl = -ls.hi * kLog2e, rest = -fmaf(ls.hi, kLog2e, nl) - ls.lo * kLog2e, more = fmaf(rest, kLn2, 1.f);
   const float by = -gh * kLn2;
-  return {t.m, nl, gl, by * more, fmaf(by, rest, -fmaf(gh, H, gl)) * more, empty || !y_ok, !plain_way_holds<T>(t.m)};
+  return {t.m, nl, gl, by * more, fmaf(by, rest, -fmaf(gh, H, gl)) * more, empty || !y_ok, !turns_plainly<T>(t.m)};
 }
 
 // dz of vectors of a row.

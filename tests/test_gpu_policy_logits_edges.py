@@ -28,3 +28,25 @@ def test_masked_rows_among_others_whose_lanes_do_not_end_together(tt, dtype, N, 
         z[::2] = fill
         got = tt.policy_loss_logits(z, _dev(y, np.int32), *pos, **kw, entropy_coef=ENT, **HOW)
         assert all(torch.equal(a, b) for a, b in zip(want, got)) and (got[3][::2] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,tops", [
+    ("fp16", [-63968, -64000, -64032, -64480, -64512, -64544, -64768, -64960, -64992, -65024, -65472, -65504, 65504]),
+    ("bf16", [-1e29, -1e30, -2e30, -1e36, -9.9e37, -1e38, -1.2e38, -3e38, 1e29, 2e30, 9e35, 1.1e36, 3e38])])
+@pytest.mark.parametrize("times,V,weight", [(1, 700, 1.0), (100, 130, 8.0), (100, 5000, 1.0), (1, 12000, 1e6), (1, 40000, 0.5)])
+def test_masked_logits_beside_a_far_maximum(tt, dtype, times, V, weight, tops):
+    """Rows whose largest logits (four of them, the target among them: log-prob -log 4 exactly) lie near the ends of the
+    type's range, with masked logits and lower finite ones (p = 0) beside them. The weight scales the gradient's line."""
+    rng = np.random.default_rng(V)
+    tops = tops * times
+    t, N, weight = DT[dtype], len(tops), min(weight, 1e6 if dtype == "bf16" else 100.0)  # (fp16 gradients end at 65,504)
+    z = torch.full((N, V), -math.inf, dtype=t, device="cuda")
+    top = torch.tensor(tops, dtype=torch.float64).to(t).cuda()
+    at = torch.from_numpy(np.argsort(rng.random((N, V)), axis=1)[:, :5].copy()).cuda()
+    y = at[:, 0].cpu().numpy()
+    z.scatter_(1, at[:, :4], top[:, None].expand(N, 4))
+    lower = (torch.arange(N, device="cuda") % 2 == 1) & (top != torch.finfo(t).min)
+    z[lower, at[lower, 4]] = torch.finfo(t).min
+    s = _inputs(rng, np.full(N, -math.log(4.0)), True, True, False)
+    s["weights"] = np.full(N, weight, np.float32)
+    _check_logits(tt, rng, z, s, y)

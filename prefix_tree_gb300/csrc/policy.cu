@@ -402,8 +402,8 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
   const float h = empty ? 0.f : ls.hi - t.u / t.s + ls.lo, H = h < 0.f ? 0.f : h;
   // log-prob, and its difference to another one, by exact sums
   const F2 a0 = two_sum(zy, -t.m), a1 = two_sum(a0.hi, -ls.hi);
-  const float logp = empty ? -INFINITY : !y_ok ? __int_as_float(0x7fc00000)
-                                               : zy == -INFINITY ? zy - log_s : a1.hi + (a0.lo + a1.lo - ls.lo);
+  const float logp = !y_ok ? __int_as_float(0x7fc00000)
+                     : empty ? -INFINITY : zy == -INFINITY ? zy - log_s : a1.hi + (a0.lo + a1.lo - ls.lo);
   auto from = [&](float other) {  // logp − other
     if (!(fabsf(logp) < INFINITY && fabsf(other) < INFINITY)) return logp - other;
     const F2 b0 = two_sum(a0.hi, -other), b1 = two_sum(b0.hi, -ls.hi);

@@ -50,3 +50,20 @@ def test_masked_logits_beside_a_far_maximum(tt, dtype, times, V, weight, tops):
     s = _inputs(rng, np.full(N, -math.log(4.0)), True, True, False)
     s["weights"] = np.full(N, weight, np.float32)
     _check_logits(tt, rng, z, s, y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N,V", [(4, 300), (1300, 100), (1300, 5000), (4, 9000), (4, 60000)])
+def test_a_bad_target_of_a_row_without_a_distribution(tt, dtype, N, V):
+    """The row's log-prob, and with it the loss, is NaN, as with any other row; entropy 0 and dlogits zeros."""
+    rng = np.random.default_rng(V)
+    z = _logits(rng, N, V, V, DT[dtype])
+    z[1:3] = -math.inf
+    y = rng.integers(0, V, N)
+    for bad in (V, -1, 2 ** 31 - 1, -2 ** 31):
+        y[1] = bad
+        err = tt.new_err("cuda")
+        sums, logp, h, dz = tt.policy_loss_logits(z, _dev(y, np.int32), _dev(np.zeros(N)), _dev(np.ones(N)), err=err)
+        assert int(err.item()) == -1 and torch.isnan(sums[:2]).all()
+        assert torch.isnan(logp).tolist() == [i == 1 for i in range(N)] and logp[2] == -math.inf
+        assert (h[1:3] == 0).all() and (dz[1:3] == 0).all() and torch.isfinite(dz).all()

@@ -943,13 +943,25 @@ def _policy(clip, dual_clip, kl_coef, entropy_coef, g):
     return ctypes.byref(_Policy(lo, hi, 0.0 if dual_clip is None else dual_clip, kl_coef, entropy_coef, g))
 
 
+def _coefficient(x, name):
+    """x as a float: a tensor's value now, not the tensor, is what a cached struct may be kept by. One on a device is refused:
+    to read it back would make every call wait for the stream, and fail in a capture."""
+    if type(x) is float:
+        return x
+    if isinstance(x, torch.Tensor) and x.device.type != "cpu":
+        raise TypeError(f"{name} must be a number on the host")
+    return float(x)
+
+
 def _policy_of(clip, dual_clip, kl_coef, entropy_coef, g):
     """The host struct tt_policy. clip: one number for both sides, or (below, above)."""
-    if not isinstance(clip, (tuple, list)):
-        clip = (clip, clip)
-    if dual_clip is not None and not dual_clip >= 1:
-        raise ValueError("dual_clip must be at least 1 (None: no such bound)")
-    return _policy(tuple(clip), dual_clip, kl_coef, entropy_coef, g)
+    lo, hi = clip if isinstance(clip, (tuple, list)) else (clip, clip)
+    if dual_clip is not None:
+        dual_clip = _coefficient(dual_clip, "dual_clip")
+        if not dual_clip >= 1:
+            raise ValueError("dual_clip must be at least 1 (None: no such bound)")
+    return _policy((_coefficient(lo, "clip"), _coefficient(hi, "clip")), dual_clip, _coefficient(kl_coef, "kl_coef"),
+                   _coefficient(entropy_coef, "entropy_coef"), _coefficient(g, "g"))
 
 
 def policy_loss(logp, old_logp, adv, adv_neg=None, ref_logp=None, entropy=None, weights=None, clip=0.2, dual_clip=None,

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 from dataclasses import dataclass
 
@@ -297,6 +298,13 @@ def _frequencies(inv_freq):
     return tuple(float(f) for f in inv_freq)
 
 
+def _section_sizes(sections):
+    """sections as the key of _rope_tables: their values now, whatever holds them."""
+    if any(isinstance(n, torch.Tensor) and n.device.type != "cpu" for n in sections):
+        raise TypeError("sections must be numbers on the host")
+    return tuple(operator.index(n) for n in sections)
+
+
 def _rope_rows(t, name):
     """(N, heads, d, elements between tokens) of a tensor of heads."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 3:
@@ -327,7 +335,7 @@ def _rope_how(positions, N, d, rot_dim, sections, interleaved, base, inv_freq):
         sections = (rot // 2,)
     elif len(sections) != axes:
         raise ValueError("positions and sections must agree on the number of axes")
-    axis, freq = _rope_tables(rot, tuple(sections), bool(interleaved), float(base), _frequencies(inv_freq))
+    axis, freq = _rope_tables(rot, _section_sizes(sections), bool(interleaved), float(base), _frequencies(inv_freq))
     return positions, positions.stride(0) if many else N, axes, rot, axis, freq
 
 

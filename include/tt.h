@@ -268,7 +268,8 @@ TT_API int tt_tree_decode_plan(const int32_t* kv_begin, const int32_t* kv_len, c
  * tt_tree_decode_attn_workspace_bytes(pairs, Hq, d) bytes, 16-byte aligned;
  * calls that may overlap (other streams, graphs) need their own. Rows of the
  * pool outside the listed segments may hold anything. The weights enter the
- * second product in type dtype; everything else is fp32. Repeated calls agree
+ * second product in type dtype (in fp16 those below 2^-21 of a row's largest
+ * as multiples of 2^-31 of it); everything else is fp32. Repeated calls agree
  * bitwise. */
 TT_API size_t tt_tree_decode_attn_workspace_bytes(int64_t pairs, int Hq, int d);
 TT_API int tt_tree_decode_attn(const void* plan, const void* Q, int64_t q_ld, const void* K, const void* V, int64_t kv_ld,

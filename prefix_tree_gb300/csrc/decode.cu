@@ -11,7 +11,7 @@
 // rows. All blocks of the step, in the order segment, head, tile, block, are
 // cut into equal runs, one for each CTA (one CTA to an SM): a CTA may end one
 // tile's keys, take others whole and begin another's. It leaves for each tile
-// that it met the unnormalised sums, the maxima and the sums of weights of
+// that it met the unnormalised sums, the references and the sums of weights of
 // its rows (fp32); a second kernel joins the parts of every query and head in
 // a fixed order. With row_base(tile) + 128·CTA as the place of a part, the
 // parts of different tiles and CTAs cannot meet: along the runs one of the two
@@ -171,7 +171,7 @@ struct DecodeArgs {
   int64_t rows, pairs;
   float scale_log2;
   float* part_o;   // [parts' rows][D]
-  float2* part_ml; // [parts' rows] maximum (log2 units) and sum of weights
+  float2* part_ml; // [parts' rows] reference (log2 units) and sum of weights
   void* o;
   float* lse;
   int32_t* err;
@@ -283,8 +283,15 @@ constexpr int kKStages = 3, kVStages = 2;  // K and V tiles in shared memory
 // Tensor memory: each of two groups of four warps has 128 columns for S, whose places its weights take, and up to 128
 // for O.
 constexpr uint32_t kTmemCols = 512, kGroupCols = 256, kColO = 128;
-// The running maximum of a row moves only when it grows by more than this (log2 units): weights stay below 2^8.
+// The weights enter the second product in the type of V, each off by up to half a step (bf16 2^-8, fp16 2^-11): the product
+// of two factors of one 16-bit type is what the tensor cores have, and 32 bits of weight (as a high and a low part) would
+// double it. The sum of weights is that of the unrounded ones.
+// A row's weights are 2^(score − reference), the reference kLift below a maximum that moves only when the scores grow by more
+// than kRescale above it (log2 units): they stay below 2^(kRescale + kLift). fp16 has room for 2^15 and ends at 2^-24, so that
+// lifted by 2^7 the weights of far keys are rounded to multiples of 2^-31 of the largest (the sum counts them in any case).
 constexpr float kRescale = 8.0f;
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
 
 template <int D>
 struct Smem {
@@ -293,7 +300,7 @@ struct Smem {
   static constexpr uint32_t q = 0;                         // the 128 rows of a wide tile, laid out as a K tile
   static constexpr uint32_t k0 = q + kTile;
   static constexpr uint32_t v0 = k0 + kKStages * kTile;
-  // wide tiles: maximum and sum [2][2][128] f32 of the two groups' rows; narrow tiles: twice [kWarps][16] f32
+  // wide tiles: reference and sum [2][2][128] f32 of the two groups' rows; narrow tiles: twice [kWarps][16] f32
   static constexpr uint32_t rows = v0 + kVStages * kTile;
   static constexpr uint32_t bars = rows + 4 * 128 * 4;
   static constexpr uint32_t misc = bars + 32 * 8;
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&bar[Q_READY]);
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f;  // the row's reference, and its sum of weights
         const float size = fabsf(a.scale_log2);
         for (int t = 0; t < n; ++t, left -= kKeys) {
           if ((t & 1) == g) {
@@ -572,11 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float top = fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * size;
             bool moved = false;
             float f = 1.f;
-            if (top > m + kRescale) {
-              f = fast_exp2(m - top);  // 0 at the group's first keys
+            if (top > m + (kRescale + kLift<T>)) {
+              f = fast_exp2(m - (top - kLift<T>));  // 0 at the group's first keys
               l *= f;
               moved = t >= 2;
-              m = top;
+              m = top - kLift<T>;
             }
             if (__any_sync(~0u, moved)) {  // (the products into O that were issued before this S are done, as it is)
               const float by = moved ? f : 1.f;
@@ -683,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(sm + L::q + row * kQLd + u * 16) = x;
         }
         const uint32_t qbase = smem_u32(sm + L::q) + ((mi & 1) * 8 + mr) * kQLd + (mi >> 1) * 16;
-        float o[D / 8][4], m[2], l[2];
+        float o[D / 8][4], m[2], l[2];  // (m: references)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           m[half] = -INFINITY;
@@ -740,10 +747,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               float x = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-              if (x > m[half] + kRescale) {
-                f[half] = fast_exp2(m[half] - x);  // 0 at the first keys
+              if (x > m[half] + (kRescale + kLift<T>)) {
+                f[half] = fast_exp2(m[half] - (x - kLift<T>));  // 0 at the first keys
                 l[half] *= f[half];
-                m[half] = x;
+                m[half] = x - kLift<T>;
                 moved = true;
               }
               const float mu = m[half] == -INFINITY ? 0.f : m[half];

@@ -1,5 +1,6 @@
 """tt_tree_decode_plan / tt_tree_decode_attn at the ends of what they take."""
 import dataclasses
+import math
 
 import pytest
 import torch
@@ -24,3 +25,46 @@ def test_a_plan_of_another_number_of_segments_is_refused(tt, held, said):
     tt.tree_decode_attn(plan, q, k, v, out=out)
     plan.check()
     assert (out[0] != 7).all() if held else (out[0] == 0).all()
+
+
+def _attention64(q, k, v, segs, scale):
+    """O and Σ p·|v| of queries with one segment each or all with the same, in 64 bits on the device."""
+    O, A = torch.zeros_like(q, dtype=torch.float64), torch.zeros_like(q, dtype=torch.float64)
+    G = q.shape[1] // k.shape[1]
+    for s, n, q0, q1 in segs:
+        for h in range(k.shape[1]):
+            x = q[q0:q1, h * G:(h + 1) * G].double() @ k[s:s + n, h].double().T * scale
+            p = torch.softmax(x, -1)
+            O[q0:q1, h * G:(h + 1) * G] = p @ v[s:s + n, h].double()
+            A[q0:q1, h * G:(h + 1) * G] = p @ v[s:s + n, h].double().abs()
+    return O, A
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,n,hq,hkv", [(32, 8192, 16, 4), (1, 131072, 160, 8)])  # rows of 4 and of 20 queries' heads
+@pytest.mark.parametrize("far", [20.0, 26.0, 28.0])
+def test_many_far_keys_beside_a_near_one(tt, dtype, d, B, n, hq, hkv, far):
+    """One key some 2^far times as likely as each of the thousands behind it, whose values are large: together they are a good
+    part of O. A weight's rounding: half a step of its type, or half of fp16's last step: 2^-32 of the largest weight."""
+    g = torch.Generator(device="cuda").manual_seed(int(far))
+    q, k, v = (torch.randn(s, device="cuda", generator=g) for s in ((B, hq, d), (B * n, hkv, d), (B * n, hkv, d)))
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    q[..., 1:] *= 0.1
+    k[::n, :, 0] = far * math.log(2.0) / 8
+    k[..., 1:] *= 0.1
+    v += 2.0 ** (far - 14)
+    v[::n] = torch.randn(B, hkv, d, device="cuda", generator=g)
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    segs = [(i * n, n, i, i + 1) for i in range(B)]
+    table = torch.tensor(segs, dtype=torch.int32).T.contiguous().cuda()
+    plan = tt.tree_decode_plan(table, B, B * n, B, hq, hkv, d)
+    o, lse = tt.tree_decode_attn(plan, q, k, v, scale=1.0)
+    plan.check()
+    O, A = _attention64(q, k, v, segs, 1.0)
+    half = torch.finfo(dtype).eps / 2
+    tol = half * O.abs() + (half + 1e-4) * A * 1.01
+    if dtype == torch.float16:
+        tol += n * 2.0 ** -32 * 1.01 * v.double().abs().max() + 2.0 ** -24
+    off = (o.double() - O).abs()
+    assert (off <= tol).all(), (off.max(), (off / tol).max())

@@ -570,7 +570,9 @@ TT_API int tt_token_logprob_bwd(const void* logits, int dtype, int64_t N, int64_
  * inputs of other tokens give what the formulas give (a sum may be NaN).
  * sums: fp32 [4], written: loss, Σ w·(the gain and cost terms), Σ w·(e^x − 1
  * − x), Σ w·entropy, all without g; summed in about 48 bits in a fixed order
- * and rounded once. Repeated calls agree bitwise.
+ * and rounded once. A token's gain and cost terms, whose signs may cancel, are
+ * formed to 2^-32 of themselves (|logp − old| < 80; what logp itself is off by
+ * aside), the others and the gradients in fp32. Repeated calls agree bitwise.
  * Limits (TT_ERR_INVALID_ARG): 0 <= clip_lo <= 1, clip_hi >= 0, dual_clip >= 1
  * or 0 (no such bound), all coefficients finite. */
 typedef struct tt_policy {

@@ -26,9 +26,9 @@
 // old by exact two-sums, with log S as a pair, since rounding logp (about 12)
 // to fp32 first would leave 5e-7 in the ratio; e^x − 1 − x by its series
 // below 1/2, where the difference cancels. The sums over tokens are carried as
-// pairs of floats (about 48 bits), in a fixed order; from log-probs every
-// token's ratio and policy term too, since terms of both signs cancel (524,288
-// tokens 11 us, with ratios as single floats 8.7).
+// pairs of floats (about 48 bits), in a fixed order; every token's ratio and
+// policy term too, since terms of both signs cancel (524,288 tokens 11 us, with
+// ratios as single floats 8.7).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -148,11 +148,7 @@ __device__ __forceinline__ float policy_slope(const Policy& c, float gain, float
   const float by = (!(r < c.lo) && !(r > c.dual) ? cost : 0.f) - (r > c.hi ? 0.f : gain);
   return by != 0.f || !(r > c.hi) ? r * by : 0.f;
 }
-// The term itself; and as a pair: over many tokens the terms of both signs cancel, and their roundings do not.
-__device__ __forceinline__ float policy_term(const Policy& c, float gain, float cost, float r) {
-  const float term = -gain * (r > c.hi ? c.hi : r), b = r < c.lo ? c.lo : r;
-  return cost != 0.f ? fmaf(cost, b > c.dual ? c.dual : b, term) : term;
-}
+// The term itself, as a pair: over many tokens the terms of both signs cancel, and their roundings do not.
 __device__ __forceinline__ F2 policy_term(const Policy& c, float gain, float cost, F2 r) {
   const F2 term = scaled(-gain, r.hi > c.hi ? F2{c.hi, c.hi_rest} : r);
   if (cost == 0.f) return term;
@@ -283,7 +279,7 @@ __global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const void* par
       f[q] = i + q * kSumThreads < n ? static_cast<const float4*>(parts)[i + q * kSumThreads] : make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-      add(s.v[0], f[q].x);
+      s.v[0] = add(s.v[0], {f[q].x, f[q].w});
       add(s.v[1], f[q].y);
       add(s.v[2], f[q].z);
     }
@@ -308,7 +304,7 @@ struct LogitsArgs {
   Inputs in;
   Policy c;
   float *logp, *entropy;
-  float4* rows;  // the row's terms
+  float4* rows;  // the row's terms: policy (its first part), KL, entropy; the policy term's second part
   int32_t* err;
 };
 
@@ -404,21 +400,21 @@ __device__ __forceinline__ RowOf row_of(const LogitsArgs& a, int64_t row, const 
   const F2 a0 = two_sum(zy, -t.m), a1 = two_sum(a0.hi, -ls.hi);
   const float logp = !y_ok ? __int_as_float(0x7fc00000)
                      : empty ? -INFINITY : zy == -INFINITY ? zy - log_s : a1.hi + (a0.lo + a1.lo - ls.lo);
-  auto from = [&](float other) {  // logp − other
-    if (!(fabsf(logp) < INFINITY && fabsf(other) < INFINITY)) return logp - other;
+  auto from = [&](float other) -> F2 {  // logp − other
+    if (!(fabsf(logp) < INFINITY && fabsf(other) < INFINITY)) return {logp - other, 0.f};
     const F2 b0 = two_sum(a0.hi, -other), b1 = two_sum(b0.hi, -ls.hi);
-    return b1.hi + (a0.lo + b0.lo + b1.lo - ls.lo);
+    return two_sum(b1.hi, a0.lo + b0.lo + b1.lo - ls.lo);
   };
   float gain, cost;
   split(in.adv, a.in.adv_neg != nullptr, in.adv_neg, gain, cost);
-  const float r = expf(from(in.old_logp)), policy = policy_term(a.c, gain, cost, r);
-  float slope = policy_slope(a.c, gain, cost, r);
-  const float kl = a.in.ref_logp ? kl_term(a.c, -from(in.ref_logp), slope) : 0.f;
+  const F2 r = exp_pair(from(in.old_logp)), policy = scaled(w, policy_term(a.c, gain, cost, r));
+  float slope = policy_slope(a.c, gain, cost, r.hi);
+  const float kl = a.in.ref_logp ? kl_term(a.c, -from(in.ref_logp).hi, slope) : 0.f;
   if (writer) {
     if (!y_ok) set_err(a.err, TT_ERR_INVALID_ARG);
     a.logp[row] = logp;
     a.entropy[row] = H;
-    a.rows[row] = make_float4(w * policy, w * kl, w * H, 0.f);
+    a.rows[row] = make_float4(policy.hi, w * kl, w * H, policy.lo);
   }
   const float gl = a.c.g * w * slope, gh = a.c.ent != 0.f ? -a.c.g * w * a.c.ent : 0.f;
   constexpr float kLn2 = 0.6931471805599453f;

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import policy as P
 from oracle import token_logprob as TL
 from tests.test_gpu_policy import DT, ENT, HOW, _args, _check_logits, _dev, _f64, _inputs, _logits
 
@@ -67,3 +68,32 @@ def test_a_bad_target_of_a_row_without_a_distribution(tt, dtype, N, V):
         assert int(err.item()) == -1 and torch.isnan(sums[:2]).all()
         assert torch.isnan(logp).tolist() == [i == 1 for i in range(N)] and logp[2] == -math.inf
         assert (h[1:3] == 0).all() and (dz[1:3] == 0).all() and torch.isfinite(dz).all()
+
+
+@pytest.mark.parametrize("N,V", [(400, 64), (1300, 64), (1300, 6000), (400, 9000), (30, 5000), (120, 90000)])
+@pytest.mark.parametrize("seed", range(4))
+def test_terms_of_both_signs_cancel_and_their_roundings_do_not(tt, N, V, seed):
+    """Rows of 2^j equal logits and masked ones: the sum of exponentials is 2^j and the log-prob -j·log 2, so that nothing is
+    off but what the objective itself rounds. The policy term's sum is brought down to nearly nothing by one advantage; a ratio
+    is within 2^-34, log 2^j and the products add less than twice that, and the sum is rounded once."""
+    rng = np.random.default_rng(seed)
+    t = [torch.bfloat16, torch.float16, torch.float32][seed % 3]
+    j = rng.integers(0, int(math.log2(V)) + 1, N)
+    rank = torch.from_numpy(np.argsort(np.argsort(rng.random((N, V)), axis=1), axis=1)).cuda()
+    top = torch.from_numpy(rng.integers(-40, 40, N) / 8).cuda()
+    z = torch.where(rank < torch.from_numpy(2 ** j).cuda()[:, None], top[:, None], -math.inf).to(t)
+    y = (rank == 0).int().argmax(1).int()
+    logp = -j * math.log(2.0)
+    old = (logp + 0.2 * rng.standard_normal(N)).astype(np.float32)
+    old[0] = np.float32(logp[0])
+    adv, w = rng.standard_normal(N).astype(np.float32), (rng.integers(1, 17, N) / 16).astype(np.float32)
+    how = dict(lo=float(np.float32(0.2)), hi=float(np.float32(0.2)))
+    for _ in range(2):  # the first token's ratio is 1, its slope -weight on either side
+        adv[0] = np.float32(adv[0] + P.objective(logp, old, adv, weights=w, **how)[0][1] / w[0])
+    ref = P.objective(logp, old, adv, weights=w, **how)[0][1]
+    size = (w * np.abs(adv.astype(np.float64)) * np.maximum(np.exp(logp - old), 0.8)).sum()
+    assert abs(ref) < 1e-4 * size
+    sums, got, h, _ = tt.policy_loss_logits(z, y, _dev(old), _dev(adv), weights=_dev(w), clip=0.2)
+    assert abs(float(sums[1]) - ref) <= 2.0 ** -24 * abs(ref) + 2.0 ** -32 * size
+    assert float(sums[0]) == float(sums[1])
+    assert (np.abs(_f64(got) - logp) <= 2.0 ** -23 * np.abs(logp)).all() and (np.abs(_f64(h) + logp) <= 2.0 ** -22 * np.abs(logp)).all()

@@ -249,6 +249,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _room_of(t, name):
+    """Bytes of a buffer that a call writes from its first one on (0 for None): one without gaps, which would hold others' data."""
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def _device_of(t, *others):
     """Ordinal of t's device; the other tensors must be on it."""
     index = t.get_device()
@@ -476,7 +485,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, q_weight=None, k_weight=No
           dq_out.data_ptr(), dqo_ld, q.data_ptr(), q_ld, dq.data_ptr(), dq_ld, _ptr(dk_out), dko_ld, _ptr(k), k_ld,
           _ptr(dk), dk_ld, _DTYPES[q.dtype], N, hq, hkv, d, _ptr(q_weight), _ptr(k_weight), w_dtype, eps, rot,
           _ptr(positions), pos_ld, axes, axis, freq, 1 if adjacent else 0, _ptr(dwq), _ptr(dwk), _ptr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+          _room_of(ws, "ws"))
     return dq, dk, dwq, dwk
 
 
@@ -615,7 +624,7 @@ def tree_decode_plan(segments, B, rows, pairs, hq, hkv, d, err=None, out=None):
     err = new_err(segments.device) if err is None else err
     at, step = segments.data_ptr(), 4 * S
     _call("tt_tree_decode_plan", _device_of(segments, plan, err), at, at + step, at + 2 * step, at + 3 * step, S, B, rows,
-          pairs, hq, hkv, d, plan.data_ptr(), plan.numel() * plan.element_size(), err.data_ptr())
+          pairs, hq, hkv, d, plan.data_ptr(), _room_of(plan, "out"), err.data_ptr())
     return DecodePlan(plan, S, B, rows, pairs, hq, hkv, d, L.tt_tree_decode_attn_workspace_bytes(pairs, hq, d), err)
 
 
@@ -644,7 +653,7 @@ def tree_decode_attn(plan: DecodePlan, q, k, v, scale=None, out=None, ws=None, e
     err = plan.err if err is None else err
     _call("tt_tree_decode_attn", _device_of(q, k, v, plan.plan, O, LSE, ws, err), plan.plan.data_ptr(), q.data_ptr(), q_ld,
           k.data_ptr(), v.data_ptr(), k_ld, _DTYPES[q.dtype], plan.S, B, rows, plan.pairs, hq, hkv, d, scale, O.data_ptr(),
-          LSE.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr())
+          LSE.data_ptr(), ws.data_ptr(), _room_of(ws, "ws"), err.data_ptr())
     return O, LSE
 
 
@@ -999,8 +1008,7 @@ def policy_loss(logp, old_logp, adv, adv_neg=None, ref_logp=None, entropy=None, 
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _call("tt_policy_loss", _device_of(logp, old_logp, adv, adv_neg, ref_logp, entropy, weights, sums, dlogp, dent, ws),
           logp.data_ptr(), _ptr(entropy), old_logp.data_ptr(), adv.data_ptr(), _ptr(adv_neg), _ptr(ref_logp),
-          _ptr(weights), N, policy, sums.data_ptr(), _ptr(dlogp), _ptr(dent), _ptr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+          _ptr(weights), N, policy, sums.data_ptr(), _ptr(dlogp), _ptr(dent), _ptr(ws), _room_of(ws, "ws"))
     return sums, dlogp, dent
 
 
@@ -1040,7 +1048,7 @@ def policy_loss_logits(logits, targets, old_logp, adv, adv_neg=None, ref_logp=No
           _device_of(logits, targets, old_logp, adv, adv_neg, ref_logp, weights, sums, logp, entropy, dl, ws, err),
           logits.data_ptr(), _DTYPES[logits.dtype], N, V, ld, targets.data_ptr(), old_logp.data_ptr(), adv.data_ptr(),
           _ptr(adv_neg), _ptr(ref_logp), _ptr(weights), policy, sums.data_ptr(), logp.data_ptr(), entropy.data_ptr(),
-          _ptr(dl), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr())
+          _ptr(dl), ws.data_ptr(), _room_of(ws, "ws"), err.data_ptr())
     return sums, logp, entropy, dl
 
 

@@ -2,8 +2,11 @@
 import dataclasses
 import math
 
+import numpy as np
 import pytest
 import torch
+
+from tests.test_gpu_decode import _check, _rand, _run, _tree
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +71,35 @@ def test_many_far_keys_beside_a_near_one(tt, dtype, d, B, n, hq, hkv, far):
         tol += n * 2.0 ** -32 * 1.01 * v.double().abs().max() + 2.0 ** -24
     off = (o.double() - O).abs()
     assert (off <= tol).all(), (off.max(), (off / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq,hkv,d,page", [(8, 2, 64, 16), (6, 1, 128, 64), (20, 1, 64, 64), (4, 4, 128, 1)])
+def test_pages_in_any_order(tt, dtype, hq, hkv, d, page):
+    """A prompt and the rollouts' own rows in pages anywhere in the pool, the last of each partly filled (what lies behind its
+    keys was never written): many hundreds of segments, so that the parts of a query are joined in several goes."""
+    rng = np.random.default_rng(page)
+    whole, B, _ = _tree(rng, [(1, 700, 700), (3, 50, 200), (6, 0, 300)])
+    if page == 1:
+        whole = [(s, min(n, 60), a, b) for s, n, a, b in whole]
+    pages = [(min(page, n - i), a, b) for _, n, a, b in whole for i in range(0, n, page)]
+    rows = len(pages) * page
+    at = rng.permutation(len(pages)) * page
+    segs = [(int(x), n, a, b) for x, (n, a, b) in zip(at, pages)]
+    segs = [segs[i] for i in rng.permutation(len(segs))]
+    q, k, v = _rand(rng, (B, hq, d), dtype, 1.5), _rand(rng, (rows, hkv, d), dtype), _rand(rng, (rows, hkv, d), dtype)
+    held = np.zeros(rows, bool)
+    for s, n, _, _ in segs:
+        held[s:s + n] = True
+    for t in (k, v):
+        t[torch.from_numpy(~held).cuda()] = math.nan
+    got = _run(tt, q, k, v, segs)
+    _check(got, q, torch.nan_to_num(k), torch.nan_to_num(v), segs)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(1024, 1, 64), (1024, 1024, 64), (1024, 8, 128), (1020, 60, 128)])
+def test_most_heads(tt, hq, hkv, d):
+    rng = np.random.default_rng(hkv)
+    segs, B, rows = _tree(rng, [(1, 150, 150), (3, 0, 140)])
+    q, k, v = _rand(rng, (B, hq, d), torch.bfloat16), *(_rand(rng, (rows, hkv, d), torch.bfloat16) for _ in range(2))
+    _check(_run(tt, q, k, v, segs), q, k, v, segs)

@@ -97,3 +97,14 @@ def test_terms_of_both_signs_cancel_and_their_roundings_do_not(tt, N, V, seed):
     assert abs(float(sums[1]) - ref) <= 2.0 ** -24 * abs(ref) + 2.0 ** -32 * size
     assert float(sums[0]) == float(sums[1])
     assert (np.abs(_f64(got) - logp) <= 2.0 ** -23 * np.abs(logp)).all() and (np.abs(_f64(h) + logp) <= 2.0 ** -22 * np.abs(logp)).all()
+
+
+@pytest.mark.parametrize("dtype,V,ld", [("bf16", 900_000, 900_003), ("fp16", 899_999, 899_999), ("fp32", 450_000, 450_001)])
+def test_widest_rows(tt, dtype, V, ld):
+    rng = np.random.default_rng(V)
+    z = _logits(rng, 5, V, ld, DT[dtype], 0.1)
+    ids = np.flatnonzero(np.isfinite(_f64(z[0])))
+    y = ids[rng.integers(0, len(ids), 5)]
+    s = _inputs(rng, TL.token_logprob(_f64(z), y)[0], True, True, True)
+    s["weights"][:3] = [1.0, 0.0, 0.5]
+    _check_logits(tt, rng, z, s, y)

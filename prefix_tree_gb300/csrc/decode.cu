@@ -17,13 +17,22 @@
 // parts of different tiles and CTAs cannot meet: along the runs one of the two
 // grows at every step, by at least the rows that the part before takes.
 //
-// Bound by memory where most keys are the rollouts' own: 480 of them with 384
-// keys each (1.07 GB) take 157 us, 6.85 TB/s. Where a long prompt has many rows
-// its products and exponentials bound it: a wide block whose keys lie in the
-// L2 cache takes 1.35 us, a narrow one 0.9. A group of 64 rollouts of 8192
-// shared and about 1150 own keys, 8 key heads of 128: 54 + 6 us for 325 MB; a
-// deep tree of 16,001 shared keys, six common turns and 120 rollouts of 1500:
-// 143 to 153 + 9 us for 842 MB.
+// Bound by memory where most keys are the rollouts' own (32 heads to 8 key
+// heads of 128, bf16; this kernel + the joining one): 500 rollouts of 2048 keys
+// 630 + 15 us for 4.19 GB (6.7 TB/s in the first), 480 of 384 keys 126 + 14 us
+// for 755 MB (6.0). With heads of 64 a block has half the bytes and the same
+// waits, and the same rollouts take 470 and 97 us (4.5 and 3.9 TB/s). Where a
+// long prompt has many rows its products and exponentials bound it: a wide
+// block whose keys lie in the L2 cache takes 1.35 us, a narrow one 0.9. A group
+// of 64 rollouts of 8192 shared and about 1150 own keys: 57 to 62 + 6 us for 325
+// MB; a deep tree of 16,001 shared keys, six common turns and 120 rollouts of
+// 1500, 40 heads to 8: 150 to 163 + 9 us for 842 MB.
+//
+// A segment is a tile of its own, with a start, a part and at least one block,
+// and the join looks at every segment for each query and eight heads. Small
+// pages are therefore dear: 64 rollouts of 8192 shared and 1024 own keys 59 + 6
+// us (302 MB), the same in pages of 256 rows 83 + 31, of 64 rows 276 + 126, of 16
+// rows 1073 + 473; the plan, one CTA, 61 us for 16,000 segments.
 #include "tc_common.cuh"
 
 #include <cuda_fp16.h>
@@ -45,11 +54,14 @@ constexpr int kMostCtas = 1024;
 constexpr int kMostSegs = (1 << 24) - 1;
 constexpr int kPiece = 32;       // rows of a copy
 // Work is shared out by cost: of a block, and of a tile's start (its queries have to be fetched first and its sums
-// written last). A narrow block at 2.5 or 3.5 in place of 3: the group of 64 rollouts 5 and 13 % slower, the deep tree 1 % and
-// 18 %.
+// written last). Measured on a group of 64 rollouts, a deep tree and 40 groups of six, bf16 and fp16. A narrow block at 2.5 or
+// 3.5 in place of 3: with heads of 64 2 to 5 % slower either way, with heads of 128 up to 5 % slower at 2.5, between 4 % slower
+// and 5 % faster at 3.5; at 4: up to 13 % slower. Starts of 12 and 2, or 16 and 8, in place of 12 and 4: the groups of six 23 %
+// slower, or 14 % (heads of 64), the others within 3 %.
 constexpr int kBlockWide = 4, kBlockNarrow = 3, kStartWide = 12, kStartNarrow = 4;
 // A segment with more rows than this is taken by tiles of 128 rows on the tensor cores' asynchronous path, one with
-// fewer by tiles of 16 on the warps' own: 24 rows to a segment take 18.8 us by one wide tile and 23.3 by two narrow ones.
+// fewer by tiles of 16 on the warps' own: 40 segments of 3000 keys with 24 rows take 110 us by one wide tile and 186 by two
+// narrow ones (with their rollouts' own keys; heads of 64: 85 and 130).
 constexpr int kWideFrom = 16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 

@@ -17,10 +17,13 @@
 // shared memory, takes (max, Σe^d, Σd·e^d) there, joins them over the CTAs
 // of the row's cluster, and forms dz from the same shared memory: one read of
 // the logits and one write of the gradient, bound by memory: 12,669 rows of
-// 151,936 bf16 (a sixth masked) 1179 us, 6.0 TB/s and 0.88 of a plain
+// 151,936 bf16 (a sixth masked) 1184 us, 6.0 TB/s and 0.88 of a plain
 // copy's rate: a CTA's reads, joins and writes follow one another, and only the
-// other CTAs of the SM fill the gaps. 1537 fp32 rows of 32,003 71 us. Streaming
-// stores and loads that the L2 cache drops first were slower (by 0.5, 2.5 %).
+// other CTAs of the SM fill the gaps. 1537 fp32 rows of 32,003 70 us, for the
+// same reason (three CTAs to an SM; issue slots busy in 0.39 of the cycles). A
+// masked row's first batches are read too: they are on their way before its
+// weight is known. Streaming stores and loads that the L2 cache drops first were
+// slower (by 0.5, 2.5 %).
 //
 // Where the numbers need it: logp − old is formed from (z_y − m), log S and
 // old by exact two-sums, with log S as a pair, since rounding logp (about 12)
@@ -701,8 +704,8 @@ int launch_rows(const LogitsArgs& a, int log_CL, cudaStream_t st) {
 // How rows are taken: by a warp or two each while they are short and many, by a CTA of eight warps, or by 2, 4 or 8 CTAs. A
 // slice of up to 80 KB leaves two CTAs and more to an SM, one's copies under way during another's joins. Few rows are cut
 // further while every slice finds an SM of its own. Measured, us for the choice and the next one (bf16):
-//   20,000 x 1000: warp 29, two warps 41;        20,000 x 8000: two warps 108, four 156;
-//   20,000 x 16,000: one CTA 201, two 245;       12,669 x 151,936 (16 % masked): 4 CTAs 1180, 8 CTAs 1320, 1 persistent CTA
+//   20,000 x 1000: warp 30, two warps 43;        20,000 x 8000: two warps 112, eight 142;
+//   20,000 x 16,000: one CTA 206, two 376;       12,669 x 151,936 (16 % masked): 4 CTAs 1184, 8 CTAs 1320, 1 persistent CTA
 //   to an SM with part of the row read again 1440, persistent clusters that copy the next row ahead 1590.
 constexpr int64_t kSliceVectors = 5120;
 template <typename T>

@@ -61,7 +61,7 @@ constexpr int kPiece = 32;       // rows of a copy
 constexpr int kBlockWide = 4, kBlockNarrow = 3, kStartWide = 12, kStartNarrow = 4;
 // A segment with more rows than this is taken by tiles of 128 rows on the tensor cores' asynchronous path, one with
 // fewer by tiles of 16 on the warps' own: 40 segments of 3000 keys with 24 rows take 110 us by one wide tile and 186 by two
-// narrow ones (with their rollouts' own keys; heads of 64: 85 and 130).
+// narrow ones (with their rollouts' own keys; heads of 64: 90 and 130).
 constexpr int kWideFrom = 16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -300,7 +300,8 @@ constexpr uint32_t kTmemCols = 512, kGroupCols = 256, kColO = 128;
 // double it. The sum of weights is that of the unrounded ones.
 // A row's weights are 2^(score − reference), the reference kLift below a maximum that moves only when the scores grow by more
 // than kRescale above it (log2 units): they stay below 2^(kRescale + kLift). fp16 has room for 2^15 and ends at 2^-24, so that
-// lifted by 2^7 the weights of far keys are rounded to multiples of 2^-31 of the largest (the sum counts them in any case).
+// lifted by 2^7 the weights of far keys are rounded to multiples of 2^-31 of the largest (the sum counts them in any case). The
+// bound is put to the difference, which is exact: reference and bound added would round to more from scores of 2^26 on.
 constexpr float kRescale = 8.0f;
 template <typename T>
 constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
@@ -588,10 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mx[e & 3] = fmax3f(mx[e & 3], __uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1]));
               }
             }
-            const float top = fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * size;
+            const float top = __fmul_rn(fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3])), size);  // (rounded here, not in an fma)
             bool moved = false;
             float f = 1.f;
-            if (top > m + (kRescale + kLift<T>)) {
+            if (top - m > kRescale + kLift<T>) {
               f = fast_exp2(m - (top - kLift<T>));  // 0 at the group's first keys
               l *= f;
               moved = t >= 2;
@@ -611,7 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float mu = m == -INFINITY ? 0.f : m;
-            const float2 nm = make_float2(-mu, -mu), by = make_float2(size, size);
+            // The maximum is a rounded product, the differences below are not: from scores of 2^24 on they part by more than
+            // half a unit, which soon leaves fp16's range (2^28) and then fp32's (2^31). There the scores are scaled, and
+            // rounded, by themselves.
+            const bool far = __any_sync(~0u, !(fabsf(mu) < 16777216.f));
+            const float2 nm = make_float2(-mu, -mu), by = make_float2(far ? 1.f : size, far ? 1.f : size);
             float2 rs = make_float2(0.f, 0.f);
             // the weights of 32 scores take half of the columns of those: never ones that are still to be read
             auto weigh = [&](int q, const uint32_t (&y)[32]) {
@@ -635,6 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int q = 0; q < 2; ++q) {
                 tmem_pin(x[q]);
                 scores(2 * half + q, x[q]);
+                if (far) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) x[q][e] = __float_as_uint(__fmul_rn(__uint_as_float(x[q][e]), size));
+                }
                 weigh(2 * half + q, x[q]);
               }
             }
@@ -738,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[t][e] = (s[t][e] + s2[t][e]) * a.scale_log2;
+              for (int e = 0; e < 4; ++e) s[t][e] = __fmul_rn(s[t][e] + s2[t][e], a.scale_log2);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[K_EMPTY + kst]);
@@ -759,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float x = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-              if (x > m[half] + (kRescale + kLift<T>)) {
+              if (x - m[half] > kRescale + kLift<T>) {
                 f[half] = fast_exp2(m[half] - (x - kLift<T>));  // 0 at the first keys
                 l[half] *= f[half];
                 m[half] = x - kLift<T>;

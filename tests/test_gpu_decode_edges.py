@@ -103,3 +103,23 @@ def test_most_heads(tt, hq, hkv, d):
     segs, B, rows = _tree(rng, [(1, 150, 150), (3, 0, 140)])
     q, k, v = _rand(rng, (B, hq, d), torch.bfloat16), *(_rand(rng, (rows, hkv, d), torch.bfloat16) for _ in range(2))
     _check(_run(tt, q, k, v, segs), q, k, v, segs)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq", [4, 40])  # narrow and wide tiles
+@pytest.mark.parametrize("scale", [0.125, 0.1, -0.0625, 0.03, 0.005, 1.0, 3.0, 300.0, -1e5, 1e20])
+def test_scores_whose_steps_are_whole_powers_of_two(tt, dtype, hq, scale):
+    """Scores of 2^30·scale, some of fp32's steps apart and growing along the keys: weights stay within their type, and O a mean of
+    the values (of which all are 1: a weight is off by half a step of its type)."""
+    g = torch.Generator(device="cuda").manual_seed(int(1000 * abs(scale)) % 2 ** 31)
+    n, d, B = 3000, 64, 6
+    q, k = torch.zeros(B, hq, d, device="cuda"), torch.zeros(n * B, 1, d, device="cuda")
+    q[..., 0], q[..., 1] = 32768.0, 128.0
+    k[..., 0] = 32768.0
+    steps = torch.randint(0, 2, (B, n), device="cuda", generator=g).cumsum(1) % torch.tensor([[3], [7], [20], [128], [200], [256]]).cuda()
+    k[..., 1] = steps.reshape(-1, 1) * (1.0 if scale > 0 else -1.0)
+    v = torch.ones(n * B, 1, d, device="cuda", dtype=dtype)
+    table = torch.tensor([[i * n, n, i, i + 1] for i in range(B)], dtype=torch.int32).T.contiguous().cuda()
+    plan = tt.tree_decode_plan(table, B, n * B, B, hq, 1, d)
+    o, lse = tt.tree_decode_attn(plan, q.to(dtype), k.to(dtype), v, scale=scale)
+    assert ((o.double() - 1).abs() <= 2 * torch.finfo(dtype).eps / 2 + 1e-4).all() and torch.isfinite(lse).all()
